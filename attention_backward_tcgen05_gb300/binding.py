@@ -10,9 +10,16 @@ Tensor shapes (torch, C order; the reverse of ggml's ne order):
     q (B, H, N, DK)  k (B, Hkv, M, DK)  v (B, Hkv, M, DV)
     d, o (B, N, H, DV)  lse (B, H, N) float32  mask (N, M) float16 or None
     packed: float32 of fab_packed_bytes(dims) / 4 elements
+    projection rows, read by qk_norm_rope: q (B, N, H, DK)  k (B, N, Hkv, DK)  v (B, N, Hkv, DV),
+        heads contiguous, any distance between tokens (views of one fused projection, for example)
+    wq, wk (DK,) in q's dtype or None  cos, sin (P, rot / 2) float32  pos (B, N) int32 or None
+    paged: projection rows q (T, H, DK)  k (T, Hkv, DK)  v (T, Hkv, DV)
+        k_cache (pages, Hkv, page, DK)  v_cache (pages, Hkv, page, DV)
+        starts (B + 1,)  lens (B,)  table (B, max_pages), int32;  o (T, H, DV)  lse (H, T) float32
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -29,7 +36,9 @@ EXPORTS = ("fab_version", "fab_status_string", "fab_packed_offsets", "fab_packed
            "fab_backward_workspace_bytes", "fab_backward_recompute_workspace_bytes", "fab_forward_lse",
            "fab_backward", "fab_backward_preprocess",
            "fab_backward_main", "fab_backward_query_pass", "fab_backward_key_pass", "fab_backward_noalloc",
-           "fab_last_device_error")
+           "fab_last_device_error", "fab_qk_norm_rope", "fab_qk_norm_rope_backward",
+           "fab_qk_norm_rope_backward_workspace_bytes", "fab_paged_append", "fab_paged_attention",
+           "fab_paged_attention_workspace_bytes")
 NOALLOC_MAX_ROWS = 1048576  # FAB_NOALLOC_MAX_ROWS
 
 
@@ -38,6 +47,16 @@ class fab_dims(ctypes.Structure):
 
     def tuple(self):
         return tuple(getattr(self, n) for n in ("B", "H", "Hkv", "N", "M", "DK", "DV"))
+
+
+class fab_rope_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "N", "H", "Hkv", "DK", "DV", "rot", "P", "ldq", "ldk", "ldv",
+                                              "ldgq", "ldgk", "ldgv")]
+
+
+class fab_paged_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "H", "Hkv", "DK", "DV", "page", "pages", "max_pages", "rot",
+                                              "P", "ldq", "ldk", "ldv")]
 
 
 class FabError(RuntimeError):
@@ -61,6 +80,7 @@ def lib():
                 L = ctypes.CDLL(LIB_PATH)
                 vp, sz, i32, f32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
                 dp = ctypes.POINTER(fab_dims)
+                rp, pp = ctypes.POINTER(fab_rope_dims), ctypes.POINTER(fab_paged_dims)
                 szp = ctypes.POINTER(ctypes.c_size_t)
                 sig = {
                     "fab_version": ([], i32),
@@ -77,6 +97,12 @@ def lib():
                     "fab_backward_key_pass": ([vp, vp, vp, vp, vp, vp, i32, f32, i32, dp, vp, sz, vp, vp], i32),
                     "fab_backward_noalloc": ([vp, vp, vp, vp, vp, vp, vp, i32, f32, i32, dp, vp, vp], i32),
                     "fab_last_device_error": ([vp], i32),
+                    "fab_qk_norm_rope": ([vp] * 8 + [f32, i32, i32, rp, vp, vp, vp, vp], i32),
+                    "fab_qk_norm_rope_backward_workspace_bytes": ([rp], sz),
+                    "fab_qk_norm_rope_backward": ([vp] * 10 + [f32, i32, i32, rp, vp, sz] + [vp] * 6, i32),
+                    "fab_paged_append": ([vp] * 7 + [f32, i32, vp, vp, vp, i32, pp, vp, vp, vp, vp], i32),
+                    "fab_paged_attention_workspace_bytes": ([pp, i32], sz),
+                    "fab_paged_attention": ([vp] * 6 + [i32, f32, i32, pp, vp, sz, vp, vp, vp], i32),
                 }
                 for name, (args, res) in sig.items():
                     f = getattr(L, name)
@@ -260,7 +286,267 @@ def fab_last_device_error(stream=None) -> int:
     return lib().fab_last_device_error(_stream(stream))
 
 
+# ------------------------------------------------------------------ norms + rotation, paged cache
+
+
+def _here(*tensors):
+    """All the given tensors (None: skipped) are on the current device, which
+    is where libfab launches; returns that device's index."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    return dev
+
+
+def _ptr(t, name, dtype, shape):
+    """Address of a contiguous tensor of that dtype and shape (None: 0)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, {dtype}, of shape {tuple(shape)}; "
+                         f"got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _ld(t, name, dtype, shape):
+    """Elements between the rows of consecutive tokens of t, of shape
+    (..., tokens, heads, width): heads contiguous inside a row, rows evenly
+    spaced over all tokens."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    st = t.stride()
+    heads, width = shape[-2], shape[-1]
+    if (st[-1] != 1 and width > 1) or (st[-2] != width and heads > 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous, got strides {st}")
+    n = shape[-3]
+    if len(shape) == 4 and shape[0] > 1:
+        if n == 1:
+            return st[0]
+        if st[0] != n * st[1]:
+            raise ValueError(f"{name}: the rows of all tokens must be evenly spaced, got strides {st}")
+    return st[-3] if n > 1 else heads * width
+
+
+def _check_tables(cos, sin, wq, wk, DK, dtype):
+    """(rot, P) of the tables (None, None: no rotation)."""
+    rot, P = 0, 0
+    if cos is not None:
+        P, half = cos.shape
+        rot = 2 * half
+        _ptr(cos, "cos", torch.float32, cos.shape)
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    _ptr(sin, "sin", torch.float32, cos.shape if cos is not None else None)
+    _ptr(wq, "wq", dtype, (DK,))
+    _ptr(wk, "wk", dtype, (DK,))
+    return rot, P
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def fab_qk_norm_rope(q, k, v, wq, wk, cos, sin, pos, eps, interleaved, q_out, k_out, v_out, stream=None):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k must be 4-D: (B,N,H,DK), (B,N,Hkv,DK)")
+    B, N, H, DK = q.shape
+    Hkv, DV = k.shape[2], DK if v is None else v.shape[-1]
+    dt = q.dtype
+    _here(q, k, v, wq, wk, cos, sin, pos, q_out, k_out, v_out)
+    rot, P = _check_tables(cos, sin, wq, wk, DK, dt)
+    dims = fab_rope_dims(B, N, H, Hkv, DK, DV, rot, P, _ld(q, "q", dt, (B, N, H, DK)),
+                         _ld(k, "k", dt, (B, N, Hkv, DK)), 0 if v is None else _ld(v, "v", dt, (B, N, Hkv, DV)))
+    _check(lib().fab_qk_norm_rope(
+        q.data_ptr(), k.data_ptr(), _addr(v), _addr(wq), _addr(wk), _addr(cos), _addr(sin),
+        _ptr(pos, "pos", torch.int32, (B, N)), float(eps), int(bool(interleaved)), dtype_code(q), ctypes.byref(dims),
+        _ptr(q_out, "q_out", dt, (B, H, N, DK)), _ptr(k_out, "k_out", dt, (B, Hkv, N, DK)),
+        _ptr(v_out, "v_out", dt, (B, Hkv, N, DV)), _stream(stream)), "fab_qk_norm_rope")
+
+
+def fab_qk_norm_rope_backward_workspace_bytes(dims: fab_rope_dims) -> int:
+    return lib().fab_qk_norm_rope_backward_workspace_bytes(ctypes.byref(dims))
+
+
+def _rope_backward_dims(dq, dk, dv, q, k, wq, wk, rot, P, gq, gk, gv):
+    B, H, N, DK = dq.shape
+    Hkv, DV = dk.shape[1], DK if dv is None else dv.shape[-1]
+    dt = gq.dtype
+    qs, ks = (B, N, H, DK), (B, N, Hkv, DK)
+    return fab_rope_dims(B, N, H, Hkv, DK, DV, rot, P, 0 if wq is None else _ld(q, "q", dt, qs),
+                         0 if wk is None else _ld(k, "k", dt, ks), 0, _ld(gq, "gq", dt, qs), _ld(gk, "gk", dt, ks),
+                         0 if gv is None else _ld(gv, "gv", dt, (B, N, Hkv, DV)))
+
+
+def fab_qk_norm_rope_backward(dq, dk, dv, q, k, wq, wk, cos, sin, pos, eps, interleaved, workspace, gq, gk, gv, gwq,
+                              gwk, stream=None):
+    """q and k are read only where wq and wk are given (None otherwise is fine)."""
+    if dq.dim() != 4 or dk.dim() != 4:
+        raise ValueError("dq, dk must be 4-D: (B,H,N,DK), (B,Hkv,N,DK)")
+    B, H, N, DK = dq.shape
+    _here(dq, dk, dv, q, k, wq, wk, cos, sin, pos, workspace, gq, gk, gv, gwq, gwk)
+    rot, P = _check_tables(cos, sin, wq, wk, DK, gq.dtype)
+    dims = _rope_backward_dims(dq, dk, dv, q, k, wq, wk, rot, P, gq, gk, gv)
+    f32 = torch.float32
+    _check(lib().fab_qk_norm_rope_backward(
+        _ptr(dq, "dq", f32, dq.shape), _ptr(dk, "dk", f32, (B, dims.Hkv, N, DK)),
+        _ptr(dv, "dv", f32, (B, dims.Hkv, N, dims.DV)), None if wq is None else q.data_ptr(),
+        None if wk is None else k.data_ptr(), _addr(wq), _addr(wk), _addr(cos), _addr(sin),
+        _ptr(pos, "pos", torch.int32, (B, N)), float(eps), int(bool(interleaved)), dtype_code(gq),
+        ctypes.byref(dims), _addr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), gq.data_ptr(), gk.data_ptr(),
+        _addr(gv), _ptr(gwq, "gwq", f32, (DK,)), _ptr(gwk, "gwk", f32, (DK,)), _stream(stream)),
+        "fab_qk_norm_rope_backward")
+
+
+def _paged_dims(H, T, k_cache, v_cache, starts, lens, table):
+    """dims of a paged call, its cache and its int32 arrays checked."""
+    if k_cache.dim() != 4 or v_cache.dim() != 4 or table.dim() != 2:
+        raise ValueError("k_cache, v_cache must be 4-D (pages,Hkv,page,width), table 2-D (B,max_pages)")
+    pages, Hkv, page, DK = k_cache.shape
+    DV = v_cache.shape[3]
+    B, max_pages = table.shape
+    _ptr(k_cache, "k_cache", k_cache.dtype, k_cache.shape)
+    _ptr(v_cache, "v_cache", k_cache.dtype, (pages, Hkv, page, DV))
+    i32 = torch.int32
+    _ptr(starts, "starts", i32, (B + 1,))
+    _ptr(lens, "lens", i32, (B,))
+    _ptr(table, "table", i32, (B, max_pages))
+    return fab_paged_dims(B, T, H, Hkv, DK, DV, page, pages, max_pages)
+
+
+def fab_paged_append(q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, q_out, k_cache, v_cache,
+                     stream=None):
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k, v must be 3-D: (T,H,DK), (T,Hkv,DK), (T,Hkv,DV)")
+    T, H, DK = q.shape
+    dt = q.dtype
+    _here(q, k, v, wq, wk, cos, sin, starts, lens, table, q_out, k_cache, v_cache)
+    dims = _paged_dims(H, T, k_cache, v_cache, starts, lens, table)
+    if k_cache.dtype != dt:
+        raise ValueError(f"k_cache must be {dt}, got {k_cache.dtype}")
+    dims.rot, dims.P = _check_tables(cos, sin, wq, wk, DK, dt)
+    dims.ldq = _ld(q, "q", dt, (T, H, dims.DK))
+    dims.ldk = _ld(k, "k", dt, (T, dims.Hkv, DK))
+    dims.ldv = _ld(v, "v", dt, (T, dims.Hkv, dims.DV))
+    _check(lib().fab_paged_append(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(wq), _addr(wk), _addr(cos), _addr(sin), float(eps),
+        int(bool(interleaved)), starts.data_ptr(), lens.data_ptr(), table.data_ptr(), dtype_code(q),
+        ctypes.byref(dims), _ptr(q_out, "q_out", dt, (T, H, DK)), k_cache.data_ptr(), v_cache.data_ptr(),
+        _stream(stream)), "fab_paged_append")
+
+
+def fab_paged_attention_workspace_bytes(dims: fab_paged_dims, dtype: int) -> int:
+    return lib().fab_paged_attention_workspace_bytes(ctypes.byref(dims), int(dtype))
+
+
+def fab_paged_attention(q, k_cache, v_cache, starts, lens, table, causal, scale, workspace, o, lse, stream=None):
+    """lse may be None."""
+    if q.dim() != 3:
+        raise ValueError("q must be 3-D: (T,H,DK)")
+    T, H, DK = q.shape
+    dt = q.dtype
+    _here(q, k_cache, v_cache, starts, lens, table, workspace, o, lse)
+    dims = _paged_dims(H, T, k_cache, v_cache, starts, lens, table)
+    if k_cache.dtype != dt:
+        raise ValueError(f"k_cache must be {dt}, got {k_cache.dtype}")
+    _check(lib().fab_paged_attention(
+        _ptr(q, "q", dt, (T, H, dims.DK)), k_cache.data_ptr(), v_cache.data_ptr(), starts.data_ptr(),
+        lens.data_ptr(), table.data_ptr(), int(bool(causal)), float(scale), dtype_code(q), ctypes.byref(dims),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(o, "o", dt, (T, H, dims.DV)),
+        _ptr(lse, "lse", torch.float32, (H, T)), _stream(stream)), "fab_paged_attention")
+
+
 # ------------------------------------------------------------------ conveniences (torch allocates, libfab computes)
+
+
+def _on(stream):
+    """A context whose allocations belong to `stream` (None: the current one),
+    so that torch does not hand their memory to other work too early."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def qk_norm_rope(q, k, v, wq=None, wk=None, cos=None, sin=None, pos=None, eps=1e-6, interleaved=False, stream=None):
+    """Projection rows q (B,N,H,DK), k (B,N,Hkv,DK), v (B,N,Hkv,DV) or None to
+    what forward() takes: q (B,H,N,DK), k (B,Hkv,N,DK) normalised per head
+    (where weights are given) and rotated (where tables are), v (B,Hkv,N,DV)."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k must be 4-D: (B,N,H,DK), (B,N,Hkv,DK)")
+    B, N, H, DK = q.shape
+    with _on(stream):
+        qo = q.new_empty((B, H, N, DK))
+        ko = q.new_empty((B, k.shape[2], N, DK))
+        vo = None if v is None else q.new_empty((B, v.shape[2], N, v.shape[3]))
+        fab_qk_norm_rope(q, k, v, wq, wk, cos, sin, pos, eps, interleaved, qo, ko, vo, stream)
+    return qo, ko, vo
+
+
+def qk_norm_rope_backward(dq, dk, dv, q, k, wq=None, wk=None, cos=None, sin=None, pos=None, eps=1e-6,
+                          interleaved=False, dtype=None, stream=None):
+    """The gradients of qk_norm_rope's q, k, v, wq, wk for those of its results
+    (unpack()'s float32 slices): (gq (B,N,H,DK), gk (B,N,Hkv,DK), gv (B,N,Hkv,DV)
+    or None, gwq, gwk float32 (DK,) or None).  gq, gk and gv are in `dtype`
+    (None: q's) and are views of one row of H*DK + Hkv*DK + Hkv*DV values a
+    token: gq._base is the gradient of a fused projection."""
+    if dq.dim() != 4 or dk.dim() != 4:
+        raise ValueError("dq, dk must be 4-D: (B,H,N,DK), (B,Hkv,N,DK)")
+    B, H, N, DK = dq.shape
+    Hkv = dk.shape[1]
+    dtype = q.dtype if dtype is None else dtype
+    nq, nk, nv = H * DK, Hkv * DK, 0 if dv is None else dv.shape[1] * dv.shape[3]
+    with _on(stream):
+        g = torch.empty((B, N, nq + nk + nv), dtype=dtype, device=dq.device)
+        gq = g.as_strided((B, N, H, DK), (N * g.shape[2], g.shape[2], DK, 1))
+        gk = g.as_strided((B, N, Hkv, DK), (N * g.shape[2], g.shape[2], DK, 1), nq)
+        gv = None
+        if dv is not None:
+            gv = g.as_strided((B, N, dv.shape[1], dv.shape[3]), (N * g.shape[2], g.shape[2], dv.shape[3], 1), nq + nk)
+        gwq = None if wq is None else torch.empty((DK,), dtype=torch.float32, device=dq.device)
+        gwk = None if wk is None else torch.empty((DK,), dtype=torch.float32, device=dq.device)
+        ws = None
+        if wq is not None or wk is not None:
+            wsb = fab_qk_norm_rope_backward_workspace_bytes(fab_rope_dims(B, N, H, Hkv, DK, DK))
+            ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dq.device)
+        fab_qk_norm_rope_backward(dq, dk, dv, q, k, wq, wk, cos, sin, pos, eps, interleaved, ws, gq, gk, gv, gwq, gwk,
+                                  stream)
+    return gq, gk, gv, gwq, gwk
+
+
+def paged_append(q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cache, eps=1e-6, interleaved=False,
+                 stream=None):
+    """Puts the new tokens' keys and values into the caches and returns their
+    queries (T,H,DK), normalised and rotated as qk_norm_rope does; rows of
+    padding tokens are left as allocated."""
+    with _on(stream):
+        qo = q.new_empty(q.shape)
+        fab_paged_append(q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, qo, k_cache, v_cache, stream)
+    return qo
+
+
+def alloc_paged(q, k_cache, v_cache, table):
+    """A workspace (uint8 tensor) for fab_paged_attention calls of these sizes."""
+    dims = fab_paged_dims(table.shape[0], q.shape[0], q.shape[1], k_cache.shape[1], k_cache.shape[3], v_cache.shape[3],
+                          k_cache.shape[2], k_cache.shape[0], table.shape[1])
+    wsb = fab_paged_attention_workspace_bytes(dims, dtype_code(q))
+    return torch.empty(max(wsb, 16), dtype=torch.uint8, device=q.device)
+
+
+def paged_attention(q, k_cache, v_cache, starts, lens, table, causal=True, scale=None, stream=None):
+    """Returns (o (T,H,DV) in q's dtype, lse (H,T) float32); rows of padding
+    tokens are left as allocated."""
+    scale = q.shape[-1] ** -0.5 if scale is None else scale
+    with _on(stream):
+        o = q.new_empty((q.shape[0], q.shape[1], v_cache.shape[-1]))
+        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+        ws = alloc_paged(q, k_cache, v_cache, table)
+        fab_paged_attention(q, k_cache, v_cache, starts, lens, table, causal, scale, ws, o, lse, stream)
+    return o, lse
+
+
 
 
 def forward(q, k, v, mask=None, causal=False, scale=None, stream=None):

@@ -386,6 +386,15 @@ FAB_DEV uint4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
+// Sets kErrIndex in *err unless starts[0 .. B] ascends from 0 to at most T;
+// `count` threads share the work, this one is `rank`.
+FAB_DEV void check_starts(const int32_t* starts, int64_t B, int64_t T, int rank, int count, uint32_t* err) {
+  bool bad = false;
+  for (int64_t b = rank; b < B; b += count) bad |= starts[b] > starts[b + 1];
+  if (rank == 0) bad |= starts[0] != 0 || starts[B] > T;
+  if (bad) atomicOr(err, kErrIndex);
+}
+
 // The first live tile and one past the last of a live-tile map row of n
 // bytes (16-byte aligned; the padding after n is ignored): first = n and
 // end = 0 when none is live.

@@ -25,10 +25,11 @@ EncodeTiledFn encode_tiled_fn() {
   return fn;
 }
 
-namespace {
+bool dtype_ok(int dtype) { return dtype == FAB_F32 || dtype == FAB_BF16 || dtype == FAB_F16; }
 
-constexpr int64_t kMaxWidth = 256;  // DK, DV limit of every kernel
-constexpr int64_t kMaxElems = int64_t(1) << 40;
+int from_cuda(cudaError_t e) { return e == cudaSuccess ? FAB_OK : FAB_ERR_CUDA; }
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -118,11 +119,7 @@ Problem make_problem(const fab_dims* d, int dtype, float scale, int causal) {
   return p;
 }
 
-bool dtype_ok(int dtype) { return dtype == FAB_F32 || dtype == FAB_BF16 || dtype == FAB_F16; }
-
 bool widths_supported(const fab_dims* d) { return d->DK <= kMaxWidth && d->DV <= kMaxWidth; }
-
-int from_cuda(cudaError_t e) { return e == cudaSuccess ? FAB_OK : FAB_ERR_CUDA; }
 
 // Common checks of the backward entry points.  `need_*` select which pointers
 // the entry point reads.
@@ -389,7 +386,8 @@ FAB_API int fab_backward(const void* q, const void* k, const void* v, const void
 
 FAB_API int fab_last_device_error(fab_stream stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FAB_ERR_CUDA;
-  const uint32_t e = take_error_tc() | take_error_dq() | take_error_fwd();
+  const uint32_t e = take_error_tc() | take_error_dq() | take_error_fwd() | take_error_rope() | take_error_paged();
   if (e & kErrSmemAlign) return FAB_ERR_CUDA;
-  return (e & kErrTimeout) ? FAB_ERR_TIMEOUT : FAB_OK;
+  if (e & kErrTimeout) return FAB_ERR_TIMEOUT;
+  return (e & kErrIndex) ? FAB_ERR_INVALID : FAB_OK;
 }

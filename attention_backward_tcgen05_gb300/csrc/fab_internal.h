@@ -12,6 +12,7 @@ namespace fab {
 // Error bits a kernel may OR into its translation unit's device error word.
 constexpr uint32_t kErrTimeout = 1u;
 constexpr uint32_t kErrSmemAlign = 2u;  // dynamic shared memory not 1024-byte aligned
+constexpr uint32_t kErrIndex = 4u;      // a position, page or start read from device memory is out of range
 
 // One validated call, in the units the kernels use.
 struct Problem {
@@ -69,6 +70,55 @@ cudaError_t launch_backward_tc(const Problem& p, cudaStream_t s);
 // otherwise it reads D_i from p.di.
 cudaError_t launch_dq_tc(const Problem& p, bool fuse_d, cudaStream_t s);
 
+// One validated call of the norm + rotation entry points (fab_rope.cu).
+struct RopeProblem {
+  int64_t B, N, H, Hkv, DK, DV, rot, P;
+  int64_t ldq, ldk, ldv, ldgq, ldgk, ldgv;
+  float eps;
+  int interleaved;
+  int dtype;
+  const void *q, *k, *v;
+  const void *wq, *wk;  // null: no norm
+  const float *cos, *sin;
+  const int32_t* pos;  // [N,B] or null: token n is at position n
+  void *q_out, *k_out, *v_out;
+  // appending to a paged cache (starts non-null; then B = 1, N = T): k_out and
+  // v_out are the caches
+  const int32_t *starts, *lens, *table;
+  int64_t seqs, page, pages, max_pages;
+  // backward
+  const float *dq, *dk, *dv;
+  void *gq, *gk, *gv;
+  float *gwq, *gwk;
+  float* partial;  // workspace: rope_partial_rows rows of DK floats
+};
+// Rows of partial sums of a backward call (q's and k's together at most).
+constexpr int64_t kRopePartialRows = 1280;
+cudaError_t launch_rope(const RopeProblem& p, cudaStream_t s);
+cudaError_t launch_rope_backward(const RopeProblem& p, cudaStream_t s);
+
+// One validated fab_paged_attention call.
+struct PagedProblem {
+  int64_t B, T, H, Hkv, DK, DV, page, pages, max_pages;
+  float scale;
+  int causal;
+  int dtype;
+  const void *q, *k, *v;
+  const int32_t *starts, *lens, *table;
+  void* o;
+  float* lse;  // or null
+  void* workspace;
+};
+size_t paged_workspace_bytes(const PagedProblem& p);
+// fab_paged_simt.cu: CUDA cores, every dtype, DK, DV <= 256, any page.
+cudaError_t launch_paged_simt(const PagedProblem& p, cudaStream_t s);
+
+// fab_host.cu: the checks the entry points share.
+bool dtype_ok(int dtype);
+int from_cuda(cudaError_t e);
+constexpr int64_t kMaxWidth = 256;  // DK, DV limit of every kernel
+constexpr int64_t kMaxElems = int64_t(1) << 40;
+
 // fab_host.cu: cuTensorMapEncodeTiled from the driver, looked up once.
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -80,5 +130,7 @@ EncodeTiledFn encode_tiled_fn();
 uint32_t take_error_tc();
 uint32_t take_error_dq();
 uint32_t take_error_fwd();
+uint32_t take_error_rope();
+uint32_t take_error_paged();
 
 }  // namespace fab

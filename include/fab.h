@@ -67,7 +67,7 @@ extern "C" {
 
 typedef enum {
   FAB_OK = 0,
-  FAB_ERR_INVALID = 1,     /* null/misaligned pointer, bad dims, H % Hkv != 0 */
+  FAB_ERR_INVALID = 1,     /* null/misaligned pointer, bad dims, H % Hkv != 0; or see fab_last_device_error */
   FAB_ERR_UNSUPPORTED = 2, /* valid op, but no GPU kernel for these dims/dtype */
   FAB_ERR_WORKSPACE = 3,   /* workspace missing or smaller than required */
   FAB_ERR_CUDA = 4,        /* a CUDA runtime call or launch failed */
@@ -203,9 +203,122 @@ FAB_EXPORT int fab_backward_noalloc(const void* q, const void* k, const void* v,
                                     const float* lse, const uint16_t* mask, int causal, float scale, int dtype,
                                     const fab_dims* dims, float* packed_out, fab_stream stream);
 
+/* ---- Around the attention: query/key norms with the position rotation ----
+ *
+ * A projection leaves one row of H*DK queries, Hkv*DK keys and Hkv*DV values
+ * for each token, heads contiguous inside a row.  fab_qk_norm_rope turns those
+ * rows into fab_forward_lse's q, k and v; fab_qk_norm_rope_backward turns the
+ * slices of fab_backward's packed result into the gradient of the rows.
+ * With x a head's row, w its weights and r = 1 / sqrt(mean(x^2) + eps):
+ *   n = r x w (or n = x without weights),  y = R(pos) n,
+ * where R rotates pair i < rot / 2 by the angle whose cosine and sine are
+ * cos[i + rot/2*pos] and sin[i + rot/2*pos]: y_a = n_a cos - n_b sin,
+ * y_b = n_b cos + n_a sin, with (a, b) = (i, i + rot/2), or (2i, 2i + 1) when
+ * `interleaved` is nonzero.  Columns from rot on are not rotated.  Arithmetic
+ * is f32, rounded once to the output's type. */
+typedef struct {
+  int64_t B, N;          /* sequences, tokens in each */
+  int64_t H, Hkv;        /* query heads, key/value heads (H % Hkv == 0) */
+  int64_t DK, DV;        /* query/key width, value width (<= 256) */
+  int64_t rot;           /* rotated columns of q and k: even, 0 .. DK */
+  int64_t P;             /* positions held by cos and sin (read when rot > 0) */
+  int64_t ldq, ldk, ldv; /* elements from one token's row to the next in q, k, v:
+                            q[i, h, n, b] is at i + DK*h + ldq*(n + N*b) */
+  int64_t ldgq, ldgk, ldgv; /* the same for gq, gk, gv (backward only) */
+} fab_rope_dims;
+
+/* q, k, v: device, `dtype`, rows as above, aligned to their element only (v
+ * may be NULL with v_out NULL).  wq, wk: device, `dtype`, [DK], or NULL: that
+ * operand is not normalised.  cos, sin: device f32 [rot/2, P].  pos: device
+ * int32 [N,B], or NULL: token n is at position n (N <= P).  A position
+ * outside 0 .. P-1 is reported by fab_last_device_error as FAB_ERR_INVALID
+ * and its token's q_out and k_out are then meaningless.  q_out [DK,N,H,B],
+ * k_out [DK,N,Hkv,B], v_out [DV,N,Hkv,B]: `dtype`, as fab_forward_lse reads
+ * them; they must not overlap the inputs. */
+FAB_EXPORT int fab_qk_norm_rope(const void* q, const void* k, const void* v, const void* wq, const void* wk,
+                                const float* cos, const float* sin, const int32_t* pos, float eps, int interleaved,
+                                int dtype, const fab_rope_dims* dims, void* q_out, void* k_out, void* v_out,
+                                fab_stream stream);
+
+/* Device workspace bytes of fab_qk_norm_rope_backward (partial sums of the
+ * weights' gradients); 0 for bad dims. */
+FAB_EXPORT size_t fab_qk_norm_rope_backward_workspace_bytes(const fab_rope_dims* dims);
+
+/* With g = R(pos)^T dy and u = g w:  dw = sum over rows of g r x,
+ *   dx = r (u - r x mean(u r x))   (dx = g where there are no weights).
+ * dq, dk, dv: device f32, [DK,N,H,B], [DK,N,Hkv,B], [DV,N,Hkv,B] (dv NULL with
+ * gv NULL).  q, k: the forward's inputs; each is read only when its weights
+ * are given, and may be NULL otherwise.  gq, gk, gv: `dtype`, rows of ldgq,
+ * ldgk, ldgv elements, aligned to their element only; only the heads' columns
+ * are written.  gwq, gwk: device f32 [DK], overwritten (NULL exactly where the
+ * weights are).  Sums run in an order that depends on the sizes alone: two
+ * calls give the same bits. */
+FAB_EXPORT int fab_qk_norm_rope_backward(const float* dq, const float* dk, const float* dv, const void* q,
+                                         const void* k, const void* wq, const void* wk, const float* cos,
+                                         const float* sin, const int32_t* pos, float eps, int interleaved, int dtype,
+                                         const fab_rope_dims* dims, void* workspace, size_t workspace_bytes, void* gq,
+                                         void* gk, void* gv, float* gwq, float* gwk, fab_stream stream);
+
+/* ---- The same attention served from a paged key/value cache ----
+ *
+ * A cache is an array of pages, each holding `page` key (or value) rows of
+ * every key/value head: k_cache [DK, page, Hkv, pages], v_cache [DV, page, Hkv,
+ * pages].  Sequence b holds lens[b] tokens; token m of it lies in row m % page
+ * of page table[m / page + max_pages*b].  One call works on the T new tokens of
+ * B sequences laid end to end: sequence b owns tokens starts[b] ..
+ * starts[b+1]-1 (starts has B + 1 ascending entries, the first 0), and they are
+ * the last of its lens[b] tokens: lens counts them already, for both calls
+ * below.  A sequence may have no new token, and tokens from starts[B] on are
+ * padding: nothing is written for them.  starts, lens and table are device
+ * int32 and are read when the kernels run, so a captured call follows their
+ * contents.  A page number outside 0 .. pages-1, a token past max_pages*page
+ * or starts that do not ascend within 0 .. T touch no memory outside the
+ * arguments; fab_last_device_error reports FAB_ERR_INVALID, and what was
+ * computed for those tokens is meaningless. */
+typedef struct {
+  int64_t B, T;          /* sequences, rows of new tokens (T may be 0) */
+  int64_t H, Hkv;        /* query heads, key/value heads (H % Hkv == 0) */
+  int64_t DK, DV;        /* query/key width, value width (<= 256) */
+  int64_t page;          /* rows of a page */
+  int64_t pages;         /* pages of the cache */
+  int64_t max_pages;     /* entries of a sequence's row of the table */
+  int64_t rot, P;        /* as in fab_rope_dims (fab_paged_append only) */
+  int64_t ldq, ldk, ldv; /* as in fab_rope_dims, by token (fab_paged_append only) */
+} fab_paged_dims;
+
+/* Writes the new tokens' keys and values into the cache and their queries into
+ * q_out [DK,H,T], norms and rotation as in fab_qk_norm_rope, each token at
+ * its place in its sequence (token i of the n new ones is at position
+ * lens[b] - n + i, which must be in 0 .. P-1).  q, k, v: [DK,H] rows of ldq, ...
+ * elements by token, aligned to their element only.  No other row of the caches
+ * or of q_out is touched.  A row of the cache that two tokens of one call map
+ * to gets either of them. */
+FAB_EXPORT int fab_paged_append(const void* q, const void* k, const void* v, const void* wq, const void* wk,
+                                const float* cos, const float* sin, float eps, int interleaved, const int32_t* starts,
+                                const int32_t* lens, const int32_t* table, int dtype, const fab_paged_dims* dims,
+                                void* q_out, void* k_cache, void* v_cache, fab_stream stream);
+
+/* Device workspace bytes of fab_paged_attention; 0 for bad dims. */
+FAB_EXPORT size_t fab_paged_attention_workspace_bytes(const fab_paged_dims* dims, int dtype);
+
+/* Attention of the new tokens over their sequences' caches: token i of the n
+ * new ones of sequence b sees keys m < lens[b], and with `causal` only
+ * m <= lens[b] - n + i (the last token sees all: aligned at the end, unlike
+ * fab_forward_lse's top-left rule).  q [DK,H,T], o [DV,H,T]: `dtype`; lse f32
+ * [T,H] (natural log), or NULL.  A token that sees no key gets o = 0 and
+ * lse = +inf.  Cache rows from lens[b] on are never read into a result, whatever
+ * they hold.  workspace: device, fab_paged_attention_workspace_bytes() bytes,
+ * contents overwritten; calls that may overlap on the GPU need one each. */
+FAB_EXPORT int fab_paged_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* starts,
+                                   const int32_t* lens, const int32_t* table, int causal, float scale, int dtype,
+                                   const fab_paged_dims* dims, void* workspace, size_t workspace_bytes, void* o,
+                                   float* lse, fab_stream stream);
+
 /* Synchronises `stream`, then returns and clears the device-side error word
  * of the current device: FAB_OK, FAB_ERR_TIMEOUT (a bounded wait inside a
- * kernel ran out; that kernel's outputs are invalid) or FAB_ERR_CUDA. */
+ * kernel ran out; that kernel's outputs are invalid), FAB_ERR_INVALID (a
+ * position, page number or start that a kernel read from device memory was out
+ * of range) or FAB_ERR_CUDA. */
 FAB_EXPORT int fab_last_device_error(fab_stream stream);
 
 #ifdef __cplusplus
