@@ -347,13 +347,19 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _raw_stream(stream, dev):
+    """As _stream, without building a Stream object for the current one (3 us
+    a call on the host, more than a small launch takes)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
 def fab_qk_norm_rope(q, k, v, wq, wk, cos, sin, pos, eps, interleaved, q_out, k_out, v_out, stream=None):
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q, k must be 4-D: (B,N,H,DK), (B,N,Hkv,DK)")
     B, N, H, DK = q.shape
     Hkv, DV = k.shape[2], DK if v is None else v.shape[-1]
     dt = q.dtype
-    _here(q, k, v, wq, wk, cos, sin, pos, q_out, k_out, v_out)
+    dev = _here(q, k, v, wq, wk, cos, sin, pos, q_out, k_out, v_out)
     rot, P = _check_tables(cos, sin, wq, wk, DK, dt)
     dims = fab_rope_dims(B, N, H, Hkv, DK, DV, rot, P, _ld(q, "q", dt, (B, N, H, DK)),
                          _ld(k, "k", dt, (B, N, Hkv, DK)), 0 if v is None else _ld(v, "v", dt, (B, N, Hkv, DV)))
@@ -361,7 +367,7 @@ def fab_qk_norm_rope(q, k, v, wq, wk, cos, sin, pos, eps, interleaved, q_out, k_
         q.data_ptr(), k.data_ptr(), _addr(v), _addr(wq), _addr(wk), _addr(cos), _addr(sin),
         _ptr(pos, "pos", torch.int32, (B, N)), float(eps), int(bool(interleaved)), dtype_code(q), ctypes.byref(dims),
         _ptr(q_out, "q_out", dt, (B, H, N, DK)), _ptr(k_out, "k_out", dt, (B, Hkv, N, DK)),
-        _ptr(v_out, "v_out", dt, (B, Hkv, N, DV)), _stream(stream)), "fab_qk_norm_rope")
+        _ptr(v_out, "v_out", dt, (B, Hkv, N, DV)), _raw_stream(stream, dev)), "fab_qk_norm_rope")
 
 
 def fab_qk_norm_rope_backward_workspace_bytes(dims: fab_rope_dims) -> int:
@@ -384,7 +390,7 @@ def fab_qk_norm_rope_backward(dq, dk, dv, q, k, wq, wk, cos, sin, pos, eps, inte
     if dq.dim() != 4 or dk.dim() != 4:
         raise ValueError("dq, dk must be 4-D: (B,H,N,DK), (B,Hkv,N,DK)")
     B, H, N, DK = dq.shape
-    _here(dq, dk, dv, q, k, wq, wk, cos, sin, pos, workspace, gq, gk, gv, gwq, gwk)
+    dev = _here(dq, dk, dv, q, k, wq, wk, cos, sin, pos, workspace, gq, gk, gv, gwq, gwk)
     rot, P = _check_tables(cos, sin, wq, wk, DK, gq.dtype)
     dims = _rope_backward_dims(dq, dk, dv, q, k, wq, wk, rot, P, gq, gk, gv)
     f32 = torch.float32
@@ -395,7 +401,7 @@ def fab_qk_norm_rope_backward(dq, dk, dv, q, k, wq, wk, cos, sin, pos, eps, inte
         _ptr(pos, "pos", torch.int32, (B, N)), float(eps), int(bool(interleaved)), dtype_code(gq),
         ctypes.byref(dims), _addr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(), gq.data_ptr(), gk.data_ptr(),
-        _addr(gv), _ptr(gwq, "gwq", f32, (DK,)), _ptr(gwk, "gwk", f32, (DK,)), _stream(stream)),
+        _addr(gv), _ptr(gwq, "gwq", f32, (DK,)), _ptr(gwk, "gwk", f32, (DK,)), _raw_stream(stream, dev)),
         "fab_qk_norm_rope_backward")
 
 
@@ -421,7 +427,7 @@ def fab_paged_append(q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, 
         raise ValueError("q, k, v must be 3-D: (T,H,DK), (T,Hkv,DK), (T,Hkv,DV)")
     T, H, DK = q.shape
     dt = q.dtype
-    _here(q, k, v, wq, wk, cos, sin, starts, lens, table, q_out, k_cache, v_cache)
+    dev = _here(q, k, v, wq, wk, cos, sin, starts, lens, table, q_out, k_cache, v_cache)
     dims = _paged_dims(H, T, k_cache, v_cache, starts, lens, table)
     if k_cache.dtype != dt:
         raise ValueError(f"k_cache must be {dt}, got {k_cache.dtype}")
@@ -433,7 +439,7 @@ def fab_paged_append(q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, 
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(wq), _addr(wk), _addr(cos), _addr(sin), float(eps),
         int(bool(interleaved)), starts.data_ptr(), lens.data_ptr(), table.data_ptr(), dtype_code(q),
         ctypes.byref(dims), _ptr(q_out, "q_out", dt, (T, H, DK)), k_cache.data_ptr(), v_cache.data_ptr(),
-        _stream(stream)), "fab_paged_append")
+        _raw_stream(stream, dev)), "fab_paged_append")
 
 
 def fab_paged_attention_workspace_bytes(dims: fab_paged_dims, dtype: int) -> int:
@@ -446,7 +452,7 @@ def fab_paged_attention(q, k_cache, v_cache, starts, lens, table, causal, scale,
         raise ValueError("q must be 3-D: (T,H,DK)")
     T, H, DK = q.shape
     dt = q.dtype
-    _here(q, k_cache, v_cache, starts, lens, table, workspace, o, lse)
+    dev = _here(q, k_cache, v_cache, starts, lens, table, workspace, o, lse)
     dims = _paged_dims(H, T, k_cache, v_cache, starts, lens, table)
     if k_cache.dtype != dt:
         raise ValueError(f"k_cache must be {dt}, got {k_cache.dtype}")
@@ -454,7 +460,7 @@ def fab_paged_attention(q, k_cache, v_cache, starts, lens, table, causal, scale,
         _ptr(q, "q", dt, (T, H, dims.DK)), k_cache.data_ptr(), v_cache.data_ptr(), starts.data_ptr(),
         lens.data_ptr(), table.data_ptr(), int(bool(causal)), float(scale), dtype_code(q), ctypes.byref(dims),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(o, "o", dt, (T, H, dims.DV)),
-        _ptr(lse, "lse", torch.float32, (H, T)), _stream(stream)), "fab_paged_attention")
+        _ptr(lse, "lse", torch.float32, (H, T)), _raw_stream(stream, dev)), "fab_paged_attention")
 
 
 # ------------------------------------------------------------------ conveniences (torch allocates, libfab computes)
