@@ -105,6 +105,10 @@ PagedProblem paged_problem(const fab_paged_dims* d, int dtype) {
   return p;
 }
 
+size_t paged_workspace_bytes(const PagedProblem& p) {
+  return paged_tc_supported(p) ? paged_tc_workspace_bytes(p) : paged_simt_workspace_bytes(p);
+}
+
 }  // namespace
 }  // namespace fab
 
@@ -275,5 +279,9 @@ FAB_API int fab_paged_attention(const void* q, const void* k_cache, const void* 
   p.o = o;
   p.lse = lse;
   p.workspace = workspace;
+  if (paged_tc_supported(p)) {
+    if (!encode_tiled_fn()) return FAB_ERR_CUDA;
+    return from_cuda(launch_paged_tc(p, static_cast<cudaStream_t>(stream)));
+  }
   return from_cuda(launch_paged_simt(p, static_cast<cudaStream_t>(stream)));
 }

@@ -109,8 +109,13 @@ struct PagedProblem {
   float* lse;  // or null
   void* workspace;
 };
-size_t paged_workspace_bytes(const PagedProblem& p);
+// fab_paged_tc.cu: tcgen05, bf16 or f16, DK and DV multiples of 8 up to 128,
+// pages of a multiple of 8 rows.
+bool paged_tc_supported(const PagedProblem& p);
+size_t paged_tc_workspace_bytes(const PagedProblem& p);
+cudaError_t launch_paged_tc(const PagedProblem& p, cudaStream_t s);
 // fab_paged_simt.cu: CUDA cores, every dtype, DK, DV <= 256, any page.
+size_t paged_simt_workspace_bytes(const PagedProblem& p);
 cudaError_t launch_paged_simt(const PagedProblem& p, cudaStream_t s);
 
 // fab_host.cu: the checks the entry points share.
@@ -132,5 +137,6 @@ uint32_t take_error_dq();
 uint32_t take_error_fwd();
 uint32_t take_error_rope();
 uint32_t take_error_paged();
+uint32_t take_error_paged_tc();
 
 }  // namespace fab

@@ -1,0 +1,349 @@
+// fab_paged.cuh -- how the paged attention kernels share out their work, and
+// how the pieces of a split row are joined.
+//
+// The lengths live on the device, so the kernels divide the work themselves.
+// A tile is `nt` tokens times `gw` query heads of one key/value head (a row
+// per pair); a unit is one tile or two (consecutive tokens) and walks its key
+// tiles.  Units in order of (sequence, head, tokens) form one line, each as
+// long as its key tiles times its tiles, and CTA c of G takes the piece from
+// W c / G to W (c+1) / G of that line, so every CTA has the same work
+// whatever the lengths are.  A unit cut by a border leaves unnormalised
+// partial results (output, maximum, sum) in the workspace, at most two to a
+// CTA, which paged_combine_kernel joins.
+#pragma once
+
+#include "fab_device.cuh"
+#include "fab_internal.h"
+
+namespace fab {
+
+constexpr int kPagedMaxGrid = 304;  // CTAs that the workspace has room for
+
+// What planning needs to know.
+struct PagedPlan {
+  const int32_t *starts, *lens;
+  int64_t B, T, max_keys;  // max_keys: keys that a row of the table can hold
+  int causal;
+  int G, gw, gblocks;  // query heads of a key/value head, of a tile; tiles over them
+  int heads;           // Hkv * gblocks
+  int nt, tiles;       // tokens of a tile, tiles of a unit (1 or 2)
+  int kt;              // keys of a key tile
+};
+
+struct PagedSeq {
+  int s0, n;     // first new token, how many
+  int last0;     // last key its first new token sees under a causal mask (may be negative)
+  int len;       // keys
+};
+
+FAB_DEV PagedSeq paged_seq(const PagedPlan& p, int b) {
+  PagedSeq q;
+  // (clamped: starts and lengths out of range must not reach an address)
+  const int64_t T = p.T, a = p.starts[b], e = p.starts[b + 1];
+  const int64_t s0 = a < 0 ? 0 : a > T ? T : a, s1 = e < s0 ? s0 : e > T ? T : e;
+  const int64_t len = p.lens[b];
+  q.s0 = (int)s0;
+  q.n = (int)(s1 - s0);
+  q.last0 = (int)(len - q.n < -q.n - 1 ? -q.n - 1 : len - q.n);
+  q.len = (int)(len < 0 ? 0 : len > p.max_keys ? p.max_keys : len);
+  return q;
+}
+
+FAB_DEV int paged_units(const PagedPlan& p, const PagedSeq& q) {
+  const int per = p.nt * p.tiles;
+  return (q.n + per - 1) / per;
+}
+// Tiles of unit i (one where its tokens fit one tile), and its key tiles.
+FAB_DEV int paged_width(const PagedPlan& p, const PagedSeq& q, int i) {
+  return p.tiles == 2 && q.n - i * 2 * p.nt > p.nt ? 2 : 1;
+}
+FAB_DEV int paged_key_tiles(const PagedPlan& p, const PagedSeq& q, int i) {
+  int end = q.len;
+  if (p.causal) {
+    const int per = p.nt * p.tiles, hi = (i + 1) * per < q.n ? (i + 1) * per : q.n;
+    if (q.last0 + hi < end) end = q.last0 + hi;
+  }
+  return end > 0 ? (end + p.kt - 1) / p.kt : 1;
+}
+
+// Place on the line: unit i of head `head` of sequence b, which begins at u0.
+struct PagedPlace {
+  int b, head, i;
+  int64_t u0;
+};
+
+struct PagedShared {
+  int64_t sums[32];
+  int64_t total;
+  PagedPlace at;
+};
+
+// Where CTA c's piece begins.
+FAB_DEV int64_t paged_border(int64_t W, int G, int c) {
+  const int64_t q = W / G;
+  return q * c + (int64_t)((uint32_t)((int)(W - q * G) * c) / (uint32_t)G);
+}
+
+// The line's length in s->total.  Called by the whole block (NT threads).
+template <int NT>
+FAB_DEV void paged_total(const PagedPlan& p, PagedShared* s, int64_t* mine) {
+  int64_t sum = 0, one = 0;
+  for (int64_t b = threadIdx.x; b < p.B; b += NT) {
+    const PagedSeq q = paged_seq(p, (int)b);
+    one = 0;
+    for (int i = 0, k = paged_units(p, q); i < k; ++i) one += paged_width(p, q, i) * paged_key_tiles(p, q, i);
+    one *= p.heads;
+    sum += one;
+  }
+  *mine = one;  // (of use where B <= NT: then the only one)
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((threadIdx.x & 31) == 0) s->sums[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int64_t w = 0;
+    for (int i = 0; i < NT / 32; ++i) w += s->sums[i];
+    s->total = w;
+  }
+  __syncthreads();
+}
+
+// The unit that holds `pos` (0 <= pos < s->total) in s->at.  Whole block.
+template <int NT>
+FAB_DEV void paged_locate(const PagedPlan& p, PagedShared* s, int64_t mine, int64_t pos) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t base = 0;
+  for (int64_t b0 = 0; b0 < p.B; b0 += NT) {
+    const int64_t b = b0 + threadIdx.x;
+    int64_t one = mine;
+    if (p.B > NT) {
+      one = 0;
+      if (b < p.B) {
+        const PagedSeq q = paged_seq(p, (int)b);
+        for (int i = 0, k = paged_units(p, q); i < k; ++i) one += paged_width(p, q, i) * paged_key_tiles(p, q, i);
+        one *= p.heads;
+      }
+    }
+    int64_t incl = one;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 31) s->sums[warp] = incl;
+    __syncthreads();
+    int64_t before = base;
+    for (int i = 0; i < warp; ++i) before += s->sums[i];
+    const int64_t first = before + incl - one;
+    if (one > 0 && pos >= first && pos < first + one) {
+      const PagedSeq q = paged_seq(p, (int)b);
+      const int64_t head_len = one / p.heads;
+      PagedPlace at;
+      at.b = (int)b;
+      at.head = (int)((pos - first) / head_len);
+      at.u0 = first + at.head * head_len;
+      at.i = 0;
+      for (;;) {
+        const int64_t len = paged_width(p, q, at.i) * (int64_t)paged_key_tiles(p, q, at.i);
+        if (pos < at.u0 + len) break;
+        at.u0 += len;
+        ++at.i;
+      }
+      s->at = at;
+    }
+    for (int i = 0; i < NT / 32; ++i) base += s->sums[i];
+    __syncthreads();
+    if (base > pos) break;
+  }
+}
+
+// Walks a CTA's piece of the line, unit by unit.
+struct PagedWalk {
+  PagedSeq q;
+  PagedPlace at;
+  int width, ntiles;   // of the present unit
+  int j0, j1;          // its key tiles that lie in the piece
+  int units;           // of a head of the sequence
+
+  FAB_DEV void load(const PagedPlan& p) {
+    width = paged_width(p, q, at.i);
+    ntiles = paged_key_tiles(p, q, at.i);
+  }
+  FAB_DEV void begin(const PagedPlan& p, const PagedPlace& start) {
+    at = start;
+    q = paged_seq(p, at.b);
+    units = paged_units(p, q);
+    load(p);
+  }
+  // Key tiles of the present unit before `pos` on the line.
+  FAB_DEV int tiles_before(int64_t pos) const {
+    const int64_t d = pos - at.u0;
+    if (d <= 0) return 0;
+    const int64_t t = width == 2 ? (d + 1) >> 1 : d;
+    return t < ntiles ? (int)t : ntiles;
+  }
+  // The part of the piece [p0, p1) that lies in the present unit; false past the piece.
+  FAB_DEV bool piece(int64_t p0, int64_t p1) {
+    if (at.u0 >= p1) return false;
+    j0 = tiles_before(p0);
+    j1 = tiles_before(p1);
+    return true;
+  }
+  // The next unit (its j0, j1 are not set); false at the end of the line.
+  FAB_DEV bool next(const PagedPlan& p) {
+    at.u0 += (int64_t)width * ntiles;
+    if (++at.i == units) {
+      at.i = 0;
+      if (++at.head == p.heads) {
+        at.head = 0;
+        do {
+          if (++at.b >= p.B) return false;
+          q = paged_seq(p, at.b);
+          units = paged_units(p, q);
+        } while (units == 0);
+      }
+    }
+    load(p);
+    return true;
+  }
+  FAB_DEV bool whole() const { return j0 == 0 && j1 == ntiles; }
+  // The piece's partial slot: 2c for a unit that began before it, else 2c + 1.
+  FAB_DEV int slot(int c) const { return 2 * c + (j0 == 0 ? 1 : 0); }
+};
+
+// Partial results: rows of `dp` floats, and (maximum in log2 units, sum) pairs.
+struct PagedParts {
+  float* out;
+  float2* ml;
+  int rows, dp;  // rows of a slot, floats of a row
+};
+inline size_t paged_parts_bytes(int rows, int dp) {
+  return (size_t)(2 * kPagedMaxGrid) * rows * (dp + 2) * sizeof(float);
+}
+inline PagedParts paged_parts(void* workspace, int rows, int dp) {
+  PagedParts x;
+  x.out = static_cast<float*>(workspace);
+  x.ml = reinterpret_cast<float2*>(x.out + (size_t)(2 * kPagedMaxGrid) * rows * dp);
+  x.rows = rows;
+  x.dp = dp;
+  return x;
+}
+
+FAB_DEV void paged_store(float* p, float x) { *p = x; }
+FAB_DEV void paged_store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+FAB_DEV void paged_store(__half* p, float x) { *p = __float2half_rn(x); }
+
+constexpr int kCombineThreads = 256;
+
+// Joins the units that the border between CTA blockIdx.x and the next cuts, if
+// the former holds the unit's first part: out = sum 2^(m_i - M) out_i / sum
+// 2^(m_i - M) l_i over its parts.  A warp per row, blockIdx.y of gridDim.y of
+// them.  Launched while the attention kernel still runs; waits for it first.
+template <typename T>
+__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedPlan p, const PagedParts parts,
+                                                                        int grid, int DV, int H, T* o, float* lse) {
+  __shared__ PagedShared sh;
+  int64_t mine;
+  paged_total<kCombineThreads>(p, &sh, &mine);
+  const int64_t W = sh.total;
+  const int c = (int)blockIdx.x;
+  const int64_t p0 = paged_border(W, grid, c), p1 = paged_border(W, grid, c + 1);
+  if (p1 < W && p1 > p0) paged_locate<kCombineThreads>(p, &sh, mine, p1);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p1 >= W || p1 <= p0) return;
+  PagedWalk w;
+  w.begin(p, sh.at);
+  // not cut here, or the first part is an earlier CTA's
+  const int mine_tiles = w.tiles_before(p1);
+  if (mine_tiles == 0 || mine_tiles == w.ntiles || p0 > w.at.u0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // CTAs c .. ce hold the unit's parts
+  int ce = c;
+  for (int base = c + 1;; base += 32) {
+    const int x = base + lane;
+    const bool done = x >= grid - 1 || w.tiles_before(paged_border(W, grid, x + 1)) >= w.ntiles;
+    const unsigned v = __ballot_sync(0xffffffffu, done);
+    if (v != 0) {
+      ce = base + __ffs((int)v) - 1;
+      break;
+    }
+  }
+  const int rows = w.width * p.nt * p.gw;
+  const int hk = w.at.head / p.gblocks, gb = w.at.head - hk * p.gblocks;
+  const int token0 = w.at.i * p.nt * p.tiles;
+  for (int x = (int)blockIdx.y * (kCombineThreads / 32) + warp; x < rows; x += (int)gridDim.y * (kCombineThreads / 32)) {
+    const int tile = x / (p.nt * p.gw), r = x - tile * p.nt * p.gw;
+    const int token = token0 + tile * p.nt + r / p.gw, g = gb * p.gw + r % p.gw;
+    if (token >= w.q.n || g >= p.G) continue;
+    const int row = tile * (parts.rows / p.tiles) + r;
+    // this lane's part of up to 32 at a time: a part without tiles has no weight
+    auto part_ml = [&](int k) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (k <= ce) {
+        const int a = k == c ? 0 : w.tiles_before(paged_border(W, grid, k));
+        const int b = w.tiles_before(paged_border(W, grid, k + 1));
+        if (a < b) ml = parts.ml[(int64_t)(k == c ? 2 * k + 1 : 2 * k) * parts.rows + row];
+      }
+      return ml;
+    };
+    float top = -INFINITY;
+    for (int k0 = c; k0 <= ce; k0 += 32) {
+      float m = part_ml(k0 + lane).x;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+      top = fmaxf(top, m);
+    }
+    const float ref = top == -INFINITY ? 0.f : top;
+    float acc[8], l = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    for (int k0 = c; k0 <= ce; k0 += 32) {
+      const float2 ml = part_ml(k0 + lane);
+      // (a part whose sum is zero has nothing to add, whatever its row holds)
+      const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - ref);
+      float sum = f * ml.y;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+      l += sum;
+      const int count = ce - k0 + 1 < 32 ? ce - k0 + 1 : 32;
+#pragma unroll 4
+      for (int k = 0; k < count; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k);
+        const int kk = k0 + k;
+        const float* src = parts.out + ((int64_t)(kk == c ? 2 * kk + 1 : 2 * kk) * parts.rows + row) * parts.dp;
+        if (fk != 0.f) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (lane + 32 * e < DV) acc[e] += fk * src[lane + 32 * e];
+        }
+      }
+    }
+    const int64_t t = w.q.s0 + token, h = (int64_t)hk * p.G + g;
+    T* dst = o + (t * H + h) * DV;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (lane + 32 * e < DV) paged_store(dst + lane + 32 * e, acc[e] * inv);
+    if (lse != nullptr && lane == 0) lse[h * p.T + t] = l == 0.f ? INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+// Enqueues the combine kernel behind an attention kernel of `grid` CTAs.
+template <typename T>
+cudaError_t launch_combine(const PagedPlan& plan, const PagedParts& parts, int grid, int DV, int H, T* o, float* lse,
+                           cudaStream_t s) {
+  if (grid < 2) return cudaSuccess;  // nothing is cut
+  const int rows = plan.tiles * plan.nt * plan.gw;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)((rows + 31) / 32));
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<T>, plan, parts, grid, DV, H, o, lse);
+}
+
+}  // namespace fab

@@ -110,7 +110,7 @@ cudaError_t paged_t(const PagedProblem& p, cudaStream_t s) {
 
 }  // namespace
 
-size_t paged_workspace_bytes(const PagedProblem&) { return 256; }
+size_t paged_simt_workspace_bytes(const PagedProblem&) { return 256; }
 
 cudaError_t launch_paged_simt(const PagedProblem& p, cudaStream_t s) {
   if (p.dtype == FAB_BF16) return paged_t<__nv_bfloat16>(p, s);

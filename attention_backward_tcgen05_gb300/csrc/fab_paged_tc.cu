@@ -1,0 +1,634 @@
+// fab_paged_tc.cu -- attention of new tokens over a paged key/value cache, on
+// tcgen05: bf16 or f16, DK and DV multiples of 8 up to 128, pages of a
+// multiple of 8 rows.
+//
+//   token i of the n new ones of sequence b, head h:
+//   s_m = scale q . k_m over m <= lens[b] - n + i (causal) or m < lens[b],
+//   o = sum softmax(s)_m v_m,  lse = log sum exp(s_m)
+//
+// Tiles.  A row of a tile is a (token, query head) pair of one key/value head:
+// 128 / group tokens times the group's heads, so a page of keys is read once
+// for the whole group and a single token still fills as many rows as it has
+// heads.  Two streams of four softmax warps each own a score tile S_s and an
+// output O_s in tensor memory (thread = row, all 128 keys of a tile), and the
+// tensor core alternates between them: while one stream's softmax runs, the
+// other's products do.  A unit of two row tiles gives each stream a row tile
+// and lets both use every key tile; a unit of one (a decoding step, a short
+// chunk) gives the streams alternate key tiles of the same rows, joined at
+// the end.  Work is cut evenly over the SMs by fab_paged.cuh whatever the
+// lengths are.
+//
+// Keys and values stream through TMA rings; each box holds min(page, 128)
+// rows of one page, fetched by the lane that looked its page up.  Past the
+// last key, scores are masked by index and value rows are zeroed in shared
+// memory, so nothing of a cache's unused rows reaches a product.
+//
+// The running maximum is raised only when a tile exceeds it by more than 8
+// (log2): weights then stay below 2^8 and the output is rescaled rarely; the
+// sum and the output share the stale maximum, so the result is exact.  f16
+// weights are kept 2^7 larger, which moves their smallest step 2^7 down.
+// Weights are rounded to the input type for the second product; their sum is
+// not.
+//
+// Warps (384 threads): 0 = query and key loads, 1 = matrix instructions, 2 =
+// value loads, 3 = tensor memory; 4-7 and 8-11 = the two softmax streams.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "fab.h"
+#include "fab_device.cuh"
+#include "fab_internal.h"
+#include "fab_paged.cuh"
+
+namespace fab {
+namespace {
+
+__device__ uint32_t g_err_paged_tc;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleThreshold = 8.f;  // log2 units
+constexpr int kThreads = 384;
+
+template <int DP>
+struct PCfg {
+  static constexpr int ATOMS = DP / 64;
+  static constexpr uint32_t ATOM = 128 * 128;  // 128 rows of 128 swizzled bytes
+  static constexpr uint32_t TILE = ATOMS * ATOM;
+  static constexpr int NK = DP == 128 ? 2 : 4, NV = DP == 128 ? 3 : 4;  // ring slots
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_K = 2 * TILE;
+  static constexpr uint32_t OFF_V = OFF_K + NK * TILE;
+  static constexpr uint32_t OFF_BAR = OFF_V + NV * TILE;
+  static constexpr uint32_t OFF_MISC = OFF_BAR + 32 * 8;
+  static constexpr uint32_t OFF_ML = OFF_MISC + 512;  // 128 (maximum, sum) pairs
+  static constexpr uint32_t USED = OFF_ML + 128 * 8;
+  static constexpr uint32_t SMEM = USED > 118784 ? USED : 118784;  // one CTA owns the SM's tensor memory
+  static constexpr uint32_t TM_S = 0;    // + 128 * stream
+  static constexpr uint32_t TM_O = 256;  // + DP * stream
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(sizeof(PagedShared) + 16 <= 512, "misc area");
+};
+
+enum : int {
+  B_KF = 0,   // + slot: K landed
+  B_KE = 4,   // + slot: K free
+  B_VF = 8,   // + slot: V landed
+  B_VE = 12,  // + slot: V free
+  B_QF = 16,  // a unit's Q landed
+  B_QE = 17,  // a unit's S products finished
+  B_S = 18,   // + stream: S landed (and every product issued before it)
+  B_P = 20,   // + stream: P written (and O rescaled where it had to be)
+  B_O = 22,   // + stream: the unit's last product of the stream finished
+  B_ML = 24,  // one-tile units: stream 1's maxima and sums are in shared memory
+  B_MD = 25,  // one-tile units: stream 0 has read stream 1's output
+  B_FIN = 26,
+  B_COUNT = 27
+};
+
+struct TcParams {
+  PagedPlan plan;
+  PagedParts parts;
+  const int32_t* table;
+  int64_t max_pages, pages;
+  int page, box;  // rows of a page, of a TMA box
+  int H, DV;
+  float scale;
+  void* o;
+  float* lse;
+};
+
+FAB_DEV void reg_dealloc() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
+FAB_DEV void reg_alloc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+
+template <int DP, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TcParams p) {
+  using C = PCfg<DP>;
+  using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
+  extern __shared__ uint8_t smem[];
+  if (smem_u32(smem) & 1023u) {  // swizzled tiles need a 1024-byte-aligned base
+    if (threadIdx.x == 0) atomicOr(&g_err_paged_tc, kErrSmemAlign);
+    return;
+  }
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + C::OFF_BAR + 8u * (uint32_t)i; };
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 4);
+  PagedShared* sh = reinterpret_cast<PagedShared*>(smem + C::OFF_MISC + 16);
+  float2* ml_s = reinterpret_cast<float2*>(smem + C::OFF_ML);
+  uint32_t* err = &g_err_paged_tc;
+  const int warp = (int)warp_id(), lane = (int)lane_id();
+  const PagedPlan& plan = p.plan;
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0u;
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(bar(B_KF + s), 1);
+      mbar_init(bar(B_KE + s), 1);
+      mbar_init(bar(B_VF + s), 1);
+      mbar_init(bar(B_VE + s), 1);
+    }
+    mbar_init(bar(B_QF), 1);
+    mbar_init(bar(B_QE), 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(B_S + s), 1);
+      mbar_init(bar(B_P + s), 4);
+      mbar_init(bar(B_O + s), 1);
+    }
+    mbar_init(bar(B_ML), 128);
+    mbar_init(bar(B_MD), 128);
+    mbar_init(bar(B_FIN), 1);
+    fence_mbar_init();
+    prefetch_tensormap(&tmQ);
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+  if (warp == 3) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_relinquish();
+  }
+  if (blockIdx.x == 0) check_starts(plan.starts, plan.B, plan.T, (int)threadIdx.x, kThreads, err);
+  int64_t mine;
+  paged_total<kThreads>(plan, sh, &mine);
+  const int64_t W = sh->total;
+  const int64_t p0 = paged_border(W, (int)gridDim.x, (int)blockIdx.x);
+  const int64_t p1 = paged_border(W, (int)gridDim.x, (int)blockIdx.x + 1);
+  if (p0 < p1) paged_locate<kThreads>(plan, sh, mine, p0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tm = *tmem_holder;
+  const PagedPlace start = sh->at;
+  const bool any = p0 < p1;
+
+  if (warp < 4) {
+    reg_dealloc();
+    if (any && (warp == 0 || warp == 2)) {
+      // ------------------------------------------------------------ loads
+      // Warp 0: a unit's Q (once the previous unit's S products are done with
+      // theirs) and its keys; warp 2: its values.  Lane i fetches box i of a
+      // tile; its page number is looked up a tile ahead.
+      const bool keys = warp == 0;
+      const int full = keys ? B_KF : B_VF, empty = keys ? B_KE : B_VE, slots = keys ? C::NK : C::NV;
+      const uint32_t ring = sbase + (keys ? C::OFF_K : C::OFF_V);
+      const CUtensorMap* map = keys ? &tmK : &tmV;
+      int slot = 0, phase = 1, units = 0;
+      bool ok = true;
+      PagedWalk w;
+      w.begin(plan, start);
+      bool more = true;
+      while (ok && more && w.piece(p0, p1)) {
+        if (w.j0 < w.j1) {
+          const int hk = w.at.head / plan.gblocks;
+          // page of box `lane` of key tile j, and how many boxes hold keys
+          auto lookup = [&](int j, int& row) {
+            const uint32_t m = (uint32_t)j * 128u + (uint32_t)(lane * p.box);
+            const uint32_t at = m / (uint32_t)p.page;
+            row = (int)(m - at * (uint32_t)p.page);
+            if (lane * p.box >= 128 || m >= (uint32_t)w.q.len) return 0;
+            const int page = __ldg(p.table + (int64_t)w.at.b * p.max_pages + at);
+            // (out of range: the copy fills zeros, the call is reported)
+            if (page < 0 || page >= p.pages) atomicOr(err, kErrIndex);
+            return page;
+          };
+          int row, page = lookup(w.j0, row);
+          if (keys) {
+            if (plan.lens[w.at.b] > plan.max_keys && lane == 0) atomicOr(err, kErrIndex);
+            if (units > 0 && !(ok = mbar_wait(bar(B_QE), (units - 1) & 1, abort_flag, err))) break;
+            if (lane == 0) {
+              const uint32_t bytes = (uint32_t)(64 * 2 * plan.gw * plan.nt * C::ATOMS);
+              mbar_arrive_expect_tx(bar(B_QF), bytes * w.width);
+              const int head = hk * plan.G + (w.at.head - hk * plan.gblocks) * plan.gw;
+              for (int s = 0; s < w.width; ++s)
+                for (int a = 0; a < C::ATOMS; ++a)
+                  tma_load_3d(sbase + C::OFF_Q + s * C::TILE + a * C::ATOM, &tmQ, bar(B_QF), a * 64, head,
+                              w.q.s0 + w.at.i * plan.nt * 2 + s * plan.nt);
+            }
+            ++units;
+          }
+          for (int j = w.j0; j < w.j1; ++j) {
+            if (!(ok = mbar_wait(bar(empty + slot), phase, abort_flag, err))) break;
+            const int held = w.q.len - j * 128;  // keys of the tile and beyond
+            const int boxes = held <= 0 ? 0 : held >= 128 ? 128 / p.box : (held + p.box - 1) / p.box;
+            fence_proxy_async_smem();
+            if (lane == 0) mbar_arrive_expect_tx(bar(full + slot), (uint32_t)(boxes * p.box * 128 * C::ATOMS));
+            __syncwarp();
+            if (lane < boxes) {
+              const uint32_t dst = ring + slot * C::TILE + lane * p.box * 128;
+#pragma unroll
+              for (int a = 0; a < C::ATOMS; ++a)
+                tma_load_4d(dst + a * C::ATOM, map, bar(full + slot), a * 64, row, hk, page);
+            }
+            if (++slot == slots) slot = 0, phase ^= 1;
+            if (j + 1 < w.j1) page = lookup(j + 1, row);
+          }
+        }
+        more = w.next(plan);
+      }
+      // let the copies in flight land before shared memory goes
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok && lane == 0 && keys && units > 0) mbar_drain(bar(B_QF), (units - 1) & 1);
+      if (!ok && lane == 0)
+        for (int s = 0; s < slots; ++s) mbar_drain(bar(full + s), s < slot ? phase ^ 1 : phase);
+    } else if (any && warp == 1) {
+      // ------------------------------------------------------------ products
+      // Step i of a unit belongs to stream i & 1.  S(i + 2) is issued behind
+      // O += P(i) V, which frees its columns (matrix instructions of a CTA run
+      // in the order of their issue).
+      const uint32_t issue = lane == 0 ? 1u : 0u;
+      constexpr uint32_t ID_S = idesc_16(128, 128, false, false, F16);
+      constexpr uint32_t ID_PV = idesc_16(128, DP, false, true, F16);
+      auto wall = [&](int i, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort_flag, err));
+      };
+      int kslot = 0, kphase = 0, vslot = 0, vphase = 0, units = 0;
+      uint32_t pphase[2] = {0, 0};
+      bool ok = true, more = true;
+      PagedWalk w;
+      w.begin(plan, start);
+      while (ok && more && w.piece(p0, p1)) {
+        if (w.j0 < w.j1) {
+          const bool wide = w.width == 2;
+          const int steps = (w.j1 - w.j0) * w.width;
+          auto issue_s = [&](int i) {
+            const int s = i & 1;
+            if (!wide || s == 0) ok = wall(B_KF + kslot, kphase);
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t sQ = sbase + C::OFF_Q + (wide && s ? C::TILE : 0u), sK = sbase + C::OFF_K + kslot * C::TILE;
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * C::ATOM + (kk & 3) * 32;
+              mma_ss(tm + C::TM_S + s * 128, sdesc_sw128(sQ + off, 16, 1024), sdesc_sw128(sK + off, 16, 1024), ID_S,
+                     kk > 0, issue);
+            }
+            mma_commit(bar(B_S + s), issue);
+            if (!wide || s == 1) {
+              mma_commit(bar(B_KE + kslot), issue);
+              if (++kslot == C::NK) kslot = 0, kphase ^= 1;
+            }
+            if (i == steps - 1) mma_commit(bar(B_QE), issue);
+          };
+          if (!(ok = wall(B_QF, units & 1))) break;
+          ++units;
+          issue_s(0);
+          if (ok && steps > 1) issue_s(1);
+          for (int i = 0; ok && i < steps; ++i) {
+            const int s = i & 1;
+            const int j = w.j0 + (wide ? i >> 1 : i);
+            const uint32_t sV = sbase + C::OFF_V + vslot * C::TILE;
+            int ksteps = 8;
+            if (!wide || s == 0) {
+              if (!(ok = wall(B_VF + vslot, vphase))) break;
+            }
+            const int held = w.q.len - j * 128;
+            if (held < 128) {
+              // the last keys' tile: products over whole 16-key steps, the
+              // rows between the last key and the step's end zeroed
+              const int live = held < 0 ? 0 : held;
+              ksteps = live == 0 ? 1 : (live + 15) / 16;
+              if (!wide || s == 0) {
+                for (int x = live * 8 + lane; x < ksteps * 128; x += 32)
+#pragma unroll
+                  for (int a = 0; a < C::ATOMS; ++a) st_shared_v4(sV + a * C::ATOM + x * 16, 0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+                __syncwarp();
+              }
+            }
+            if (!(ok = wall(B_P + s, pphase[s]))) break;
+            pphase[s] ^= 1;
+            tc_fence_after();
+            for (int kk = 0; kk < ksteps; ++kk)
+              mma_ts(tm + C::TM_O + s * DP, tm + C::TM_S + s * 128 + kk * 8, sdesc_sw128(sV + kk * 2048, C::ATOM, 1024),
+                     ID_PV, (i >= 2 || kk > 0) ? 1u : 0u, issue);
+            if (!wide || s == 1) {
+              mma_commit(bar(B_VE + vslot), issue);
+              if (++vslot == C::NV) vslot = 0, vphase ^= 1;
+            }
+            if (i + 2 < steps) issue_s(i + 2); else mma_commit(bar(B_O + s), issue);
+          }
+        }
+        more = w.next(plan);
+      }
+      mma_commit(bar(B_FIN), issue);
+      mbar_drain(bar(B_FIN), 0);
+    }
+  } else {
+    reg_alloc();
+    // -------------------------------------------------------------- softmax
+    const int s = (warp - 4) >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tm + lane_off + C::TM_S + s * 128, tO = tm + lane_off + C::TM_O + s * DP;
+    // weights 2^(s c1 - m); a scale below zero turns the scores' signs, and a
+    // zero one is taken as one too small to tell the scores apart (0 times a
+    // masked score would be NaN)
+    const bool neg = p.scale < 0.f;
+    const float c1 = fmaxf(fabsf(p.scale) * kLog2e, 1e-37f);
+    constexpr float kBias = F16 ? 7.f : 0.f;
+    const int i_row = r / plan.gw, g_row = r - i_row * plan.gw;
+    uint32_t sphase = 0, ophase = 0, mphase = 0;
+    bool ok = true, more = any;
+    PagedWalk w;
+    if (any) w.begin(plan, start);
+    while (ok && more && w.piece(p0, p1)) {
+      if (w.j0 < w.j1) {
+        const bool wide = w.width == 2;
+        const int n = w.j1 - w.j0;
+        const int hk = w.at.head / plan.gblocks, gb = w.at.head - hk * plan.gblocks;
+        const int token = w.at.i * plan.nt * 2 + (wide ? s * plan.nt : 0) + i_row;
+        const int g = gb * plan.gw + g_row;
+        const bool row_ok = i_row < plan.nt && token < w.q.n && g < plan.G;
+        const bool active = __any_sync(0xffffffffu, row_ok);
+        int last = w.q.len - 1;  // last key the row sees
+        if (plan.causal && w.q.last0 + token < last) last = w.q.last0 + token;
+        if (!row_ok) last = -1;
+        float m_run = -INFINITY, l = 0.f;
+        for (int t = wide ? 0 : s; t < n; t += wide ? 1 : 2) {
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(B_S + s), sphase, abort_flag, err)))) break;
+          sphase ^= 1;
+          if (active) {
+            tc_fence_after();
+            const int k0 = (w.j0 + t) * 128;
+            uint32_t x[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, x[c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld_wait(x[c]);
+            auto sv = [&](int e) -> uint32_t& { return x[e >> 5][e & 31]; };
+            if (neg) {
+#pragma unroll
+              for (int e = 0; e < 128; ++e) sv(e) ^= 0x80000000u;
+            }
+            if (__any_sync(0xffffffffu, k0 + 127 > last)) {
+              const int lim = last - k0;
+#pragma unroll
+              for (int e = 0; e < 128; ++e)
+                if (e > lim) sv(e) = 0xff800000u;  // -inf
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < 128; e += 4)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(sv(e + c)));
+            const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c1;
+            float alpha = 1.f;
+            bool need = false;
+            if (tmax > m_run + kRescaleThreshold || (m_run == -INFINITY && tmax > -INFINITY)) {
+              need = m_run != -INFINITY;
+              alpha = need ? exp2f(m_run - tmax) : 1.f;
+              m_run = tmax;
+            }
+            if (__any_sync(0xffffffffu, need)) {
+              // (every product into O_s was issued before this S, so it is done)
+#pragma unroll 1
+              for (int c0 = 0; c0 < DP; c0 += 32) {
+                uint32_t o[32];
+                tmem_ld32(tO + c0, o);
+                tmem_ld_wait(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st32(tO + c0, o);
+              }
+              l *= alpha;
+            }
+            const float ref = m_run == -INFINITY ? 0.f : m_run - kBias;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t pk[32];
+#pragma unroll
+              for (int c = 0; c < 32; ++c) {
+                const int e = h * 64 + 2 * c;
+                const float a = ex2_approx(fmaf(__uint_as_float(sv(e)), c1, -ref));
+                const float b = ex2_approx(fmaf(__uint_as_float(sv(e + 1)), c1, -ref));
+                sum[(2 * c) & 3] += a;
+                sum[(2 * c + 1) & 3] += b;
+                pk[c] = pack2<F16>(a, b);
+              }
+              tmem_st32(tS + h * 32, pk);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st_wait();
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_P + s));
+        }
+        if (!ok) break;
+        // ---- the unit's end: O / l and the log-sum-exp, or partial results
+        const float ref = m_run == -INFINITY ? 0.f : m_run - kBias;
+        const bool ran = wide || s < n;  // the stream had a key tile
+        if (ran) {
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(B_O + s), ophase, abort_flag, err)))) break;
+          ophase ^= 1;
+        }
+        float f0 = 1.f, f1 = 0.f, lt = l, mt = ref;  // the row is f0 O_0 + f1 O_1
+        if (!wide) {
+          if (s == 1) {
+            // hand over to stream 0, which has the same rows in the same lanes
+            ml_s[r] = make_float2(ref, l);
+            tc_fence_after();
+            tc_fence_before();
+            mbar_arrive(bar(B_ML));
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(B_MD), mphase, abort_flag, err)))) break;
+            mphase ^= 1;
+            more = w.next(plan);
+            continue;
+          }
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(B_ML), mphase, abort_flag, err)))) break;
+          mphase ^= 1;
+          const float2 other = ml_s[r];
+          if (other.y != 0.f) {
+            if (l == 0.f) {
+              mt = other.x;
+              f0 = 0.f;
+              f1 = 1.f;
+            } else {
+              mt = fmaxf(ref, other.x);
+              f0 = exp2f(ref - mt);
+              f1 = exp2f(other.x - mt);
+            }
+            lt = (f0 == 0.f ? 0.f : f0 * l) + f1 * other.y;
+          }
+        }
+        if (active) {
+          tc_fence_after();
+          const bool two = !wide && n > 1;
+          const int64_t tok = w.q.s0 + token, head = (int64_t)hk * plan.G + g;
+          const bool whole = w.whole();
+          const float inv = lt == 0.f ? 0.f : whole ? 1.f / lt : 1.f;
+          const float a0 = l == 0.f ? 0.f : f0 * inv, a1 = f1 * inv;
+          T* o = static_cast<T*>(p.o) + (tok * p.H + head) * p.DV;
+          const int64_t prow = (int64_t)w.slot((int)blockIdx.x) * 256 + (wide ? s * 128 : 0) + r;
+          float* part = p.parts.out + prow * DP;
+#pragma unroll 1
+          for (int c0 = 0; c0 < DP; c0 += 32) {
+            uint32_t x[32];
+            tmem_ld32(tO + c0, x);
+            tmem_ld_wait(x);
+            // (a factor of zero drops what the columns hold, NaN too)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = a0 == 0.f ? 0u : __float_as_uint(__uint_as_float(x[e]) * a0);
+            if (two) {
+              uint32_t y[32];
+              tmem_ld32(tO + DP + c0, y);
+              tmem_ld_wait(y);
+              if (a1 != 0.f) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  x[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), a1, __uint_as_float(x[e])));
+              }
+            }
+            if (!row_ok) continue;
+            if (whole) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+                if (c0 + e < p.DV)
+                  *reinterpret_cast<uint4*>(o + c0 + e) =
+                      make_uint4(pack2<F16>(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                                 pack2<F16>(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])),
+                                 pack2<F16>(__uint_as_float(x[e + 4]), __uint_as_float(x[e + 5])),
+                                 pack2<F16>(__uint_as_float(x[e + 6]), __uint_as_float(x[e + 7])));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<uint4*>(part + c0 + e) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            }
+          }
+          if (row_ok) {
+            if (!whole)
+              p.parts.ml[prow] = make_float2(mt, lt);
+            else if (p.lse != nullptr)
+              p.lse[head * plan.T + tok] = lt == 0.f ? INFINITY : (mt + log2f(lt)) * kLn2;
+          }
+          tc_fence_before();
+        }
+        if (!wide) mbar_arrive(bar(B_MD));
+      }
+      more = w.next(plan);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tm, 512);
+  }
+}
+
+int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
+
+bool make_map(CUtensorMap* map, bool f16, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+              const cuuint32_t* box) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (!enc) return false;
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+             const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int padded_width(const PagedProblem& pr) { return (pr.DK > pr.DV ? pr.DK : pr.DV) <= 64 ? 64 : 128; }
+
+PagedPlan plan_of(const PagedProblem& pr) {
+  PagedPlan p{};
+  p.starts = pr.starts;
+  p.lens = pr.lens;
+  p.B = pr.B;
+  p.T = pr.T;
+  const int64_t most = pr.max_pages * pr.page;
+  p.max_keys = most < 2147483647ll - 256 ? most : 2147483647ll - 256;  // (lengths are 32-bit)
+  p.causal = pr.causal;
+  p.G = (int)(pr.H / pr.Hkv);
+  p.gw = p.G < 128 ? p.G : 128;
+  p.gblocks = (p.G + p.gw - 1) / p.gw;
+  p.heads = (int)pr.Hkv * p.gblocks;
+  p.nt = 128 / p.gw;
+  p.tiles = 2;
+  p.kt = 128;
+  return p;
+}
+
+template <int DP, bool F16>
+cudaError_t launch_d(const PagedProblem& pr, int sms, cudaStream_t s) {
+  using C = PCfg<DP>;
+  using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
+  TcParams p;
+  p.plan = plan_of(pr);
+  p.parts = paged_parts(pr.workspace, 256, DP);
+  p.table = pr.table;
+  p.max_pages = pr.max_pages;
+  p.pages = pr.pages;
+  p.page = (int)pr.page;
+  p.box = gcd((int)pr.page, 128);
+  p.H = (int)pr.H;
+  p.DV = (int)pr.DV;
+  p.scale = pr.scale;
+  p.o = pr.o;
+  p.lse = pr.lse;
+  CUtensorMap mq, mk, mv;
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)pr.DK, (cuuint64_t)pr.H, (cuuint64_t)pr.T};
+    const cuuint64_t str[2] = {(cuuint64_t)pr.DK * 2, (cuuint64_t)(pr.H * pr.DK) * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.plan.gw, (cuuint32_t)p.plan.nt};
+    if (!make_map(&mq, F16, 3, pr.q, dims, str, box)) return cudaErrorInvalidValue;
+  }
+  for (int v = 0; v < 2; ++v) {
+    const cuuint64_t D = (cuuint64_t)(v ? pr.DV : pr.DK);
+    const cuuint64_t dims[4] = {D, (cuuint64_t)pr.page, (cuuint64_t)pr.Hkv, (cuuint64_t)pr.pages};
+    const cuuint64_t str[3] = {D * 2, (cuuint64_t)pr.page * D * 2, (cuuint64_t)(pr.Hkv * pr.page) * D * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)p.box, 1, 1};
+    if (!make_map(v ? &mv : &mk, F16, 4, v ? pr.v : pr.k, dims, str, box)) return cudaErrorInvalidValue;
+  }
+  // no more CTAs than there can be pieces of one key tile
+  const int64_t units = (pr.T / (2 * p.plan.nt) + pr.B) * p.plan.heads;
+  const int64_t tiles = (p.plan.max_keys + 127) / 128 * 2;
+  int grid = sms < kPagedMaxGrid ? sms : kPagedMaxGrid;
+  if (units < grid && tiles < grid && units * tiles < grid) grid = (int)(units * tiles);
+  cudaError_t err =
+      cudaFuncSetAttribute(paged_tc_kernel<DP, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (err != cudaSuccess) return err;
+  paged_tc_kernel<DP, F16><<<(unsigned)grid, kThreads, C::SMEM, s>>>(mq, mk, mv, p);
+  err = cudaPeekAtLastError();
+  if (err != cudaSuccess) return err;
+  return launch_combine<T>(p.plan, p.parts, grid, (int)pr.DV, (int)pr.H, static_cast<T*>(pr.o), pr.lse, s);
+}
+
+}  // namespace
+
+bool paged_tc_supported(const PagedProblem& p) {
+  if (p.dtype != FAB_BF16 && p.dtype != FAB_F16) return false;
+  // rows of whole 16-byte pieces, boxes of whole swizzle groups of 8 rows
+  if (p.DK % 8 != 0 || p.DV % 8 != 0 || p.DK > 128 || p.DV > 128 || p.page % 8 != 0) return false;
+  // what a tensor map can describe
+  const int64_t D = p.DK > p.DV ? p.DK : p.DV, lim = int64_t(1) << 40;
+  return p.Hkv * p.page * D * 2 < lim && p.H * p.DK * 2 < lim && p.H < (1ll << 31);
+}
+
+size_t paged_tc_workspace_bytes(const PagedProblem& p) { return paged_parts_bytes(256, padded_width(p)); }
+
+cudaError_t launch_paged_tc(const PagedProblem& p, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return cudaErrorInvalidValue;
+  if (padded_width(p) == 128)
+    return p.dtype == FAB_F16 ? launch_d<128, true>(p, sms, s) : launch_d<128, false>(p, sms, s);
+  return p.dtype == FAB_F16 ? launch_d<64, true>(p, sms, s) : launch_d<64, false>(p, sms, s);
+}
+
+uint32_t take_error_paged_tc() {
+  uint32_t v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_err_paged_tc, sizeof(v)) != cudaSuccess) return 0;
+  if (v) cudaMemcpyToSymbol(g_err_paged_tc, &z, sizeof(z));
+  return v;
+}
+
+}  // namespace fab
