@@ -5,9 +5,9 @@
 // A tile is `nt` tokens times `gw` query heads of one key/value head (a row
 // per pair); a unit is one tile or two (consecutive tokens) and walks its key
 // tiles.  Units in order of (sequence, head, tokens) form one line, each as
-// long as its key tiles times its tiles, and CTA c of G takes the piece from
-// W c / G to W (c+1) / G of that line, so every CTA has the same work
-// whatever the lengths are.  A unit cut by a border leaves unnormalised
+// long as its key tiles (and kPagedLead more for its start and end) times its
+// tiles, and CTA c of G takes the piece from W c / G to W (c+1) / G of that
+// line, so every CTA has the same work whatever the lengths are.  A unit cut by a border leaves unnormalised
 // partial results (output, maximum, sum) in the workspace, at most two to a
 // CTA, which paged_combine_kernel joins.
 #pragma once
@@ -17,6 +17,7 @@
 
 namespace fab {
 
+constexpr int kPagedLead = 2;  // what starting and ending a unit costs, in key tiles
 constexpr int kPagedMaxGrid = 304;  // CTAs that the workspace has room for
 
 // What planning needs to know.
@@ -78,33 +79,67 @@ struct PagedShared {
   PagedPlace at;
 };
 
-// Where CTA c's piece begins.
-FAB_DEV int64_t paged_border(int64_t W, int G, int c) {
-  const int64_t q = W / G;
-  return q * c + (int64_t)((uint32_t)((int)(W - q * G) * c) / (uint32_t)G);
+// Length on the line of unit i.
+FAB_DEV int paged_length(const PagedPlan& p, const PagedSeq& q, int i) {
+  return paged_width(p, q, i) * (paged_key_tiles(p, q, i) + kPagedLead);
 }
 
-// The line's length in s->total.  Called by the whole block (NT threads).
+// Length on the line of one head of the sequence of each lane; whole warps.
+FAB_DEV int64_t paged_head_length(const PagedPlan& p, const PagedSeq& q) {
+  const int units = paged_units(p, q);
+  int64_t len = 0;
+  if (units <= 2) {
+    for (int i = 0; i < units; ++i) len += paged_length(p, q, i);
+  }
+  // the lanes of a warp share the longer ones' units
+  for (unsigned left = __ballot_sync(0xffffffffu, units > 2); left != 0; left &= left - 1) {
+    const int src = __ffs((int)left) - 1;
+    PagedSeq x;
+    x.s0 = 0;
+    x.n = __shfl_sync(0xffffffffu, q.n, src);
+    x.last0 = __shfl_sync(0xffffffffu, q.last0, src);
+    x.len = __shfl_sync(0xffffffffu, q.len, src);
+    int64_t sum = 0;
+    for (int i = (int)lane_id(), k = paged_units(p, x); i < k; i += 32) sum += paged_length(p, x, i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((int)lane_id() == src) len = sum;
+  }
+  return len;
+}
+
+// Where CTAs' pieces begin.
+struct PagedBorders {
+  int64_t q;
+  uint32_t r, G;
+  FAB_DEV PagedBorders(int64_t W, int grid) {
+    G = (uint32_t)grid;
+    q = W < (int64_t(1) << 32) ? (int64_t)((uint32_t)W / G) : W / grid;
+    r = (uint32_t)(W - q * grid);
+  }
+  FAB_DEV int64_t operator()(int c) const { return q * c + (int64_t)(r * (uint32_t)c / G); }
+};
+
+// The line's length in s->total.  Called by the whole block (NT threads); `mine`
+// gets the length of a head of sequence threadIdx.x.
 template <int NT>
 FAB_DEV void paged_total(const PagedPlan& p, PagedShared* s, int64_t* mine) {
-  int64_t sum = 0, one = 0;
-  for (int64_t b = threadIdx.x; b < p.B; b += NT) {
-    const PagedSeq q = paged_seq(p, (int)b);
-    one = 0;
-    for (int i = 0, k = paged_units(p, q); i < k; ++i) one += paged_width(p, q, i) * paged_key_tiles(p, q, i);
-    one *= p.heads;
-    sum += one;
+  int64_t sum = 0;
+  for (int64_t b0 = 0; b0 < p.B; b0 += NT) {
+    const int64_t b = b0 + threadIdx.x;
+    PagedSeq q{0, 0, 0, 0};
+    if (b < p.B) q = paged_seq(p, (int)b);
+    const int64_t one = paged_head_length(p, q);
+    if (b0 == 0) *mine = one;
+    sum += one * p.heads;
   }
-  *mine = one;  // (of use where B <= NT: then the only one)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if ((threadIdx.x & 31) == 0) s->sums[threadIdx.x >> 5] = sum;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int64_t w = 0;
-    for (int i = 0; i < NT / 32; ++i) w += s->sums[i];
-    s->total = w;
-  }
+  int64_t w = 0;
+  for (int i = 0; i < NT / 32; ++i) w += s->sums[i];
+  if (threadIdx.x == 0) s->total = w;
   __syncthreads();
 }
 
@@ -116,15 +151,13 @@ FAB_DEV void paged_locate(const PagedPlan& p, PagedShared* s, int64_t mine, int6
   for (int64_t b0 = 0; b0 < p.B; b0 += NT) {
     const int64_t b = b0 + threadIdx.x;
     int64_t one = mine;
-    if (p.B > NT) {
-      one = 0;
-      if (b < p.B) {
-        const PagedSeq q = paged_seq(p, (int)b);
-        for (int i = 0, k = paged_units(p, q); i < k; ++i) one += paged_width(p, q, i) * paged_key_tiles(p, q, i);
-        one *= p.heads;
-      }
+    if (b0 > 0) {
+      PagedSeq q{0, 0, 0, 0};
+      if (b < p.B) q = paged_seq(p, (int)b);
+      one = paged_head_length(p, q);
     }
-    int64_t incl = one;
+    const int64_t all = one * p.heads;
+    int64_t incl = all;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
@@ -133,25 +166,47 @@ FAB_DEV void paged_locate(const PagedPlan& p, PagedShared* s, int64_t mine, int6
     if (lane == 31) s->sums[warp] = incl;
     __syncthreads();
     int64_t before = base;
-    for (int i = 0; i < warp; ++i) before += s->sums[i];
-    const int64_t first = before + incl - one;
-    if (one > 0 && pos >= first && pos < first + one) {
-      const PagedSeq q = paged_seq(p, (int)b);
-      const int64_t head_len = one / p.heads;
-      PagedPlace at;
-      at.b = (int)b;
-      at.head = (int)((pos - first) / head_len);
-      at.u0 = first + at.head * head_len;
-      at.i = 0;
-      for (;;) {
-        const int64_t len = paged_width(p, q, at.i) * (int64_t)paged_key_tiles(p, q, at.i);
-        if (pos < at.u0 + len) break;
-        at.u0 += len;
-        ++at.i;
-      }
-      s->at = at;
+    for (int i = 0; i < NT / 32; ++i) {
+      if (i < warp) before += s->sums[i];
+      base += s->sums[i];
     }
-    for (int i = 0; i < NT / 32; ++i) base += s->sums[i];
+    const int64_t first = before + incl - all;
+    const unsigned hit = __ballot_sync(0xffffffffu, all > 0 && pos >= first && pos < first + all);
+    if (hit != 0) {  // in this warp: its lanes look for the unit together
+      const int src = __ffs((int)hit) - 1;
+      const int64_t f = __shfl_sync(0xffffffffu, first, src), head_len = __shfl_sync(0xffffffffu, one, src);
+      const int bb = (int)(b0 + warp * 32 + src);
+      const PagedSeq q = paged_seq(p, bb);
+      int64_t d = pos - f;
+      const int head = d < (int64_t(1) << 32) && head_len < (int64_t(1) << 32)
+                           ? (int)((uint32_t)d / (uint32_t)head_len)
+                           : (int)(d / head_len);
+      int64_t u0 = f + head * head_len;
+      for (int i0 = 0;; i0 += 32) {
+        const int64_t len = i0 + lane < paged_units(p, q) ? paged_length(p, q, i0 + lane) : 0;
+        int64_t end = len;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t up = __shfl_up_sync(0xffffffffu, end, o);
+          if (lane >= o) end += up;
+        }
+        const unsigned in = __ballot_sync(0xffffffffu, pos < u0 + end);
+        if (in != 0) {
+          if (lane == __ffs((int)in) - 1) {
+            s->at.b = bb;
+            s->at.head = head;
+            s->at.i = i0 + lane;
+            s->at.u0 = u0 + end - len;
+          }
+          break;
+        }
+        if (i0 >= paged_units(p, q)) {  // only if the lengths changed under the kernel
+          s->at = PagedPlace{bb, head, 0, u0};
+          break;
+        }
+        u0 += __shfl_sync(0xffffffffu, end, 31);
+      }
+    }
     __syncthreads();
     if (base > pos) break;
   }
@@ -177,12 +232,12 @@ struct PagedWalk {
   }
   // Key tiles of the present unit before `pos` on the line.
   FAB_DEV int tiles_before(int64_t pos) const {
-    const int64_t d = pos - at.u0;
+    const int64_t d = pos - at.u0 - width * kPagedLead;
     if (d <= 0) return 0;
     const int64_t t = width == 2 ? (d + 1) >> 1 : d;
     return t < ntiles ? (int)t : ntiles;
   }
-  // The part of the piece [p0, p1) that lies in the present unit; false past the piece.
+  // The part of the piece [p0, p1) that lies in the present unit.
   FAB_DEV bool piece(int64_t p0, int64_t p1) {
     if (at.u0 >= p1) return false;
     j0 = tiles_before(p0);
@@ -191,7 +246,7 @@ struct PagedWalk {
   }
   // The next unit (its j0, j1 are not set); false at the end of the line.
   FAB_DEV bool next(const PagedPlan& p) {
-    at.u0 += (int64_t)width * ntiles;
+    at.u0 += (int64_t)width * (ntiles + kPagedLead);
     if (++at.i == units) {
       at.i = 0;
       if (++at.head == p.heads) {
@@ -205,6 +260,14 @@ struct PagedWalk {
     }
     load(p);
     return true;
+  }
+  // From the present unit on, the first with key tiles in the piece; false past the piece.
+  FAB_DEV bool seek(const PagedPlan& p, int64_t p0, int64_t p1) {
+    for (;;) {
+      if (!piece(p0, p1)) return false;
+      if (j0 < j1) return true;
+      if (!next(p)) return false;
+    }
   }
   FAB_DEV bool whole() const { return j0 == 0 && j1 == ntiles; }
   // The piece's partial slot: 2c for a unit that began before it, else 2c + 1.
@@ -247,7 +310,8 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
   paged_total<kCombineThreads>(p, &sh, &mine);
   const int64_t W = sh.total;
   const int c = (int)blockIdx.x;
-  const int64_t p0 = paged_border(W, grid, c), p1 = paged_border(W, grid, c + 1);
+  const PagedBorders border(W, grid);
+  const int64_t p0 = border(c), p1 = border(c + 1);
   if (p1 < W && p1 > p0) paged_locate<kCombineThreads>(p, &sh, mine, p1);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (p1 >= W || p1 <= p0) return;
@@ -255,13 +319,13 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
   w.begin(p, sh.at);
   // not cut here, or the first part is an earlier CTA's
   const int mine_tiles = w.tiles_before(p1);
-  if (mine_tiles == 0 || mine_tiles == w.ntiles || p0 > w.at.u0) return;
+  if (mine_tiles == 0 || mine_tiles == w.ntiles || w.tiles_before(p0) > 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // CTAs c .. ce hold the unit's parts
   int ce = c;
   for (int base = c + 1;; base += 32) {
     const int x = base + lane;
-    const bool done = x >= grid - 1 || w.tiles_before(paged_border(W, grid, x + 1)) >= w.ntiles;
+    const bool done = x >= grid - 1 || w.tiles_before(border(x + 1)) >= w.ntiles;
     const unsigned v = __ballot_sync(0xffffffffu, done);
     if (v != 0) {
       ce = base + __ffs((int)v) - 1;
@@ -280,8 +344,8 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
     auto part_ml = [&](int k) {
       float2 ml = make_float2(-INFINITY, 0.f);
       if (k <= ce) {
-        const int a = k == c ? 0 : w.tiles_before(paged_border(W, grid, k));
-        const int b = w.tiles_before(paged_border(W, grid, k + 1));
+        const int a = k == c ? 0 : w.tiles_before(border(k));
+        const int b = w.tiles_before(border(k + 1));
         if (a < b) ml = parts.ml[(int64_t)(k == c ? 2 * k + 1 : 2 * k) * parts.rows + row];
       }
       return ml;
@@ -335,7 +399,7 @@ cudaError_t launch_combine(const PagedPlan& plan, const PagedParts& parts, int g
   if (grid < 2) return cudaSuccess;  // nothing is cut
   const int rows = plan.tiles * plan.nt * plan.gw;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)((rows + 31) / 32));
+  cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)((rows + 63) / 64));
   cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = s;
   cudaLaunchAttribute at{};

@@ -77,15 +77,15 @@ enum : int {
   B_KE = 4,   // + slot: K free
   B_VF = 8,   // + slot: V landed
   B_VE = 12,  // + slot: V free
-  B_QF = 16,  // a unit's Q landed
-  B_QE = 17,  // a unit's S products finished
-  B_S = 18,   // + stream: S landed (and every product issued before it)
-  B_P = 20,   // + stream: P written (and O rescaled where it had to be)
-  B_O = 22,   // + stream: the unit's last product of the stream finished
-  B_ML = 24,  // one-tile units: stream 1's maxima and sums are in shared memory
-  B_MD = 25,  // one-tile units: stream 0 has read stream 1's output
-  B_FIN = 26,
-  B_COUNT = 27
+  B_QF = 16,  // + slot: Q landed
+  B_QE = 18,  // + slot: Q free
+  B_S = 20,   // + stream: S landed (and every product issued before it)
+  B_P = 22,   // + stream: P written (and O rescaled where it had to be)
+  B_O = 24,   // + stream: the unit's last product of the stream finished
+  B_ML = 26,  // one-tile units: stream 1's maxima and sums are in shared memory
+  B_MD = 27,  // one-tile units: stream 0 has read stream 1's output
+  B_FIN = 28,
+  B_COUNT = 29
 };
 
 struct TcParams {
@@ -132,9 +132,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(B_VF + s), 1);
       mbar_init(bar(B_VE + s), 1);
     }
-    mbar_init(bar(B_QF), 1);
-    mbar_init(bar(B_QE), 1);
     for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(B_QF + s), 1);
+      mbar_init(bar(B_QE + s), 1);
       mbar_init(bar(B_S + s), 1);
       mbar_init(bar(B_P + s), 4);
       mbar_init(bar(B_O + s), 1);
@@ -155,8 +155,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t mine;
   paged_total<kThreads>(plan, sh, &mine);
   const int64_t W = sh->total;
-  const int64_t p0 = paged_border(W, (int)gridDim.x, (int)blockIdx.x);
-  const int64_t p1 = paged_border(W, (int)gridDim.x, (int)blockIdx.x + 1);
+  const PagedBorders border(W, (int)gridDim.x);
+  const int64_t p0 = border((int)blockIdx.x), p1 = border((int)blockIdx.x + 1);
   if (p0 < p1) paged_locate<kThreads>(plan, sh, mine, p0);
   tc_fence_before();
   __syncthreads();
@@ -177,143 +177,188 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int full = keys ? B_KF : B_VF, empty = keys ? B_KE : B_VE, slots = keys ? C::NK : C::NV;
       const uint32_t ring = sbase + (keys ? C::OFF_K : C::OFF_V);
       const CUtensorMap* map = keys ? &tmK : &tmV;
-      int slot = 0, phase = 1, units = 0;
+      int slot = 0, phase = 1, qslot = 0, qphase = 1;
       bool ok = true;
       PagedWalk w;
       w.begin(plan, start);
-      bool more = true;
-      while (ok && more && w.piece(p0, p1)) {
-        if (w.j0 < w.j1) {
-          const int hk = w.at.head / plan.gblocks;
-          // page of box `lane` of key tile j, and how many boxes hold keys
-          auto lookup = [&](int j, int& row) {
-            const uint32_t m = (uint32_t)j * 128u + (uint32_t)(lane * p.box);
-            const uint32_t at = m / (uint32_t)p.page;
-            row = (int)(m - at * (uint32_t)p.page);
-            if (lane * p.box >= 128 || m >= (uint32_t)w.q.len) return 0;
-            const int page = __ldg(p.table + (int64_t)w.at.b * p.max_pages + at);
-            // (out of range: the copy fills zeros, the call is reported)
-            if (page < 0 || page >= p.pages) atomicOr(err, kErrIndex);
-            return page;
-          };
-          int row, page = lookup(w.j0, row);
-          if (keys) {
-            if (plan.lens[w.at.b] > plan.max_keys && lane == 0) atomicOr(err, kErrIndex);
-            if (units > 0 && !(ok = mbar_wait(bar(B_QE), (units - 1) & 1, abort_flag, err))) break;
+      for (bool more = w.seek(plan, p0, p1); ok && more; more = w.next(plan) && w.seek(plan, p0, p1)) {
+        const int hk = w.at.head / plan.gblocks;
+        // page of box `lane` of key tile j, and its first row there
+        auto lookup = [&](int j, int& row) {
+          const uint32_t m = (uint32_t)j * 128u + (uint32_t)(lane * p.box);
+          const uint32_t at = m / (uint32_t)p.page;
+          row = (int)(m - at * (uint32_t)p.page);
+          if (lane * p.box >= 128 || m >= (uint32_t)w.q.len) return 0;
+          const int page = __ldg(p.table + (int64_t)w.at.b * p.max_pages + at);
+          // (out of range: the copy fills zeros, the call is reported)
+          if (page < 0 || page >= p.pages) atomicOr(err, kErrIndex);
+          return page;
+        };
+        int row, page = lookup(w.j0, row);
+        if (keys) {
+          if (lane == 0 && plan.lens[w.at.b] > plan.max_keys) atomicOr(err, kErrIndex);
+          const int head = hk * plan.G + (w.at.head - hk * plan.gblocks) * plan.gw;
+          for (int s = 0; s < w.width; ++s) {
+            if (!(ok = mbar_wait(bar(B_QE + qslot), qphase, abort_flag, err))) break;
             if (lane == 0) {
-              const uint32_t bytes = (uint32_t)(64 * 2 * plan.gw * plan.nt * C::ATOMS);
-              mbar_arrive_expect_tx(bar(B_QF), bytes * w.width);
-              const int head = hk * plan.G + (w.at.head - hk * plan.gblocks) * plan.gw;
-              for (int s = 0; s < w.width; ++s)
-                for (int a = 0; a < C::ATOMS; ++a)
-                  tma_load_3d(sbase + C::OFF_Q + s * C::TILE + a * C::ATOM, &tmQ, bar(B_QF), a * 64, head,
-                              w.q.s0 + w.at.i * plan.nt * 2 + s * plan.nt);
-            }
-            ++units;
-          }
-          for (int j = w.j0; j < w.j1; ++j) {
-            if (!(ok = mbar_wait(bar(empty + slot), phase, abort_flag, err))) break;
-            const int held = w.q.len - j * 128;  // keys of the tile and beyond
-            const int boxes = held <= 0 ? 0 : held >= 128 ? 128 / p.box : (held + p.box - 1) / p.box;
-            fence_proxy_async_smem();
-            if (lane == 0) mbar_arrive_expect_tx(bar(full + slot), (uint32_t)(boxes * p.box * 128 * C::ATOMS));
-            __syncwarp();
-            if (lane < boxes) {
-              const uint32_t dst = ring + slot * C::TILE + lane * p.box * 128;
-#pragma unroll
+              mbar_arrive_expect_tx(bar(B_QF + qslot), (uint32_t)(64 * 2 * plan.gw * plan.nt * C::ATOMS));
               for (int a = 0; a < C::ATOMS; ++a)
-                tma_load_4d(dst + a * C::ATOM, map, bar(full + slot), a * 64, row, hk, page);
+                tma_load_3d(sbase + C::OFF_Q + qslot * C::TILE + a * C::ATOM, &tmQ, bar(B_QF + qslot), a * 64, head,
+                            w.q.s0 + w.at.i * plan.nt * 2 + s * plan.nt);
             }
-            if (++slot == slots) slot = 0, phase ^= 1;
-            if (j + 1 < w.j1) page = lookup(j + 1, row);
+            if (++qslot == 2) qslot = 0, qphase ^= 1;
           }
+          if (!ok) break;
         }
-        more = w.next(plan);
+        for (int j = w.j0; j < w.j1; ++j) {
+          if (!(ok = mbar_wait(bar(empty + slot), phase, abort_flag, err))) break;
+          const int held = w.q.len - j * 128;  // keys of the tile and beyond
+          const int boxes = held <= 0 ? 0 : held >= 128 ? 128 / p.box : (held + p.box - 1) / p.box;
+          fence_proxy_async_smem();
+          if (lane == 0) mbar_arrive_expect_tx(bar(full + slot), (uint32_t)(boxes * p.box * 128 * C::ATOMS));
+          __syncwarp();
+          if (lane < boxes) {
+            const uint32_t dst = ring + slot * C::TILE + lane * p.box * 128;
+#pragma unroll
+            for (int a = 0; a < C::ATOMS; ++a)
+              tma_load_4d(dst + a * C::ATOM, map, bar(full + slot), a * 64, row, hk, page);
+          }
+          if (++slot == slots) slot = 0, phase ^= 1;
+          if (j + 1 < w.j1) page = lookup(j + 1, row);
+        }
       }
-      // let the copies in flight land before shared memory goes
+      // after a failed wait, let the copies in flight land before shared memory goes
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok && lane == 0 && keys && units > 0) mbar_drain(bar(B_QF), (units - 1) & 1);
-      if (!ok && lane == 0)
+      if (!ok && lane == 0) {
         for (int s = 0; s < slots; ++s) mbar_drain(bar(full + s), s < slot ? phase ^ 1 : phase);
+        if (keys)
+          for (int s = 0; s < 2; ++s) mbar_drain(bar(B_QF + s), s < qslot ? qphase ^ 1 : qphase);
+      }
     } else if (any && warp == 1) {
       // ------------------------------------------------------------ products
-      // Step i of a unit belongs to stream i & 1.  S(i + 2) is issued behind
-      // O += P(i) V, which frees its columns (matrix instructions of a CTA run
-      // in the order of their issue).
+      // Step i of a unit belongs to stream i & 1.  A stream's next S is issued
+      // once O += P V of its last one is, which frees the columns (a CTA's
+      // matrix instructions run in the order of their issue): S products run
+      // two steps ahead, into the next unit too where its operands have
+      // landed, so that a unit's end leaves the tensor core with work.
+      // Everything that decides what is issued is made warp-uniform where it
+      // is read, once a unit, so that descriptors and slots stay in uniform
+      // registers (from ordinary ones the issue of a step's 16 instructions
+      // took 2000 cycles instead of the 1024 that they run for).
       const uint32_t issue = lane == 0 ? 1u : 0u;
       constexpr uint32_t ID_S = idesc_16(128, 128, false, false, F16);
       constexpr uint32_t ID_PV = idesc_16(128, DP, false, true, F16);
+      constexpr uint32_t HI = sdesc_hi_sw128(1024);
       auto wall = [&](int i, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort_flag, err));
       };
-      int kslot = 0, kphase = 0, vslot = 0, vphase = 0, units = 0;
-      uint32_t pphase[2] = {0, 0};
-      bool ok = true, more = true;
-      PagedWalk w;
-      w.begin(plan, start);
-      while (ok && more && w.piece(p0, p1)) {
-        if (w.j0 < w.j1) {
-          const bool wide = w.width == 2;
-          const int steps = (w.j1 - w.j0) * w.width;
-          auto issue_s = [&](int i) {
-            const int s = i & 1;
-            if (!wide || s == 0) ok = wall(B_KF + kslot, kphase);
-            if (!ok) return;
-            tc_fence_after();
-            const uint32_t sQ = sbase + C::OFF_Q + (wide && s ? C::TILE : 0u), sK = sbase + C::OFF_K + kslot * C::TILE;
-#pragma unroll
-            for (int kk = 0; kk < DP / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * C::ATOM + (kk & 3) * 32;
-              mma_ss(tm + C::TM_S + s * 128, sdesc_sw128(sQ + off, 16, 1024), sdesc_sw128(sK + off, 16, 1024), ID_S,
-                     kk > 0, issue);
-            }
-            mma_commit(bar(B_S + s), issue);
-            if (!wide || s == 1) {
-              mma_commit(bar(B_KE + kslot), issue);
-              if (++kslot == C::NK) kslot = 0, kphase ^= 1;
-            }
-            if (i == steps - 1) mma_commit(bar(B_QE), issue);
-          };
-          if (!(ok = wall(B_QF, units & 1))) break;
-          ++units;
-          issue_s(0);
-          if (ok && steps > 1) issue_s(1);
-          for (int i = 0; ok && i < steps; ++i) {
-            const int s = i & 1;
-            const int j = w.j0 + (wide ? i >> 1 : i);
-            const uint32_t sV = sbase + C::OFF_V + vslot * C::TILE;
-            int ksteps = 8;
-            if (!wide || s == 0) {
-              if (!(ok = wall(B_VF + vslot, vphase))) break;
-            }
-            const int held = w.q.len - j * 128;
-            if (held < 128) {
-              // the last keys' tile: products over whole 16-key steps, the
-              // rows between the last key and the step's end zeroed
-              const int live = held < 0 ? 0 : held;
-              ksteps = live == 0 ? 1 : (live + 15) / 16;
-              if (!wide || s == 0) {
-                for (int x = live * 8 + lane; x < ksteps * 128; x += 32)
-#pragma unroll
-                  for (int a = 0; a < C::ATOMS; ++a) st_shared_v4(sV + a * C::ATOM + x * 16, 0u, 0u, 0u, 0u);
-                fence_proxy_async_smem();
-                __syncwarp();
-              }
-            }
-            if (!(ok = wall(B_P + s, pphase[s]))) break;
-            pphase[s] ^= 1;
-            tc_fence_after();
-            for (int kk = 0; kk < ksteps; ++kk)
-              mma_ts(tm + C::TM_O + s * DP, tm + C::TM_S + s * 128 + kk * 8, sdesc_sw128(sV + kk * 2048, C::ATOM, 1024),
-                     ID_PV, (i >= 2 || kk > 0) ? 1u : 0u, issue);
-            if (!wide || s == 1) {
-              mma_commit(bar(B_VE + vslot), issue);
-              if (++vslot == C::NV) vslot = 0, vphase ^= 1;
-            }
-            if (i + 2 < steps) issue_s(i + 2); else mma_commit(bar(B_O + s), issue);
-          }
+      struct Part {  // a unit's part of the piece, uniform
+        uint32_t wide, steps, last_held;  // last_held: keys from its last key tile on
+      };
+      auto part_of = [&](const PagedWalk& x) {
+        Part y;
+        y.wide = uniform(x.width == 2 ? 1u : 0u);
+        y.steps = uniform((uint32_t)((x.j1 - x.j0) * x.width));
+        const int held = x.q.len - (x.j1 - 1) * 128;
+        y.last_held = uniform(held < 0 ? 0u : (uint32_t)held);
+        return y;
+      };
+      const uint32_t tmu = uniform(tm), sbu = uniform(sbase);
+      const uint32_t q_lo = sdesc_lo(sbu + C::OFF_Q, 16), k_lo = sdesc_lo(sbu + C::OFF_K, 16);
+      const uint32_t v_lo = sdesc_lo(sbu + C::OFF_V, C::ATOM);
+      uint32_t kslot = 0, kphase = 0, vslot = 0, vphase = 0, qslot = 0, qphase = 0, pphase = 0, busy = 0;
+      bool ok = true;
+      PagedWalk ws, w;  // of the S products, of the products with V
+      ws.begin(plan, start);
+      bool smore = __all_sync(0xffffffffu, ws.seek(plan, p0, p1));
+      w = ws;
+      Part sp = part_of(ws);
+      uint32_t si = 0, ahead = 0;  // ahead: the S products are in a later unit
+      auto issue_s = [&]() {
+        const uint32_t s = si & 1u;
+        const uint32_t qs = sp.wide ? qslot ^ s : qslot;
+        if (si <= sp.wide) {
+          if (!(ok = wall(B_QF + qs, (qphase >> qs) & 1u))) return;
+          qphase ^= 1u << qs;
         }
-        more = w.next(plan);
+        if (!sp.wide || s == 0) {
+          if (!(ok = wall(B_KF + kslot, kphase))) return;
+        }
+        tc_fence_after();
+        const uint32_t a_lo = q_lo + qs * (C::TILE >> 4), b_lo = k_lo + kslot * (C::TILE >> 4);
+        const uint32_t d = tmu + C::TM_S + s * 128;
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * C::ATOM + (kk & 3) * 32) >> 4;
+          mma_ss_lo(d, a_lo + off, b_lo + off, HI, ID_S, kk > 0, issue);
+        }
+        mma_commit(bar(B_S + s), issue);
+        if (!sp.wide || s == 1) {
+          mma_commit(bar(B_KE + kslot), issue);
+          if (++kslot == C::NK) kslot = 0, kphase ^= 1;
+        }
+        if (si + 1 + sp.wide >= sp.steps) mma_commit(bar(B_QE + qs), issue);
+        busy |= 1u << s;
+        if (++si == sp.steps) {
+          si = 0;
+          qslot ^= 1u ^ sp.wide;
+          smore = __all_sync(0xffffffffu, ws.next(plan) && ws.seek(plan, p0, p1));
+          if (smore) sp = part_of(ws);
+          ++ahead;
+        }
+      };
+      for (bool more = smore; ok && more;
+           more = __all_sync(0xffffffffu, w.next(plan) && w.seek(plan, p0, p1)), --ahead) {
+        const Part pv = part_of(w);
+        for (uint32_t i = 0; ok && i < pv.steps; ++i) {
+          const uint32_t s = i & 1u;
+          while (ok && smore && !((busy >> (si & 1u)) & 1u)) {
+            // another unit's operands are waited for only when nothing else is left to do
+            if (busy != 0 && ahead != 0 && si < 2) {
+              const uint32_t qs = sp.wide ? qslot ^ si : qslot;
+              const bool here = (si > sp.wide || mbar_test(bar(B_QF + qs), (qphase >> qs) & 1u)) &&
+                                ((sp.wide && si == 1) || mbar_test(bar(B_KF + kslot), kphase));
+              if (!__all_sync(0xffffffffu, here)) break;
+            }
+            issue_s();
+          }
+          if (!ok) break;
+          const bool tail = pv.last_held < 128 && i + 1 + pv.wide >= pv.steps;
+          if (!pv.wide || s == 0) {
+            if (!(ok = wall(B_VF + vslot, vphase))) break;
+            if (tail) {
+              // the last keys' tile: the products below run over whole steps
+              // of 16 keys, the rows from the last key to the step's end zeroed
+              const uint32_t end = pv.last_held == 0 ? 16 : (pv.last_held + 15) / 16 * 16;
+              for (uint32_t x = pv.last_held * 8 + lane; x < end * 8; x += 32)
+#pragma unroll
+                for (int a = 0; a < C::ATOMS; ++a)
+                  st_shared_v4(sbu + C::OFF_V + vslot * C::TILE + a * C::ATOM + x * 16, 0u, 0u, 0u, 0u);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
+          if (!(ok = wall(B_P + s, (pphase >> s) & 1u))) break;
+          pphase ^= 1u << s;
+          tc_fence_after();
+          const uint32_t d = tmu + C::TM_O + s * DP, a = tmu + C::TM_S + s * 128;
+          const uint32_t b_lo = v_lo + vslot * (C::TILE >> 4);
+          if (!tail) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts_lo(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, (i >= 2 || kk > 0) ? 1u : 0u, issue);
+          } else {
+            const uint32_t ksteps = pv.last_held == 0 ? 1 : (pv.last_held + 15) / 16;
+            for (uint32_t kk = 0; kk < ksteps; ++kk)
+              mma_ts_lo(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, (i >= 2 || kk > 0) ? 1u : 0u, issue);
+          }
+          if (!pv.wide || s == 1) {
+            mma_commit(bar(B_VE + vslot), issue);
+            if (++vslot == C::NV) vslot = 0, vphase ^= 1;
+          }
+          if (i + 2 >= pv.steps) mma_commit(bar(B_O + s), issue);
+          busy &= ~(1u << s);
+        }
       }
       mma_commit(bar(B_FIN), issue);
       mbar_drain(bar(B_FIN), 0);
@@ -335,9 +380,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t sphase = 0, ophase = 0, mphase = 0;
     bool ok = true, more = any;
     PagedWalk w;
-    if (any) w.begin(plan, start);
-    while (ok && more && w.piece(p0, p1)) {
-      if (w.j0 < w.j1) {
+    if (any) {
+      w.begin(plan, start);
+      more = w.seek(plan, p0, p1);
+    }
+    for (; more; more = w.next(plan) && w.seek(plan, p0, p1)) {
+      {
         const bool wide = w.width == 2;
         const int n = w.j1 - w.j0;
         const int hk = w.at.head / plan.gblocks, gb = w.at.head - hk * plan.gblocks;
@@ -365,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 128; ++e) sv(e) ^= 0x80000000u;
             }
-            if (__any_sync(0xffffffffu, k0 + 127 > last)) {
+            if (__any_sync(0xffffffffu, row_ok && k0 + 127 > last)) {
               const int lim = last - k0;
 #pragma unroll
               for (int e = 0; e < 128; ++e)
@@ -380,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float alpha = 1.f;
             bool need = false;
             if (tmax > m_run + kRescaleThreshold || (m_run == -INFINITY && tmax > -INFINITY)) {
-              need = m_run != -INFINITY;
+              need = row_ok && m_run != -INFINITY;
               alpha = need ? exp2f(m_run - tmax) : 1.f;
               m_run = tmax;
             }
@@ -438,7 +486,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(bar(B_ML));
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(B_MD), mphase, abort_flag, err)))) break;
             mphase ^= 1;
-            more = w.next(plan);
             continue;
           }
           if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(B_ML), mphase, abort_flag, err)))) break;
@@ -511,7 +558,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!wide) mbar_arrive(bar(B_MD));
       }
-      more = w.next(plan);
     }
   }
 
