@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0 && plan.lens[w.at.b] > plan.max_keys) atomicOr(err, kErrIndex);
           const int head = hk * plan.G + (w.at.head - hk * plan.gblocks) * plan.gw;
           for (int s = 0; s < w.width; ++s) {
-            if (!(ok = mbar_wait(bar(B_QE + qslot), qphase, abort_flag, err))) break;
+            if (!(ok = mbar_wait_asleep(bar(B_QE + qslot), qphase, abort_flag, err))) break;
             if (lane == 0) {
               mbar_arrive_expect_tx(bar(B_QF + qslot), (uint32_t)(64 * 2 * plan.gw * plan.nt * C::ATOMS));
               for (int a = 0; a < C::ATOMS; ++a)
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
         }
         for (int j = w.j0; j < w.j1; ++j) {
-          if (!(ok = mbar_wait(bar(empty + slot), phase, abort_flag, err))) break;
+          if (!(ok = mbar_wait_asleep(bar(empty + slot), phase, abort_flag, err))) break;
           const int held = w.q.len - j * 128;  // keys of the tile and beyond
           const int boxes = held <= 0 ? 0 : held >= 128 ? 128 / p.box : (held + p.box - 1) / p.box;
           fence_proxy_async_smem();
@@ -243,14 +243,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // landed, so that a unit's end leaves the tensor core with work.
       // Everything that decides what is issued is made warp-uniform where it
       // is read, once a unit, so that descriptors and slots stay in uniform
-      // registers (from ordinary ones the issue of a step's 16 instructions
-      // took 2000 cycles instead of the 1024 that they run for).
-      const uint32_t issue = lane == 0 ? 1u : 0u;
+      // registers, and one elected lane issues: from a lane chosen by its number
+      // each instruction takes 47 cycles to issue, from an elected one 9, of the
+      // 64 that it runs for.
       constexpr uint32_t ID_S = idesc_16(128, 128, false, false, F16);
       constexpr uint32_t ID_PV = idesc_16(128, DP, false, true, F16);
       constexpr uint32_t HI = sdesc_hi_sw128(1024);
       auto wall = [&](int i, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, abort_flag, err));
+        return __all_sync(0xffffffffu, mbar_wait_asleep(bar(i), parity, abort_flag, err));
       };
       struct Part {  // a unit's part of the piece, uniform
         uint32_t wide, steps, last_held;  // last_held: keys from its last key tile on
@@ -287,17 +287,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t a_lo = q_lo + qs * (C::TILE >> 4), b_lo = k_lo + kslot * (C::TILE >> 4);
         const uint32_t d = tmu + C::TM_S + s * 128;
+        const bool k_done = !sp.wide || s == 1, q_done = si + 1 + sp.wide >= sp.steps;
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * C::ATOM + (kk & 3) * 32) >> 4;
-          mma_ss_lo(d, a_lo + off, b_lo + off, HI, ID_S, kk > 0, issue);
+          for (int kk = 0; kk < DP / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * C::ATOM + (kk & 3) * 32) >> 4;
+            mma_ss_one(d, a_lo + off, b_lo + off, HI, ID_S, kk > 0);
+          }
+          mma_commit_one(bar(B_S + s));
+          if (k_done) mma_commit_one(bar(B_KE + kslot));
+          if (q_done) mma_commit_one(bar(B_QE + qs));
         }
-        mma_commit(bar(B_S + s), issue);
-        if (!sp.wide || s == 1) {
-          mma_commit(bar(B_KE + kslot), issue);
-          if (++kslot == C::NK) kslot = 0, kphase ^= 1;
-        }
-        if (si + 1 + sp.wide >= sp.steps) mma_commit(bar(B_QE + qs), issue);
+        __syncwarp();
+        if (k_done && ++kslot == C::NK) kslot = 0, kphase ^= 1;
         busy |= 1u << s;
         if (++si == sp.steps) {
           si = 0;
@@ -343,24 +345,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t d = tmu + C::TM_O + s * DP, a = tmu + C::TM_S + s * 128;
           const uint32_t b_lo = v_lo + vslot * (C::TILE >> 4);
-          if (!tail) {
+          const bool v_done = !pv.wide || s == 1;
+          if (elect_one()) {
+            if (!tail) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ts_lo(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, (i >= 2 || kk > 0) ? 1u : 0u, issue);
-          } else {
-            const uint32_t ksteps = pv.last_held == 0 ? 1 : (pv.last_held + 15) / 16;
-            for (uint32_t kk = 0; kk < ksteps; ++kk)
-              mma_ts_lo(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, (i >= 2 || kk > 0) ? 1u : 0u, issue);
+              for (int kk = 0; kk < 8; ++kk)
+                mma_ts_one(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, (i >= 2 || kk > 0) ? 1u : 0u);
+            } else {
+              const uint32_t ksteps = pv.last_held == 0 ? 1 : (pv.last_held + 15) / 16;
+              for (uint32_t kk = 0; kk < ksteps; ++kk)
+                mma_ts_one(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, (i >= 2 || kk > 0) ? 1u : 0u);
+            }
+            if (v_done) mma_commit_one(bar(B_VE + vslot));
+            if (i + 2 >= pv.steps) mma_commit_one(bar(B_O + s));
           }
-          if (!pv.wide || s == 1) {
-            mma_commit(bar(B_VE + vslot), issue);
-            if (++vslot == C::NV) vslot = 0, vphase ^= 1;
-          }
-          if (i + 2 >= pv.steps) mma_commit(bar(B_O + s), issue);
+          __syncwarp();
+          if (v_done && ++vslot == C::NV) vslot = 0, vphase ^= 1;
           busy &= ~(1u << s);
         }
       }
-      mma_commit(bar(B_FIN), issue);
+      if (elect_one()) mma_commit_one(bar(B_FIN));
+      __syncwarp();
       mbar_drain(bar(B_FIN), 0);
     }
   } else {
@@ -398,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!row_ok) last = -1;
         float m_run = -INFINITY, l = 0.f;
         for (int t = wide ? 0 : s; t < n; t += wide ? 1 : 2) {
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(B_S + s), sphase, abort_flag, err)))) break;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait_asleep(bar(B_S + s), sphase, abort_flag, err)))) break;
           sphase ^= 1;
           if (active) {
             tc_fence_after();
@@ -421,9 +426,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < 128; e += 4)
+            for (int e = 0; e < 128; e += 8)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(sv(e + c)));
+              for (int c = 0; c < 4; ++c)
+                mx[c] = max3(mx[c], __uint_as_float(sv(e + 2 * c)), __uint_as_float(sv(e + 2 * c + 1)));
             const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c1;
             float alpha = 1.f;
             bool need = false;
@@ -446,22 +452,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               l *= alpha;
             }
             const float ref = m_run == -INFINITY ? 0.f : m_run - kBias;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint64_t c12 = pair_f32(c1, c1), ref2 = pair_f32(-ref, -ref);
+            uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               uint32_t pk[32];
 #pragma unroll
               for (int c = 0; c < 32; ++c) {
                 const int e = h * 64 + 2 * c;
-                const float a = ex2_approx(fmaf(__uint_as_float(sv(e)), c1, -ref));
-                const float b = ex2_approx(fmaf(__uint_as_float(sv(e + 1)), c1, -ref));
-                sum[(2 * c) & 3] += a;
-                sum[(2 * c + 1) & 3] += b;
+                const float2 y =
+                    split_f32(fma_f32x2(pair_f32(__uint_as_float(sv(e)), __uint_as_float(sv(e + 1))), c12, ref2));
+                const float a = ex2_approx(y.x), b = ex2_approx(y.y);
+                sum[c & 3] = add_f32x2(sum[c & 3], pair_f32(a, b));
                 pk[c] = pack2<F16>(a, b);
               }
               tmem_st32(tS + h * 32, pk);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            const float2 total = split_f32(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])));
+            l += total.x + total.y;
             tmem_st_wait();
             tc_fence_before();
           }
@@ -473,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float ref = m_run == -INFINITY ? 0.f : m_run - kBias;
         const bool ran = wide || s < n;  // the stream had a key tile
         if (ran) {
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(B_O + s), ophase, abort_flag, err)))) break;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait_asleep(bar(B_O + s), ophase, abort_flag, err)))) break;
           ophase ^= 1;
         }
         float f0 = 1.f, f1 = 0.f, lt = l, mt = ref;  // the row is f0 O_0 + f1 O_1
@@ -484,11 +492,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             tc_fence_before();
             mbar_arrive(bar(B_ML));
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(B_MD), mphase, abort_flag, err)))) break;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait_asleep(bar(B_MD), mphase, abort_flag, err)))) break;
             mphase ^= 1;
             continue;
           }
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(B_ML), mphase, abort_flag, err)))) break;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait_asleep(bar(B_ML), mphase, abort_flag, err)))) break;
           mphase ^= 1;
           const float2 other = ml_s[r];
           if (other.y != 0.f) {
