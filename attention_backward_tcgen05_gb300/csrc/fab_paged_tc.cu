@@ -100,8 +100,8 @@ struct TcParams {
   float* lse;
 };
 
-FAB_DEV void reg_dealloc() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
-FAB_DEV void reg_alloc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+FAB_DEV void reg_dealloc() { asm volatile("setmaxnreg.dec.sync.aligned.u32 96;"); }
+FAB_DEV void reg_alloc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 200;"); }
 
 template <int DP, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -236,137 +236,178 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (any && warp == 1) {
       // ------------------------------------------------------------ products
-      // Step i of a unit belongs to stream i & 1.  A stream's next S is issued
-      // once O += P V of its last one is, which frees the columns (a CTA's
-      // matrix instructions run in the order of their issue): S products run
-      // two steps ahead, into the next unit too where its operands have
-      // landed, so that a unit's end leaves the tensor core with work.
-      // Everything that decides what is issued is made warp-uniform where it
-      // is read, once a unit, so that descriptors and slots stay in uniform
-      // registers, and one elected lane issues: from a lane chosen by its number
-      // each instruction takes 47 cycles to issue, from an elected one 9, of the
-      // 64 that it runs for.
-      constexpr uint32_t ID_S = idesc_16(128, 128, false, false, F16);
-      constexpr uint32_t ID_PV = idesc_16(128, DP, false, true, F16);
-      constexpr uint32_t HI = sdesc_hi_sw128(1024);
-      auto wall = [&](int i, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait_asleep(bar(i), parity, abort_flag, err));
-      };
-      struct Part {  // a unit's part of the piece, uniform
-        uint32_t wide, steps, last_held;  // last_held: keys from its last key tile on
-      };
-      auto part_of = [&](const PagedWalk& x) {
-        Part y;
-        y.wide = uniform(x.width == 2 ? 1u : 0u);
-        y.steps = uniform((uint32_t)((x.j1 - x.j0) * x.width));
-        const int held = x.q.len - (x.j1 - 1) * 128;
-        y.last_held = uniform(held < 0 ? 0u : (uint32_t)held);
-        return y;
-      };
-      const uint32_t tmu = uniform(tm), sbu = uniform(sbase);
-      const uint32_t q_lo = sdesc_lo(sbu + C::OFF_Q, 16), k_lo = sdesc_lo(sbu + C::OFF_K, 16);
-      const uint32_t v_lo = sdesc_lo(sbu + C::OFF_V, C::ATOM);
-      uint32_t kslot = 0, kphase = 0, vslot = 0, vphase = 0, qslot = 0, qphase = 0, pphase = 0, busy = 0;
-      bool ok = true;
-      PagedWalk ws, w;  // of the S products, of the products with V
-      ws.begin(plan, start);
-      bool smore = __all_sync(0xffffffffu, ws.seek(plan, p0, p1));
-      w = ws;
-      Part sp = part_of(ws);
-      uint32_t si = 0, ahead = 0;  // ahead: the S products are in a later unit
-      auto issue_s = [&]() {
-        const uint32_t s = si & 1u;
-        const uint32_t qs = sp.wide ? qslot ^ s : qslot;
-        if (si <= sp.wide) {
-          if (!(ok = wall(B_QF + qs, (qphase >> qs) & 1u))) return;
-          qphase ^= 1u << qs;
-        }
-        if (!sp.wide || s == 0) {
-          if (!(ok = wall(B_KF + kslot, kphase))) return;
-        }
-        tc_fence_after();
-        const uint32_t a_lo = q_lo + qs * (C::TILE >> 4), b_lo = k_lo + kslot * (C::TILE >> 4);
-        const uint32_t d = tmu + C::TM_S + s * 128;
-        const bool k_done = !sp.wide || s == 1, q_done = si + 1 + sp.wide >= sp.steps;
-        if (elect_one()) {
+      // One elected lane does it all: the compiler then knows that a single lane
+      // issues the matrix instructions (9 cycles each; from a lane chosen by its
+      // number 47, of the 64 that they run for).  A stream's next S is issued
+      // right behind the O += P V that frees its columns: a thread's matrix
+      // instructions run in the order of their issue.  A slot of K's or V's ring
+      // and of Q is freed by a commit behind the last product that reads it.
+      if (elect_one()) {
+        constexpr uint32_t ID_S = idesc_16(128, 128, false, false, F16);
+        constexpr uint32_t ID_PV = idesc_16(128, DP, false, true, F16);
+        constexpr uint32_t HI = sdesc_hi_sw128(1024);
+        constexpr uint32_t SLOT = C::TILE >> 4;  // a slot, in a descriptor's units
+        const uint32_t q_lo = sdesc_lo(sbase + C::OFF_Q, 16), k_lo = sdesc_lo(sbase + C::OFF_K, 16);
+        const uint32_t v_lo = sdesc_lo(sbase + C::OFF_V, C::ATOM);
+        auto wait = [&](int i, uint32_t parity) { return mbar_wait_asleep(bar(i), parity, abort_flag, err); };
+        auto s_product = [&](uint32_t s, uint32_t a_lo, uint32_t b_lo) {
 #pragma unroll
           for (int kk = 0; kk < DP / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * C::ATOM + (kk & 3) * 32) >> 4;
-            mma_ss_one(d, a_lo + off, b_lo + off, HI, ID_S, kk > 0);
+            mma_ss_one(tm + C::TM_S + s * 128, a_lo + off, b_lo + off, HI, ID_S, kk > 0);
           }
           mma_commit_one(bar(B_S + s));
-          if (k_done) mma_commit_one(bar(B_KE + kslot));
-          if (q_done) mma_commit_one(bar(B_QE + qs));
-        }
-        __syncwarp();
-        if (k_done && ++kslot == C::NK) kslot = 0, kphase ^= 1;
-        busy |= 1u << s;
-        if (++si == sp.steps) {
-          si = 0;
-          qslot ^= 1u ^ sp.wide;
-          smore = __all_sync(0xffffffffu, ws.next(plan) && ws.seek(plan, p0, p1));
-          if (smore) sp = part_of(ws);
-          ++ahead;
-        }
-      };
-      for (bool more = smore; ok && more;
-           more = __all_sync(0xffffffffu, w.next(plan) && w.seek(plan, p0, p1)), --ahead) {
-        const Part pv = part_of(w);
-        for (uint32_t i = 0; ok && i < pv.steps; ++i) {
-          const uint32_t s = i & 1u;
-          while (ok && smore && !((busy >> (si & 1u)) & 1u)) {
-            // another unit's operands are waited for only when nothing else is left to do
-            if (busy != 0 && ahead != 0 && si < 2) {
-              const uint32_t qs = sp.wide ? qslot ^ si : qslot;
-              const bool here = (si > sp.wide || mbar_test(bar(B_QF + qs), (qphase >> qs) & 1u)) &&
-                                ((sp.wide && si == 1) || mbar_test(bar(B_KF + kslot), kphase));
-              if (!__all_sync(0xffffffffu, here)) break;
-            }
-            issue_s();
-          }
-          if (!ok) break;
-          const bool tail = pv.last_held < 128 && i + 1 + pv.wide >= pv.steps;
-          if (!pv.wide || s == 0) {
-            if (!(ok = wall(B_VF + vslot, vphase))) break;
-            if (tail) {
-              // the last keys' tile: the products below run over whole steps
-              // of 16 keys, the rows from the last key to the step's end zeroed
-              const uint32_t end = pv.last_held == 0 ? 16 : (pv.last_held + 15) / 16 * 16;
-              for (uint32_t x = pv.last_held * 8 + lane; x < end * 8; x += 32)
+        };
+        auto pv_product = [&](uint32_t s, uint32_t b_lo, uint32_t keys, uint32_t more) {  // more: to what O_s holds
+          const uint32_t d = tm + C::TM_O + s * DP, a = tm + C::TM_S + s * 128;
+          if (keys == 128) {
 #pragma unroll
-                for (int a = 0; a < C::ATOMS; ++a)
-                  st_shared_v4(sbu + C::OFF_V + vslot * C::TILE + a * C::ATOM + x * 16, 0u, 0u, 0u, 0u);
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
+            for (int kk = 0; kk < 8; ++kk) mma_ts_one(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, kk > 0 ? 1u : more);
+          } else {
+            for (uint32_t kk = 0; kk * 16 < keys; ++kk)
+              mma_ts_one(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, kk > 0 ? 1u : more);
           }
-          if (!(ok = wall(B_P + s, (pphase >> s) & 1u))) break;
-          pphase ^= 1u << s;
+        };
+        // The last keys' tile: products run over whole steps of 16 keys (one at
+        // least), with the rows from the last key to the steps' end zeroed.
+        auto end_keys = [&](uint32_t slot, uint32_t last) -> uint32_t {
+          const uint32_t keys = last == 0 ? 16u : (last + 15u) / 16u * 16u;
+          if (last < 128u) {
+            const uint32_t row0 = sbase + C::OFF_V + slot * C::TILE;
+            for (uint32_t x = last * 8u; x < keys * 8u; ++x) {
+              st_shared_v4(row0 + x * 16u, 0u, 0u, 0u, 0u);
+              if (C::ATOMS == 2) st_shared_v4(row0 + C::ATOM + x * 16u, 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+          }
+          return keys;
+        };
+        auto last_of = [&](const PagedWalk& x) {  // keys from the part's last key tile on, 128 at most
+          const int held = x.q.len - (x.j1 - 1) * 128;
+          return held < 0 ? 0u : held > 128 ? 128u : (uint32_t)held;
+        };
+        uint32_t kslot = 0, kphase = 0, vslot = 0, vphase = 0, qn = 0, pphase0 = 0, pphase1 = 0;
+        bool ok = true;
+        auto next_k = [&]() {
+          if (++kslot == C::NK) kslot = 0, kphase ^= 1;
+        };
+        auto next_v = [&]() {
+          if (++vslot == C::NV) vslot = 0, vphase ^= 1;
+        };
+        // A unit of two row tiles: per key tile O_0, S_0, O_1, S_1, so that each
+        // stream's softmax runs beside the other's products.
+        auto two_tiles = [&](const PagedWalk& x) {
+          const uint32_t tiles = (uint32_t)(x.j1 - x.j0), last = last_of(x), q0 = qn & 1u, q1 = q0 ^ 1u;
+          const uint32_t a0 = q_lo + q0 * SLOT, a1 = q_lo + q1 * SLOT;
+          if (!wait(B_QF + q0, (qn >> 1) & 1u) || !wait(B_QF + q1, ((qn + 1) >> 1) & 1u)) return false;
+          qn += 2;
+          if (!wait(B_KF + kslot, kphase)) return false;
           tc_fence_after();
-          const uint32_t d = tmu + C::TM_O + s * DP, a = tmu + C::TM_S + s * 128;
-          const uint32_t b_lo = v_lo + vslot * (C::TILE >> 4);
-          const bool v_done = !pv.wide || s == 1;
-          if (elect_one()) {
-            if (!tail) {
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                mma_ts_one(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, (i >= 2 || kk > 0) ? 1u : 0u);
-            } else {
-              const uint32_t ksteps = pv.last_held == 0 ? 1 : (pv.last_held + 15) / 16;
-              for (uint32_t kk = 0; kk < ksteps; ++kk)
-                mma_ts_one(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, (i >= 2 || kk > 0) ? 1u : 0u);
-            }
-            if (v_done) mma_commit_one(bar(B_VE + vslot));
-            if (i + 2 >= pv.steps) mma_commit_one(bar(B_O + s));
+          s_product(0, a0, k_lo + kslot * SLOT);
+          s_product(1, a1, k_lo + kslot * SLOT);
+          mma_commit_one(bar(B_KE + kslot));
+          next_k();
+          uint32_t more = 0;
+          for (uint32_t t = 1; t < tiles; ++t) {
+            if (!wait(B_KF + kslot, kphase) || !wait(B_VF + vslot, vphase)) return false;
+            const uint32_t kb = k_lo + kslot * SLOT, vb = v_lo + vslot * SLOT;
+            if (!wait(B_P, pphase0)) return false;
+            pphase0 ^= 1u;
+            tc_fence_after();
+            pv_product(0, vb, 128, more);
+            s_product(0, a0, kb);
+            if (!wait(B_P + 1, pphase1)) return false;
+            pphase1 ^= 1u;
+            tc_fence_after();
+            pv_product(1, vb, 128, more);
+            mma_commit_one(bar(B_VE + vslot));
+            s_product(1, a1, kb);
+            mma_commit_one(bar(B_KE + kslot));
+            more = 1;
+            next_k();
+            next_v();
           }
-          __syncwarp();
-          if (v_done && ++vslot == C::NV) vslot = 0, vphase ^= 1;
-          busy &= ~(1u << s);
+          mma_commit_one(bar(B_QE + q0));
+          mma_commit_one(bar(B_QE + q1));
+          if (!wait(B_VF + vslot, vphase)) return false;
+          const uint32_t vb = v_lo + vslot * SLOT, keys = end_keys(vslot, last);
+          if (!wait(B_P, pphase0)) return false;
+          pphase0 ^= 1u;
+          tc_fence_after();
+          pv_product(0, vb, keys, more);
+          mma_commit_one(bar(B_O));
+          if (!wait(B_P + 1, pphase1)) return false;
+          pphase1 ^= 1u;
+          tc_fence_after();
+          pv_product(1, vb, keys, more);
+          mma_commit_one(bar(B_O + 1));
+          mma_commit_one(bar(B_VE + vslot));
+          next_v();
+          return true;
+        };
+        // Units of one row tile: key tile i is stream i & 1's.  The S products
+        // run two tiles ahead (ws, si), into the next such unit too where its
+        // operands have landed, so that a unit's end leaves work to do.
+        PagedWalk ws, w;
+        ws.begin(plan, start);
+        bool smore = ws.seek(plan, p0, p1);
+        w = ws;
+        uint32_t si = 0, ahead = 0, busy = 0;  // ahead: units between w's and ws's; busy: streams with an S or a P
+        auto s_ahead = [&]() {
+          while (smore && ws.width == 1 && !((busy >> (si & 1u)) & 1u)) {
+            const uint32_t qs = qn & 1u, qp = (qn >> 1) & 1u;
+            // another unit's operands are waited for only when nothing else is left to do
+            if (busy != 0 && ahead != 0 &&
+                !((si > 0 || mbar_test(bar(B_QF + qs), qp)) && mbar_test(bar(B_KF + kslot), kphase)))
+              break;
+            if (si == 0 && !wait(B_QF + qs, qp)) return false;
+            if (!wait(B_KF + kslot, kphase)) return false;
+            tc_fence_after();
+            s_product(si & 1u, q_lo + qs * SLOT, k_lo + kslot * SLOT);
+            mma_commit_one(bar(B_KE + kslot));
+            next_k();
+            busy |= 1u << (si & 1u);
+            if ((int)++si == ws.j1 - ws.j0) {
+              mma_commit_one(bar(B_QE + qs));
+              ++qn;
+              si = 0;
+              ++ahead;
+              smore = ws.next(plan) && ws.seek(plan, p0, p1);
+            }
+          }
+          return true;
+        };
+        auto one_tile = [&](const PagedWalk& x) {
+          const uint32_t tiles = (uint32_t)(x.j1 - x.j0), last = last_of(x);
+          for (uint32_t i = 0; i < tiles; ++i) {
+            const uint32_t s = i & 1u;
+            if (!s_ahead() || !wait(B_VF + vslot, vphase)) return false;
+            const uint32_t keys = i + 1 == tiles ? end_keys(vslot, last) : 128u;
+            if (!wait(B_P + s, s ? pphase1 : pphase0)) return false;
+            pphase0 ^= s ^ 1u;
+            pphase1 ^= s;
+            tc_fence_after();
+            pv_product(s, v_lo + vslot * SLOT, keys, i < 2 ? 0u : 1u);
+            mma_commit_one(bar(B_VE + vslot));
+            if (i + 2 >= tiles) mma_commit_one(bar(B_O + s));
+            next_v();
+            busy &= ~(1u << s);
+          }
+          --ahead;
+          return true;
+        };
+        for (bool more = smore; ok && more; more = w.next(plan) && w.seek(plan, p0, p1)) {
+          if (w.width == 2) {
+            ok = two_tiles(w);
+            smore = ws.next(plan) && ws.seek(plan, p0, p1);
+          } else {
+            ok = one_tile(w);
+          }
         }
+        mma_commit_one(bar(B_FIN));
+        mbar_drain(bar(B_FIN), 0);
       }
-      if (elect_one()) mma_commit_one(bar(B_FIN));
       __syncwarp();
-      mbar_drain(bar(B_FIN), 0);
     }
   } else {
     reg_alloc();

@@ -128,7 +128,7 @@ class Batch:
         """Every live token's row against softmax in 64 bits."""
         o, lse = o.double().cpu(), lse.double().cpu()
         u = half_step(self.dt)
-        worst, t0 = 0.0, 0
+        t0 = 0
         for b, (n, h) in enumerate(zip(self.new, self.held)):
             G = self.H // self.Hkv
             for hq in range(self.H if n else 0):
@@ -153,7 +153,7 @@ class Batch:
                 W = p @ V
                 room = weight[:, None] * (p @ V.abs()) * 1.01
                 room = room + u * (W.abs() + room) + torch.finfo(self.dt).smallest_normal * torch.finfo(self.dt).eps
-                worst = max(worst, ((got - W).abs() / room).max().item())
+                worst = ((got - W).abs() / room).max().item()
                 assert math.isfinite(worst) and worst <= 1, (b, hq, worst)
                 off = ((z - want).abs() / (d + add + 8 * U32 * (1 + want.abs()))).max().item()
                 assert math.isfinite(off) and off <= 1, (b, hq, "lse", off)
