@@ -274,22 +274,58 @@ struct PagedWalk {
   FAB_DEV int slot(int c) const { return 2 * c + (j0 == 0 ? 1 : 0); }
 };
 
+// What a CTA leaves for the combine kernel: whether slot 2c holds a part of a
+// unit that began before it, and the cut unit whose first part it holds.
+struct PagedCut {
+  int head_part;  // 1: slot 2c holds a part
+  int last;       // the last CTA that holds a part of the unit in slot 2c + 1; 0: no such unit
+  int s0, n;      // the unit: its sequence's tokens,
+  int head, token0, rows;  // its head and tokens, how many rows
+  int pad;
+};
+
 // Partial results: rows of `dp` floats, and (maximum in log2 units, sum) pairs.
 struct PagedParts {
   float* out;
   float2* ml;
+  PagedCut* cuts;
   int rows, dp;  // rows of a slot, floats of a row
 };
 inline size_t paged_parts_bytes(int rows, int dp) {
-  return (size_t)(2 * kPagedMaxGrid) * rows * (dp + 2) * sizeof(float);
+  return (size_t)(2 * kPagedMaxGrid) * rows * (dp + 2) * sizeof(float) + kPagedMaxGrid * sizeof(PagedCut);
 }
 inline PagedParts paged_parts(void* workspace, int rows, int dp) {
   PagedParts x;
   x.out = static_cast<float*>(workspace);
   x.ml = reinterpret_cast<float2*>(x.out + (size_t)(2 * kPagedMaxGrid) * rows * dp);
+  x.cuts = reinterpret_cast<PagedCut*>(x.ml + (size_t)(2 * kPagedMaxGrid) * rows);
   x.rows = rows;
   x.dp = dp;
   return x;
+}
+
+// Writes CTA c's PagedCut for its piece [p0, p1), which begins in the unit at
+// `start`.  One thread.
+FAB_DEV void paged_note_cut(const PagedPlan& p, const PagedParts& parts, const PagedPlace& start, int64_t p0, int64_t p1,
+                            const PagedBorders& border, int c) {
+  PagedCut cut{0, 0, 0, 0, 0, 0, 0, 0};
+  if (p0 < p1) {
+    PagedWalk w;
+    w.begin(p, start);
+    for (bool more = w.seek(p, p0, p1); more; more = w.next(p) && w.seek(p, p0, p1)) {
+      if (w.j0 > 0) cut.head_part = 1;
+      if (w.j0 == 0 && w.j1 < w.ntiles) {
+        cut.last = c + 1;
+        while (w.tiles_before(border(cut.last + 1)) < w.ntiles) ++cut.last;
+        cut.s0 = w.q.s0;
+        cut.n = w.q.n;
+        cut.head = w.at.head;
+        cut.token0 = w.at.i * p.nt * p.tiles;
+        cut.rows = w.width * p.nt * p.gw;
+      }
+    }
+  }
+  parts.cuts[c] = cut;
 }
 
 FAB_DEV void paged_store(float* p, float x) { *p = x; }
@@ -298,97 +334,66 @@ FAB_DEV void paged_store(__half* p, float x) { *p = __float2half_rn(x); }
 
 constexpr int kCombineThreads = 256;
 
-// Joins the units that the border between CTA blockIdx.x and the next cuts, if
-// the former holds the unit's first part: out = sum 2^(m_i - M) out_i / sum
-// 2^(m_i - M) l_i over its parts.  A warp per row, blockIdx.y of gridDim.y of
-// them.  Launched while the attention kernel still runs; waits for it first.
-template <typename T>
-__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedPlan p, const PagedParts parts,
-                                                                        int grid, int DV, int H, T* o, float* lse) {
-  __shared__ PagedShared sh;
-  int64_t mine;
-  paged_total<kCombineThreads>(p, &sh, &mine);
-  const int64_t W = sh.total;
-  const int c = (int)blockIdx.x;
-  const PagedBorders border(W, grid);
-  const int64_t p0 = border(c), p1 = border(c + 1);
-  if (p1 < W && p1 > p0) paged_locate<kCombineThreads>(p, &sh, mine, p1);
+// Joins the cut unit whose first part CTA blockIdx.x holds, if there is one:
+// out = sum 2^(m_i - M) out_i / sum 2^(m_i - M) l_i over its parts.  LPR lanes
+// share a row, four columns at a time; blockIdx.y of gridDim.y shares the rows.
+// Launched while the attention kernel still runs; waits for it first.
+template <typename T, int LPR>
+__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedPlan p, const PagedParts parts, int DV,
+                                                                        int H, T* o, float* lse) {
+  constexpr int RPB = kCombineThreads / LPR;  // rows a block takes at once
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (p1 >= W || p1 <= p0) return;
-  PagedWalk w;
-  w.begin(p, sh.at);
-  // not cut here, or the first part is an earlier CTA's
-  const int mine_tiles = w.tiles_before(p1);
-  if (mine_tiles == 0 || mine_tiles == w.ntiles || w.tiles_before(p0) > 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // CTAs c .. ce hold the unit's parts
-  int ce = c;
-  for (int base = c + 1;; base += 32) {
-    const int x = base + lane;
-    const bool done = x >= grid - 1 || w.tiles_before(border(x + 1)) >= w.ntiles;
-    const unsigned v = __ballot_sync(0xffffffffu, done);
-    if (v != 0) {
-      ce = base + __ffs((int)v) - 1;
-      break;
-    }
-  }
-  const int rows = w.width * p.nt * p.gw;
-  const int hk = w.at.head / p.gblocks, gb = w.at.head - hk * p.gblocks;
-  const int token0 = w.at.i * p.nt * p.tiles;
-  for (int x = (int)blockIdx.y * (kCombineThreads / 32) + warp; x < rows; x += (int)gridDim.y * (kCombineThreads / 32)) {
-    const int tile = x / (p.nt * p.gw), r = x - tile * p.nt * p.gw;
-    const int token = token0 + tile * p.nt + r / p.gw, g = gb * p.gw + r % p.gw;
-    if (token >= w.q.n || g >= p.G) continue;
-    const int row = tile * (parts.rows / p.tiles) + r;
-    // this lane's part of up to 32 at a time: a part without tiles has no weight
-    auto part_ml = [&](int k) {
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (k <= ce) {
-        const int a = k == c ? 0 : w.tiles_before(border(k));
-        const int b = w.tiles_before(border(k + 1));
-        if (a < b) ml = parts.ml[(int64_t)(k == c ? 2 * k + 1 : 2 * k) * parts.rows + row];
-      }
-      return ml;
-    };
-    float top = -INFINITY;
-    for (int k0 = c; k0 <= ce; k0 += 32) {
-      float m = part_ml(k0 + lane).x;
+  const int c = (int)blockIdx.x;
+  const PagedCut cut = parts.cuts[c];
+  if (cut.last == 0) return;
+  const int sub = (int)threadIdx.x % LPR;
+  const int tile_rows = p.nt * p.gw;
+  const int hk = cut.head / p.gblocks, gb = cut.head - hk * p.gblocks;
+  for (int x = (int)blockIdx.y * RPB + (int)threadIdx.x / LPR; x < cut.rows; x += (int)gridDim.y * RPB) {
+    const int tile = x >= tile_rows ? 1 : 0, r = x - tile * tile_rows, i = r / p.gw;
+    const int token = cut.token0 + tile * p.nt + i, g = gb * p.gw + r - i * p.gw;
+    if (token >= cut.n || g >= p.G) continue;
+    const int row = tile * (parts.rows / 2) + r;
+    const int64_t t = cut.s0 + token, h = (int64_t)hk * p.G + g;
+    T* dst = o + (t * H + h) * DV;
+    for (int c0 = sub * 4; c0 < parts.dp; c0 += LPR * 4) {
+      float m = -INFINITY, l = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      constexpr int U = 4;  // parts whose loads are in flight
+      for (int k0 = c; k0 <= cut.last; k0 += U) {
+        float2 ml[U];
+        float4 v[U];
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-      top = fmaxf(top, m);
-    }
-    const float ref = top == -INFINITY ? 0.f : top;
-    float acc[8], l = 0.f;
+        for (int u = 0; u < U; ++u) {
+          const int k = k0 + u;
+          ml[u] = make_float2(-INFINITY, 0.f);
+          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k <= cut.last && (k == c || parts.cuts[k].head_part)) {
+            const int64_t at = (int64_t)(k == c ? 2 * k + 1 : 2 * k) * parts.rows + row;
+            ml[u] = parts.ml[at];
+            v[u] = *reinterpret_cast<const float4*>(parts.out + at * parts.dp + c0);
+          }
+        }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    for (int k0 = c; k0 <= ce; k0 += 32) {
-      const float2 ml = part_ml(k0 + lane);
-      // (a part whose sum is zero has nothing to add, whatever its row holds)
-      const float f = ml.y == 0.f ? 0.f : exp2f(ml.x - ref);
-      float sum = f * ml.y;
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-      l += sum;
-      const int count = ce - k0 + 1 < 32 ? ce - k0 + 1 : 32;
-#pragma unroll 4
-      for (int k = 0; k < count; ++k) {
-        const float fk = __shfl_sync(0xffffffffu, f, k);
-        const int kk = k0 + k;
-        const float* src = parts.out + ((int64_t)(kk == c ? 2 * kk + 1 : 2 * kk) * parts.rows + row) * parts.dp;
-        if (fk != 0.f) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (lane + 32 * e < DV) acc[e] += fk * src[lane + 32 * e];
+        for (int u = 0; u < U; ++u) {
+          if (ml[u].y == 0.f) continue;  // nothing to add, whatever the row holds
+          const float top = fmaxf(m, ml[u].x);
+          const float a = m == -INFINITY ? 0.f : exp2f(m - top), b = exp2f(ml[u].x - top);
+          l = l * a + ml[u].y * b;
+          acc.x = acc.x * a + v[u].x * b;
+          acc.y = acc.y * a + v[u].y * b;
+          acc.z = acc.z * a + v[u].z * b;
+          acc.w = acc.w * a + v[u].w * b;
+          m = top;
         }
       }
-    }
-    const int64_t t = w.q.s0 + token, h = (int64_t)hk * p.G + g;
-    T* dst = o + (t * H + h) * DV;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float out[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (lane + 32 * e < DV) paged_store(dst + lane + 32 * e, acc[e] * inv);
-    if (lse != nullptr && lane == 0) lse[h * p.T + t] = l == 0.f ? INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+      for (int e = 0; e < 4; ++e)
+        if (c0 + e < DV) paged_store(dst + c0 + e, out[e]);
+      if (lse != nullptr && c0 == 0) lse[h * p.T + t] = l == 0.f ? INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
   }
 }
 
@@ -399,7 +404,7 @@ cudaError_t launch_combine(const PagedPlan& plan, const PagedParts& parts, int g
   if (grid < 2) return cudaSuccess;  // nothing is cut
   const int rows = plan.tiles * plan.nt * plan.gw;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)((rows + 63) / 64));
+  cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)((rows + 31) / 32));
   cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = s;
   cudaLaunchAttribute at{};
@@ -407,7 +412,8 @@ cudaError_t launch_combine(const PagedPlan& plan, const PagedParts& parts, int g
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<T>, plan, parts, grid, DV, H, o, lse);
+  if (parts.dp <= 64) return cudaLaunchKernelEx(&cfg, paged_combine_kernel<T, 16>, plan, parts, DV, H, o, lse);
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<T, 32>, plan, parts, DV, H, o, lse);
 }
 
 }  // namespace fab

@@ -31,7 +31,8 @@
 // not.
 //
 // Warps (384 threads): 0 = query and key loads, 1 = matrix instructions, 2 =
-// value loads, 3 = tensor memory; 4-7 and 8-11 = the two softmax streams.
+// value loads, 3 = tensor memory and the note for the combine kernel; 4-7 and
+// 8-11 = the two softmax streams.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -408,6 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_drain(bar(B_FIN), 0);
       }
       __syncwarp();
+    } else if (warp == 3 && lane == 0) {
+      paged_note_cut(plan, p.parts, start, p0, p1, border, (int)blockIdx.x);
     }
   } else {
     reg_alloc();
