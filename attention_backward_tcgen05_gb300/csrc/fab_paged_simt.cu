@@ -1,18 +1,33 @@
 // fab_paged_simt.cu -- attention of new tokens over a paged key/value cache on
-// the CUDA cores: every dtype, DK, DV <= 256, any page size.
+// the CUDA cores: every dtype, DK, DV <= 256, any page size.  It serves f32,
+// whose accuracy the tensor cores' 16-bit products do not reach, and the
+// widths and pages that the tensor-core kernel does not take.
 //
 //   token i of the n new ones of sequence b, head h:
 //   s_m = scale q . k_m over m <= lens[b] - n + i (causal) or m < lens[b],
 //   o = sum softmax(s)_m v_m,  lse = log sum exp(s_m)
 //
-// One pass over the keys with a running maximum and sum.
+// The work is shared out as on the tensor cores (fab_paged.cuh), with tiles of
+// R rows and key tiles of 64.  Each of a CTA's eight warps owns 8 keys of every
+// key tile, from the copy to the sum: it fetches their rows into a ring of its
+// own with asynchronous copies, keeps a running maximum and sum of its own, and
+// adds its keys' share to an output of its own, so that the loop has no barrier
+// for the block.  The warps' shares meet at the unit's end.  Scores: a lane
+// takes R / 4 rows of one key; the output: a lane takes CPL columns of all R
+// rows, so a value is read from shared memory once for R rows.
+//
+// Bound by memory for a few rows a sequence, by shared-memory reads (5 for 16
+// multiply-adds of the scores, 5 for 64 of the output) for more.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "fab.h"
 #include "fab_device.cuh"
 #include "fab_internal.h"
+#include "fab_paged.cuh"
 
 namespace fab {
 namespace {
@@ -20,102 +35,375 @@ namespace {
 __device__ uint32_t g_err_paged;
 
 constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kKeys = 8;  // keys of a tile that a warp owns
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
-__device__ __forceinline__ void from_f32(float& dst, float x) { dst = x; }
-__device__ __forceinline__ void from_f32(__nv_bfloat16& dst, float x) { dst = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_f32(__half& dst, float x) { dst = __float2half_rn(x); }
+struct SimtParams {
+  PagedPlan plan;
+  PagedParts parts;
+  const int32_t* table;
+  int64_t max_pages, pages;
+  int page, H, Hkv, DK, DV;
+  int ks, vs;          // bytes of a key and a value row in the ring (multiples of 16)
+  int qs;              // floats of a query row in shared memory (a multiple of 4, zero past DK)
+  int stages;          // of a warp's ring
+  int vec;             // rows come in whole aligned 16-byte pieces
+  float c1;            // scale log2 e
+  const void *q, *k, *v;
+  void* o;
+  float* lse;
+};
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-  return x;
+FAB_DEV void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {  // bytes 16, or 0: zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+FAB_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits for all but the latest n (0 .. 3) groups.
+FAB_DEV void cp_async_wait(int n) {
+  if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else asm volatile("cp.async.wait_group 3;" ::: "memory");
 }
 
-// A warp per (token, head).
+FAB_DEV float to_f32(float x) { return x; }
+FAB_DEV float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+FAB_DEV float to_f32(__half x) { return __half2float(x); }
+
+// Four values of a row in shared memory.
 template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) paged_rows_kernel(const PagedProblem p) {
-  constexpr int R = (int)kMaxWidth / 32;
-  if (blockIdx.x == 0) check_starts(p.starts, p.B, p.T, (int)threadIdx.x, (int)blockDim.x, &g_err_paged);
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (row >= p.T * p.H) return;
-  const int64_t t = row / p.H, h = row - t * p.H, hk = h / (p.H / p.Hkv);
-  const int DK = (int)p.DK, DV = (int)p.DV;
-  int64_t lo = 0, hi = p.B;
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (p.starts[mid] <= t) lo = mid; else hi = mid;
+FAB_DEV float4 lds4(const T* p) {
+  if constexpr (sizeof(T) == 4) {
+    return *reinterpret_cast<const float4*>(p);
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    constexpr bool h = std::is_same<T, __half>::value;
+    const float2 a = unpack2<h>(v.x), b = unpack2<h>(v.y);
+    return make_float4(a.x, a.y, b.x, b.y);
   }
-  const int64_t s0 = p.starts[lo], s1 = p.starts[lo + 1], len = p.lens[lo];
-  if (t < s0 || t >= s1) return;  // padding after the last sequence
-  int64_t mend = p.causal ? len - (s1 - t) + 1 : len;
-  if (mend > p.max_pages * p.page) {
-    mend = p.max_pages * p.page;
-    atomicOr(&g_err_paged, kErrIndex);
-  }
-  const T* q = static_cast<const T*>(p.q) + row * DK;
-  float qv[R], acc[R];
-#pragma unroll
-  for (int e = 0; e < R; ++e) {
-    qv[e] = lane + 32 * e < DK ? to_f32(q[lane + 32 * e]) : 0.f;
-    acc[e] = 0.f;
-  }
-  float mx = -INFINITY, l = 0.f;
-  for (int64_t m = 0; m < mend; ++m) {
-    const int64_t page = p.table[lo * p.max_pages + m / p.page];
-    if (page < 0 || page >= p.pages) {
-      atomicOr(&g_err_paged, kErrIndex);
-      continue;
+}
+
+template <typename T, int R, int CPL>
+__global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_constant__ SimtParams p) {
+  static_assert(R % 4 == 0 && CPL % 4 == 0, "");
+  constexpr int RPL = R / 4;  // rows a lane scores
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ PagedShared sh;
+  const PagedPlan& plan = p.plan;
+  const int lane = (int)lane_id(), warp = (int)warp_id();
+  if (blockIdx.x == 0) check_starts(plan.starts, plan.B, plan.T, (int)threadIdx.x, kThreads, &g_err_paged);
+  int64_t mine;
+  paged_total<kThreads>(plan, &sh, &mine);
+  const PagedBorders border(sh.total, (int)gridDim.x);
+  const int64_t p0 = border((int)blockIdx.x), p1 = border((int)blockIdx.x + 1);
+  if (p0 < p1) paged_locate<kThreads>(plan, &sh, mine, p0);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const PagedPlace start = sh.at;
+  if (threadIdx.x == 0) paged_note_cut(plan, p.parts, start, p0, p1, border, (int)blockIdx.x);
+  if (p0 >= p1) return;
+
+  float* q_s = reinterpret_cast<float*>(smem);               // [R][qs]
+  float* p_s = q_s + R * p.qs + warp * (kKeys + 1) * R;      // this warp's weights [key][row], then factors [row]
+  uint8_t* ring0 = smem + (R * p.qs + kWarps * (kKeys + 1) * R) * 4;
+  const int stage_bytes = kKeys * (p.ks + p.vs);
+  uint8_t* ring = ring0 + warp * p.stages * stage_bytes;
+  float* acc_s = reinterpret_cast<float*>(ring0);            // at a unit's end: [warp][R][dp]
+  float2* ml_s = reinterpret_cast<float2*>(acc_s + kWarps * R * p.parts.dp);  // [warp][R]
+  const int key = lane & 7, rg = lane >> 3;  // scores: this lane's key, its rows rg * RPL ..
+  const T* kc = static_cast<const T*>(p.k);
+  const T* vc = static_cast<const T*>(p.v);
+
+  PagedWalk w;
+  w.begin(plan, start);
+  for (bool more = w.seek(plan, p0, p1); more; more = w.next(plan) && w.seek(plan, p0, p1)) {
+    const int hk = w.at.head / plan.gblocks, gb = w.at.head - hk * plan.gblocks;
+    const int token0 = w.at.i * plan.nt;
+    // the unit's queries, zero where there is no row
+    __syncthreads();
+    for (int x = (int)threadIdx.x; x < R * p.qs; x += kThreads) {
+      const int r = x / p.qs, d = x - r * p.qs, i = r / plan.gw, g = gb * plan.gw + r - i * plan.gw;
+      float v = 0.f;
+      if (d < p.DK && i < plan.nt && token0 + i < w.q.n && g < plan.G)
+        v = to_f32(static_cast<const T*>(p.q)[((int64_t)(w.q.s0 + token0 + i) * p.H + (int64_t)hk * plan.G + g) * p.DK + d]);
+      q_s[x] = v;
     }
-    const int64_t at = (page * p.Hkv + hk) * p.page + m % p.page;
-    const T* k = static_cast<const T*>(p.k) + at * DK;
-    float s = 0.f;
+    if (threadIdx.x == 0 && plan.lens[w.at.b] > plan.max_keys) atomicOr(&g_err_paged, kErrIndex);
+    __syncthreads();
+    int last[RPL];  // last key that each of this lane's rows sees
 #pragma unroll
-    for (int e = 0; e < R; ++e)
-      if (lane + 32 * e < DK) s += qv[e] * to_f32(k[lane + 32 * e]);
-    s = warp_sum(s) * p.scale;
-    if (s > mx) {
-      const float corr = expf(mx - s);
-      l *= corr;
-#pragma unroll
-      for (int e = 0; e < R; ++e) acc[e] *= corr;
-      mx = s;
+    for (int e = 0; e < RPL; ++e) {
+      const int i = (rg * RPL + e) / plan.gw;
+      last[e] = w.q.len - 1;
+      if (plan.causal && w.q.last0 + token0 + i < last[e]) last[e] = w.q.last0 + token0 + i;
     }
-    const float w = s == -INFINITY ? 0.f : expf(s - mx);
-    l += w;
-    const T* v = static_cast<const T*>(p.v) + at * DV;
+    float m[RPL], l[RPL], acc[R][CPL];
 #pragma unroll
-    for (int e = 0; e < R; ++e)
-      if (lane + 32 * e < DV) acc[e] += w * to_f32(v[lane + 32 * e]);
+    for (int e = 0; e < RPL; ++e) m[e] = -INFINITY, l[e] = 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) acc[r][c] = 0.f;
+
+    // fetches this warp's 8 rows of key tile j into the ring's slot
+    auto fetch = [&](int j, int slot) {
+      const int mk = j * 64 + warp * kKeys + key;  // (every group of 8 lanes looks up the same 8 pages)
+      int64_t row = -1;
+      if (j < w.j1 && mk < w.q.len) {
+        const int at = (int)((uint32_t)mk / (uint32_t)p.page);
+        const int page = p.table[(int64_t)w.at.b * p.max_pages + at];
+        if (page >= 0 && page < p.pages)
+          row = ((int64_t)page * p.Hkv + hk) * p.page + (mk - at * p.page);
+        else
+          atomicOr(&g_err_paged, kErrIndex);  // (its key and value are zeros)
+      }
+      uint8_t* kd = ring + slot * stage_bytes;
+      uint8_t* vd = kd + kKeys * p.ks;
+      if (p.vec) {
+        // 16-byte pieces of keys, then of values; a row's pieces side by side
+        const int kp = p.DK * (int)sizeof(T) / 16, vp = p.DV * (int)sizeof(T) / 16, per = kp + vp;
+        for (int x = lane; x - lane < kKeys * per; x += 32) {
+          const int kk = x / per, c = x - kk * per;
+          const int64_t src = __shfl_sync(0xffffffffu, row, kk & 7);
+          if (x >= kKeys * per) continue;
+          const bool isk = c < kp;
+          const uint8_t* from = isk ? reinterpret_cast<const uint8_t*>(kc + (src < 0 ? 0 : src) * p.DK) + c * 16
+                                    : reinterpret_cast<const uint8_t*>(vc + (src < 0 ? 0 : src) * p.DV) + (c - kp) * 16;
+          cp_async16(smem_u32(isk ? kd + kk * p.ks + c * 16 : vd + kk * p.vs + (c - kp) * 16), from, src < 0 ? 0u : 16u);
+        }
+      } else {
+        for (int kk = 0; kk < kKeys; ++kk) {
+          const int64_t src = __shfl_sync(0xffffffffu, row, kk);
+          T* kr = reinterpret_cast<T*>(kd + kk * p.ks);
+          T* vr = reinterpret_cast<T*>(vd + kk * p.vs);
+          for (int d = lane; d < p.qs; d += 32) kr[d] = src >= 0 && d < p.DK ? kc[src * p.DK + d] : T(0.f);
+          for (int d = lane; d < p.DV; d += 32) vr[d] = src >= 0 ? vc[src * p.DV + d] : T(0.f);
+        }
+      }
+      cp_async_commit();
+    };
+
+    __syncwarp();
+    for (int s = 0; s + 1 < p.stages; ++s) fetch(w.j0 + s, s);
+    int slot = 0;
+    for (int j = w.j0; j < w.j1; ++j) {
+      {
+        int ahead = slot + p.stages - 1;
+        if (ahead >= p.stages) ahead -= p.stages;
+        fetch(j + p.stages - 1, ahead);
+      }
+      cp_async_wait(p.stages - 1);
+      __syncwarp();
+      const T* kr = reinterpret_cast<const T*>(ring + slot * stage_bytes + key * p.ks);
+      const T* vb = reinterpret_cast<const T*>(ring + slot * stage_bytes + kKeys * p.ks);
+      float s[RPL];
+#pragma unroll
+      for (int e = 0; e < RPL; ++e) s[e] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < p.qs; d += 4) {
+        const float4 kv = lds4(kr + d);
+#pragma unroll
+        for (int e = 0; e < RPL; ++e) {
+          const float4 qv = *reinterpret_cast<const float4*>(q_s + (rg * RPL + e) * p.qs + d);
+          s[e] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[e]))));
+        }
+      }
+      const int mk = j * 64 + warp * kKeys + key;
+      bool grew = false;
+      float f[RPL];
+#pragma unroll
+      for (int e = 0; e < RPL; ++e) {
+        s[e] = mk <= last[e] ? s[e] * p.c1 : -INFINITY;
+        float top = s[e];
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        f[e] = 1.f;
+        if (top > m[e]) {
+          f[e] = m[e] == -INFINITY ? 0.f : exp2f(m[e] - top);  // (what there is before the first key is zero)
+          m[e] = top;
+          grew = true;
+        }
+        const float wt = s[e] == -INFINITY ? 0.f : exp2f(s[e] - m[e]);
+        l[e] = l[e] * f[e] + wt;
+        p_s[key * R + rg * RPL + e] = wt;
+        if (key == 0) p_s[kKeys * R + rg * RPL + e] = f[e];
+      }
+      grew = __any_sync(0xffffffffu, grew);
+      __syncwarp();
+      if (grew) {
+#pragma unroll
+        for (int r = 0; r < R; r += 4) {
+          const float4 fr = *reinterpret_cast<const float4*>(p_s + kKeys * R + r);
+#pragma unroll
+          for (int c = 0; c < CPL; ++c) {
+            acc[r][c] *= fr.x;
+            acc[r + 1][c] *= fr.y;
+            acc[r + 2][c] *= fr.z;
+            acc[r + 3][c] *= fr.w;
+          }
+        }
+      }
+#pragma unroll
+      for (int kk = 0; kk < kKeys; ++kk) {
+        const T* vr = reinterpret_cast<const T*>(reinterpret_cast<const uint8_t*>(vb) + kk * p.vs);
+#pragma unroll
+        for (int c = 0; c < CPL; c += 4) {
+          const int col = (c / 4) * 128 + lane * 4;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (col < p.DV) v = lds4(vr + col);
+#pragma unroll
+          for (int r = 0; r < R; r += 4) {
+            const float4 pr = *reinterpret_cast<const float4*>(p_s + kk * R + r);
+            const float wr[4] = {pr.x, pr.y, pr.z, pr.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              acc[r + i][c] = fmaf(wr[i], v.x, acc[r + i][c]);
+              acc[r + i][c + 1] = fmaf(wr[i], v.y, acc[r + i][c + 1]);
+              acc[r + i][c + 2] = fmaf(wr[i], v.z, acc[r + i][c + 2]);
+              acc[r + i][c + 3] = fmaf(wr[i], v.w, acc[r + i][c + 3]);
+            }
+          }
+        }
+      }
+      __syncwarp();  // the slot and the weights may be written again
+      if (++slot == p.stages) slot = 0;
+    }
+    // ---- the unit's end: the warps' shares
+    cp_async_wait(0);
+#pragma unroll
+    for (int e = 0; e < RPL; ++e)
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], o);
+    __syncthreads();
+    const int dp = p.parts.dp;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int c = 0; c < CPL; c += 4) {
+        const int col = (c / 4) * 128 + lane * 4;
+        if (col < dp)
+          *reinterpret_cast<float4*>(acc_s + (warp * R + r) * dp + col) =
+              make_float4(acc[r][c], acc[r][c + 1], acc[r][c + 2], acc[r][c + 3]);
+      }
+    if (key == 0) {
+#pragma unroll
+      for (int e = 0; e < RPL; ++e) ml_s[warp * R + rg * RPL + e] = make_float2(m[e], l[e]);
+    }
+    __syncthreads();
+    const bool whole = w.whole();
+    for (int x = (int)threadIdx.x; x < R * dp; x += kThreads) {
+      const int r = x / dp, col = x - r * dp, i = r / plan.gw, g = gb * plan.gw + r - i * plan.gw;
+      if (i >= plan.nt || token0 + i >= w.q.n || g >= plan.G) continue;
+      float top = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) top = fmaxf(top, ml_s[v * R + r].x);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float sum = 0.f, out = 0.f;
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) {
+        const float2 ml = ml_s[v * R + r];
+        if (ml.y == 0.f) continue;  // (no key: its output is zero)
+        const float f = exp2f(ml.x - ref);
+        sum += f * ml.y;
+        out += f * acc_s[(v * R + r) * dp + col];
+      }
+      const int64_t t = w.q.s0 + token0 + i, h = (int64_t)hk * plan.G + g;
+      if (whole) {
+        if (col < p.DV) paged_store(static_cast<T*>(p.o) + (t * p.H + h) * p.DV + col, sum == 0.f ? 0.f : out / sum);
+        if (col == 0 && p.lse != nullptr) p.lse[h * plan.T + t] = sum == 0.f ? INFINITY : (ref + log2f(sum)) * kLn2;
+      } else {
+        const int64_t at = (int64_t)w.slot((int)blockIdx.x) * p.parts.rows + r;
+        p.parts.out[at * dp + col] = out;
+        if (col == 0) p.parts.ml[at] = make_float2(ref, sum);
+      }
+    }
   }
-  // (l is NaN when a score is: the row is then NaN, not empty)
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  T* o = static_cast<T*>(p.o) + row * DV;
-#pragma unroll
-  for (int e = 0; e < R; ++e)
-    if (lane + 32 * e < DV) from_f32(o[lane + 32 * e], acc[e] * inv);
-  if (p.lse != nullptr && lane == 0) p.lse[h * p.T + t] = l == 0.f ? INFINITY : mx + logf(l);
+}
+
+constexpr int kSmemLimit = 232448 - 1024;  // (the plan's static part aside)
+
+int rows_of(const PagedProblem& pr) {
+  // four rows a tile where a sequence has no more to give (a decoding step of
+  // up to four heads a key head), else 16, or 8 of wide rows (128 registers of
+  // outputs a lane)
+  if (pr.T * (pr.H / pr.Hkv) <= 4 * pr.B) return 4;
+  return pr.DV > 128 ? 8 : 16;
+}
+int dp_of(const PagedProblem& pr) { return (int)(pr.DV + 3) / 4 * 4; }
+
+template <typename T, int R, int CPL>
+cudaError_t launch_r(const PagedProblem& pr, int sms, cudaStream_t s) {
+  SimtParams p;
+  p.plan.starts = pr.starts;
+  p.plan.lens = pr.lens;
+  p.plan.B = pr.B;
+  p.plan.T = pr.T;
+  const int64_t most = pr.max_pages * pr.page;
+  p.plan.max_keys = most < 2147483647ll - 256 ? most : 2147483647ll - 256;  // (lengths are 32-bit)
+  p.plan.causal = pr.causal;
+  p.plan.G = (int)(pr.H / pr.Hkv);
+  p.plan.gw = p.plan.G < R ? p.plan.G : R;
+  p.plan.gblocks = (p.plan.G + p.plan.gw - 1) / p.plan.gw;
+  p.plan.heads = (int)pr.Hkv * p.plan.gblocks;
+  p.plan.nt = R / p.plan.gw;
+  p.plan.tiles = 1;
+  p.plan.kt = 64;
+  p.parts = paged_parts(pr.workspace, R, dp_of(pr));
+  p.table = pr.table;
+  p.max_pages = pr.max_pages;
+  p.pages = pr.pages;
+  p.page = (int)pr.page;
+  p.H = (int)pr.H;
+  p.Hkv = (int)pr.Hkv;
+  p.DK = (int)pr.DK;
+  p.DV = (int)pr.DV;
+  const int e = (int)sizeof(T);
+  p.qs = (p.DK + 3) / 4 * 4;
+  p.ks = (p.qs * e + 15) / 16 * 16 + 16;  // (16 more: eight keys' rows start in different banks)
+  p.vs = (dp_of(pr) * e + 15) / 16 * 16;
+  p.vec = p.DK * e % 16 == 0 && p.DV * e % 16 == 0;
+  p.c1 = pr.scale * kLog2e;
+  p.q = pr.q;
+  p.k = pr.k;
+  p.v = pr.v;
+  p.o = pr.o;
+  p.lse = pr.lse;
+  const int fixed = (R * p.qs + kWarps * (kKeys + 1) * R) * 4, stage = kWarps * kKeys * (p.ks + p.vs);
+  const int end = kWarps * R * (p.parts.dp + 2) * 4;  // the warps' shares, over the rings
+  p.stages = (kSmemLimit - fixed) / stage;
+  p.stages = p.stages > 4 ? 4 : p.stages < 1 ? 1 : p.stages;
+  const int smem = fixed + (p.stages * stage > end ? p.stages * stage : end);
+  const int64_t units = (pr.T / p.plan.nt + pr.B) * p.plan.heads, tiles = (p.plan.max_keys + 63) / 64 + kPagedLead;
+  int grid = sms < kPagedMaxGrid ? sms : kPagedMaxGrid;
+  if (units < grid && tiles < grid && units * tiles < grid) grid = (int)(units * tiles);
+  cudaError_t err = cudaFuncSetAttribute(paged_simt_kernel<T, R, CPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err != cudaSuccess) return err;
+  paged_simt_kernel<T, R, CPL><<<(unsigned)grid, kThreads, smem, s>>>(p);
+  err = cudaPeekAtLastError();
+  if (err != cudaSuccess) return err;
+  return launch_combine<T>(p.plan, p.parts, grid, p.DV, p.H, static_cast<T*>(pr.o), pr.lse, s);
 }
 
 template <typename T>
-cudaError_t paged_t(const PagedProblem& p, cudaStream_t s) {
-  const int64_t grid = (p.T * p.H + kWarps - 1) / kWarps;
-  if (grid > 2147483647ll) return cudaErrorInvalidValue;
-  paged_rows_kernel<T><<<(unsigned)grid, kWarps * 32, 0, s>>>(p);
-  return cudaPeekAtLastError();
+cudaError_t launch_t(const PagedProblem& pr, int sms, cudaStream_t s) {
+  const int R = rows_of(pr);
+  if (pr.DV > 128) return R == 4 ? launch_r<T, 4, 8>(pr, sms, s) : launch_r<T, 8, 8>(pr, sms, s);
+  return R == 4 ? launch_r<T, 4, 4>(pr, sms, s) : launch_r<T, 16, 4>(pr, sms, s);
 }
 
 }  // namespace
 
-size_t paged_simt_workspace_bytes(const PagedProblem&) { return 256; }
+size_t paged_simt_workspace_bytes(const PagedProblem& p) { return paged_parts_bytes(16, dp_of(p)); }
 
 cudaError_t launch_paged_simt(const PagedProblem& p, cudaStream_t s) {
-  if (p.dtype == FAB_BF16) return paged_t<__nv_bfloat16>(p, s);
-  if (p.dtype == FAB_F16) return paged_t<__half>(p, s);
-  return paged_t<float>(p, s);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return cudaErrorInvalidValue;
+  if (p.dtype == FAB_BF16) return launch_t<__nv_bfloat16>(p, sms, s);
+  if (p.dtype == FAB_F16) return launch_t<__half>(p, sms, s);
+  return launch_t<float>(p, sms, s);
 }
 
 uint32_t take_error_paged() {
