@@ -5,11 +5,15 @@
 // A tile is `nt` tokens times `gw` query heads of one key/value head (a row
 // per pair); a unit is one tile or two (consecutive tokens) and walks its key
 // tiles.  Units in order of (sequence, head, tokens) form one line, each as
-// long as its key tiles (and kPagedLead more for its start and end) times its
-// tiles, and CTA c of G takes the piece from W c / G to W (c+1) / G of that
-// line, so every CTA has the same work whatever the lengths are.  A unit cut by a border leaves unnormalised
-// partial results (output, maximum, sum) in the workspace, at most two to a
-// CTA, which paged_combine_kernel joins.
+// long as its work, and CTA c of G takes the piece from W c / G to W (c+1) / G
+// of that line, so every CTA has the same work whatever the lengths are.  A
+// unit's work is a start and an end and its key tiles, in quarters of what a
+// key tile of a unit of two tiles takes: measured at 1.2 us for that, 0.9 us
+// for one of a unit of one tile (whose streams wait for memory or for one
+// another rather than for the tensor core) and 3 us for the start and the end,
+// by a fit over the CTAs of a batch of mixed chunks at width 64.  A unit cut by
+// a border leaves unnormalised partial results (output, maximum, sum) in the
+// workspace, at most two to a CTA, which paged_combine_kernel joins.
 #pragma once
 
 #include "fab_device.cuh"
@@ -17,7 +21,8 @@
 
 namespace fab {
 
-constexpr int kPagedLead = 2;  // what starting and ending a unit costs, in key tiles
+FAB_DEV int paged_lead(int width) { return width == 2 ? 10 : 6; }  // work of a start and an end,
+FAB_DEV int paged_step(int width) { return width == 2 ? 4 : 3; }   // of a key tile
 constexpr int kPagedMaxGrid = 304;  // CTAs that the workspace has room for
 
 // What planning needs to know.
@@ -81,18 +86,21 @@ struct PagedShared {
 
 // Length on the line of unit i.
 FAB_DEV int paged_length(const PagedPlan& p, const PagedSeq& q, int i) {
-  return paged_width(p, q, i) * (paged_key_tiles(p, q, i) + kPagedLead);
+  const int width = paged_width(p, q, i);
+  return paged_step(width) * paged_key_tiles(p, q, i) + paged_lead(width);
 }
 
 // Length on the line of one head of the sequence of each lane; whole warps.
 FAB_DEV int64_t paged_head_length(const PagedPlan& p, const PagedSeq& q) {
   const int units = paged_units(p, q);
   int64_t len = 0;
-  if (units <= 2) {
+  constexpr int kOwn = 12;  // units that a lane adds up by itself
+  if (units <= kOwn) {
+#pragma unroll 1
     for (int i = 0; i < units; ++i) len += paged_length(p, q, i);
   }
   // the lanes of a warp share the longer ones' units
-  for (unsigned left = __ballot_sync(0xffffffffu, units > 2); left != 0; left &= left - 1) {
+  for (unsigned left = __ballot_sync(0xffffffffu, units > kOwn); left != 0; left &= left - 1) {
     const int src = __ffs((int)left) - 1;
     PagedSeq x;
     x.s0 = 0;
@@ -100,6 +108,7 @@ FAB_DEV int64_t paged_head_length(const PagedPlan& p, const PagedSeq& q) {
     x.last0 = __shfl_sync(0xffffffffu, q.last0, src);
     x.len = __shfl_sync(0xffffffffu, q.len, src);
     int64_t sum = 0;
+#pragma unroll 1
     for (int i = (int)lane_id(), k = paged_units(p, x); i < k; i += 32) sum += paged_length(p, x, i);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -232,10 +241,10 @@ struct PagedWalk {
   }
   // Key tiles of the present unit before `pos` on the line.
   FAB_DEV int tiles_before(int64_t pos) const {
-    const int64_t d = pos - at.u0 - width * kPagedLead;
+    const int64_t d = pos - at.u0 - paged_lead(width);
     if (d <= 0) return 0;
-    const int64_t t = width == 2 ? (d + 1) >> 1 : d;
-    return t < ntiles ? (int)t : ntiles;
+    if (d >= (int64_t)paged_step(width) * ntiles) return ntiles;
+    return width == 2 ? ((int)d + 3) / 4 : ((int)d + 2) / 3;
   }
   // The part of the piece [p0, p1) that lies in the present unit.
   FAB_DEV bool piece(int64_t p0, int64_t p1) {
@@ -246,7 +255,7 @@ struct PagedWalk {
   }
   // The next unit (its j0, j1 are not set); false at the end of the line.
   FAB_DEV bool next(const PagedPlan& p) {
-    at.u0 += (int64_t)width * (ntiles + kPagedLead);
+    at.u0 += (int64_t)paged_step(width) * ntiles + paged_lead(width);
     if (++at.i == units) {
       at.i = 0;
       if (++at.head == p.heads) {
@@ -304,28 +313,19 @@ inline PagedParts paged_parts(void* workspace, int rows, int dp) {
   return x;
 }
 
-// Writes CTA c's PagedCut for its piece [p0, p1), which begins in the unit at
-// `start`.  One thread.
-FAB_DEV void paged_note_cut(const PagedPlan& p, const PagedParts& parts, const PagedPlace& start, int64_t p0, int64_t p1,
-                            const PagedBorders& border, int c) {
-  PagedCut cut{0, 0, 0, 0, 0, 0, 0, 0};
-  if (p0 < p1) {
-    PagedWalk w;
-    w.begin(p, start);
-    for (bool more = w.seek(p, p0, p1); more; more = w.next(p) && w.seek(p, p0, p1)) {
-      if (w.j0 > 0) cut.head_part = 1;
-      if (w.j0 == 0 && w.j1 < w.ntiles) {
-        cut.last = c + 1;
-        while (w.tiles_before(border(cut.last + 1)) < w.ntiles) ++cut.last;
-        cut.s0 = w.q.s0;
-        cut.n = w.q.n;
-        cut.head = w.at.head;
-        cut.token0 = w.at.i * p.nt * p.tiles;
-        cut.rows = w.width * p.nt * p.gw;
-      }
-    }
+// Adds what the walk's present unit says to CTA c's note.
+FAB_DEV void paged_note_part(const PagedPlan& p, const PagedWalk& w, const PagedBorders& border, int c, PagedCut* cut) {
+  if (w.j0 > 0) cut->head_part = 1;
+  if (w.j0 == 0 && w.j1 < w.ntiles) {
+    int last = c + 1;
+    while (w.tiles_before(border(last + 1)) < w.ntiles) ++last;
+    cut->last = last;
+    cut->s0 = w.q.s0;
+    cut->n = w.q.n;
+    cut->head = w.at.head;
+    cut->token0 = w.at.i * p.nt * p.tiles;
+    cut->rows = w.width * p.nt * p.gw;
   }
-  parts.cuts[c] = cut;
 }
 
 FAB_DEV void paged_store(float* p, float x) { *p = x; }

@@ -101,8 +101,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
   if (p0 < p1) paged_locate<kThreads>(plan, &sh, mine, p0);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const PagedPlace start = sh.at;
-  if (threadIdx.x == 0) paged_note_cut(plan, p.parts, start, p0, p1, border, (int)blockIdx.x);
-  if (p0 >= p1) return;
+  PagedCut cut{0, 0, 0, 0, 0, 0, 0, 0};
+  if (p0 >= p1) {
+    if (threadIdx.x == 0) p.parts.cuts[blockIdx.x] = cut;
+    return;
+  }
 
   float* q_s = reinterpret_cast<float*>(smem);               // [R][qs]
   float* p_s = q_s + R * p.qs + warp * (kKeys + 1) * R;      // this warp's weights [key][row], then factors [row]
@@ -318,7 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
         if (col == 0) p.parts.ml[at] = make_float2(ref, sum);
       }
     }
+    if (threadIdx.x == 0) paged_note_part(plan, w, border, (int)blockIdx.x, &cut);
   }
+  if (threadIdx.x == 0) p.parts.cuts[blockIdx.x] = cut;
 }
 
 constexpr int kSmemLimit = 232448 - 1024;  // (the plan's static part aside)
@@ -374,7 +379,7 @@ cudaError_t launch_r(const PagedProblem& pr, int sms, cudaStream_t s) {
   p.stages = (kSmemLimit - fixed) / stage;
   p.stages = p.stages > 4 ? 4 : p.stages < 1 ? 1 : p.stages;
   const int smem = fixed + (p.stages * stage > end ? p.stages * stage : end);
-  const int64_t units = (pr.T / p.plan.nt + pr.B) * p.plan.heads, tiles = (p.plan.max_keys + 63) / 64 + kPagedLead;
+  const int64_t units = (pr.T / p.plan.nt + pr.B) * p.plan.heads, tiles = (p.plan.max_keys + 63) / 64;
   int grid = sms < kPagedMaxGrid ? sms : kPagedMaxGrid;
   if (units < grid && tiles < grid && units * tiles < grid) grid = (int)(units * tiles);
   cudaError_t err = cudaFuncSetAttribute(paged_simt_kernel<T, R, CPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

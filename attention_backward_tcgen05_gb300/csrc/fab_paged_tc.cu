@@ -31,8 +31,8 @@
 // not.
 //
 // Warps (384 threads): 0 = query and key loads, 1 = matrix instructions, 2 =
-// value loads, 3 = tensor memory and the note for the combine kernel; 4-7 and
-// 8-11 = the two softmax streams.
+// value loads, 3 = the units in order and the note for the combine kernel (and
+// tensor memory); 4-7 and 8-11 = the two softmax streams.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -53,6 +53,23 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.f;  // log2 units
 constexpr int kThreads = 384;
 
+constexpr int kUnits = 4;  // units described ahead
+
+// A unit's part of a CTA's piece of the line, for every warp.
+struct UnitPart {
+  int more;       // 0: the piece is over
+  int width;      // row tiles
+  int j0, j1;     // key tiles
+  int s0, n;      // its sequence's new tokens,
+  int last0, len; // last key the first of them sees (causal), keys
+  int b;          // the sequence
+  int token0;     // first token of the unit
+  int hk, g0;     // key/value head, first query head of it
+  int slot;       // partial slot, or -1: the unit is whole
+  int pad[3];
+};
+static_assert(sizeof(UnitPart) == 64, "");
+
 template <int DP>
 struct PCfg {
   static constexpr int ATOMS = DP / 64;
@@ -63,14 +80,15 @@ struct PCfg {
   static constexpr uint32_t OFF_K = 2 * TILE;
   static constexpr uint32_t OFF_V = OFF_K + NK * TILE;
   static constexpr uint32_t OFF_BAR = OFF_V + NV * TILE;
-  static constexpr uint32_t OFF_MISC = OFF_BAR + 32 * 8;
-  static constexpr uint32_t OFF_ML = OFF_MISC + 512;  // 128 (maximum, sum) pairs
+  static constexpr uint32_t OFF_MISC = OFF_BAR + 40 * 8;
+  static constexpr uint32_t OFF_UNIT = OFF_MISC + 16;       // kUnits descriptions of units
+  static constexpr uint32_t OFF_ML = OFF_UNIT + kUnits * 64;  // 128 (maximum, sum) pairs; the plan's scratch before
   static constexpr uint32_t USED = OFF_ML + 128 * 8;
   static constexpr uint32_t SMEM = USED > 118784 ? USED : 118784;  // one CTA owns the SM's tensor memory
   static constexpr uint32_t TM_S = 0;    // + 128 * stream
   static constexpr uint32_t TM_O = 256;  // + DP * stream
   static_assert(SMEM <= 232448, "shared memory budget");
-  static_assert(sizeof(PagedShared) + 16 <= 512, "misc area");
+  static_assert(sizeof(PagedShared) <= 1024, "plan scratch");
 };
 
 enum : int {
@@ -81,12 +99,14 @@ enum : int {
   B_QF = 16,  // + slot: Q landed
   B_QE = 18,  // + slot: Q free
   B_S = 20,   // + stream: S landed (and every product issued before it)
-  B_P = 22,   // + stream: P written (and O rescaled where it had to be)
-  B_O = 24,   // + stream: the unit's last product of the stream finished
-  B_ML = 26,  // one-tile units: stream 1's maxima and sums are in shared memory
-  B_MD = 27,  // one-tile units: stream 0 has read stream 1's output
-  B_FIN = 28,
-  B_COUNT = 29
+  B_P = 22,   // + 2 stream + half: P's keys of that half written (and O rescaled where it had to be)
+  B_O = 26,   // + stream: the unit's last product of the stream finished
+  B_ML = 28,  // one-tile units: stream 1's maxima and sums are in shared memory
+  B_MD = 29,  // one-tile units: stream 0 has read stream 1's output
+  B_FIN = 30,
+  B_DF = 31,  // + slot: a unit is described
+  B_DE = 35,  // + slot: every warp is done with it
+  B_COUNT = 39
 };
 
 struct TcParams {
@@ -119,8 +139,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return sbase + C::OFF_BAR + 8u * (uint32_t)i; };
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 4);
-  PagedShared* sh = reinterpret_cast<PagedShared*>(smem + C::OFF_MISC + 16);
+  UnitPart* units = reinterpret_cast<UnitPart*>(smem + C::OFF_UNIT);
   float2* ml_s = reinterpret_cast<float2*>(smem + C::OFF_ML);
+  PagedShared* sh = reinterpret_cast<PagedShared*>(smem + C::OFF_ML);
   uint32_t* err = &g_err_paged_tc;
   const int warp = (int)warp_id(), lane = (int)lane_id();
   const PagedPlan& plan = p.plan;
@@ -132,12 +153,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(B_KE + s), 1);
       mbar_init(bar(B_VF + s), 1);
       mbar_init(bar(B_VE + s), 1);
+      mbar_init(bar(B_DF + s), 1);
+      mbar_init(bar(B_DE + s), 3 + 8);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(B_QF + s), 1);
       mbar_init(bar(B_QE + s), 1);
       mbar_init(bar(B_S + s), 1);
-      mbar_init(bar(B_P + s), 4);
+      mbar_init(bar(B_P + 2 * s), 4);
+      mbar_init(bar(B_P + 2 * s + 1), 4);
       mbar_init(bar(B_O + s), 1);
     }
     mbar_init(bar(B_ML), 128);
@@ -164,56 +188,94 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tm = *tmem_holder;
-  const PagedPlace start = sh->at;
   const bool any = p0 < p1;
 
   if (warp < 4) {
     reg_dealloc();
-    if (any && (warp == 0 || warp == 2)) {
+    if (warp == 3) {
+      // ------------------------------------------------------------ the units
+      if (lane == 0) {
+        PagedCut cut{0, 0, 0, 0, 0, 0, 0, 0};
+        PagedWalk w;
+        bool more = any;
+        if (any) {
+          w.begin(plan, sh->at);
+          more = w.seek(plan, p0, p1);
+        }
+        uint32_t slot = 0, phase = 1;
+        while (mbar_wait_asleep(bar(B_DE + slot), phase, abort_flag, err)) {
+          UnitPart* u = units + slot;
+          u->more = more;
+          if (more) {
+            const int hk = w.at.head / plan.gblocks;
+            u->width = w.width;
+            u->j0 = w.j0;
+            u->j1 = w.j1;
+            u->s0 = w.q.s0;
+            u->n = w.q.n;
+            u->last0 = w.q.last0;
+            u->len = w.q.len;
+            u->b = w.at.b;
+            u->token0 = w.at.i * plan.nt * 2;
+            u->hk = hk;
+            u->g0 = (w.at.head - hk * plan.gblocks) * plan.gw;
+            u->slot = w.whole() ? -1 : w.slot((int)blockIdx.x);
+          }
+          mbar_arrive(bar(B_DF + slot));
+          if (!more) break;
+          paged_note_part(plan, w, border, (int)blockIdx.x, &cut);
+          if (++slot == kUnits) slot = 0, phase ^= 1;
+          more = w.next(plan) && w.seek(plan, p0, p1);
+        }
+        p.parts.cuts[blockIdx.x] = cut;
+      }
+      __syncwarp();
+    } else if (warp != 1) {
       // ------------------------------------------------------------ loads
-      // Warp 0: a unit's Q (once the previous unit's S products are done with
-      // theirs) and its keys; warp 2: its values.  Lane i fetches box i of a
+      // Warp 0: a unit's Q (once the S products of the unit that had its slot
+      // are done) and its keys; warp 2: its values.  Lane i fetches box i of a
       // tile; its page number is looked up a tile ahead.
       const bool keys = warp == 0;
       const int full = keys ? B_KF : B_VF, empty = keys ? B_KE : B_VE, slots = keys ? C::NK : C::NV;
       const uint32_t ring = sbase + (keys ? C::OFF_K : C::OFF_V);
       const CUtensorMap* map = keys ? &tmK : &tmV;
-      int slot = 0, phase = 1, qslot = 0, qphase = 1;
+      int slot = 0, phase = 1, qslot = 0, qphase = 1, us = 0, up = 0;
       bool ok = true;
-      PagedWalk w;
-      w.begin(plan, start);
-      for (bool more = w.seek(plan, p0, p1); ok && more; more = w.next(plan) && w.seek(plan, p0, p1)) {
-        const int hk = w.at.head / plan.gblocks;
+      for (;;) {
+        if (!(ok = mbar_wait_asleep(bar(B_DF + us), up, abort_flag, err))) break;
+        const UnitPart& u = units[us];
+        if (!u.more) break;
+        const int j0 = u.j0, j1 = u.j1, len = u.len, hk = u.hk;
+        const int32_t* table = p.table + (int64_t)u.b * p.max_pages;
         // page of box `lane` of key tile j, and its first row there
         auto lookup = [&](int j, int& row) {
           const uint32_t m = (uint32_t)j * 128u + (uint32_t)(lane * p.box);
           const uint32_t at = m / (uint32_t)p.page;
           row = (int)(m - at * (uint32_t)p.page);
-          if (lane * p.box >= 128 || m >= (uint32_t)w.q.len) return 0;
-          const int page = __ldg(p.table + (int64_t)w.at.b * p.max_pages + at);
+          if (lane * p.box >= 128 || m >= (uint32_t)len) return 0;
+          const int page = __ldg(table + at);
           // (out of range: the copy fills zeros, the call is reported)
           if (page < 0 || page >= p.pages) atomicOr(err, kErrIndex);
           return page;
         };
-        int row, page = lookup(w.j0, row);
+        int row, page = lookup(j0, row);
         if (keys) {
-          if (lane == 0 && plan.lens[w.at.b] > plan.max_keys) atomicOr(err, kErrIndex);
-          const int head = hk * plan.G + (w.at.head - hk * plan.gblocks) * plan.gw;
-          for (int s = 0; s < w.width; ++s) {
+          if (lane == 0 && plan.lens[u.b] > plan.max_keys) atomicOr(err, kErrIndex);
+          for (int s = 0; s < u.width; ++s) {
             if (!(ok = mbar_wait_asleep(bar(B_QE + qslot), qphase, abort_flag, err))) break;
             if (lane == 0) {
               mbar_arrive_expect_tx(bar(B_QF + qslot), (uint32_t)(64 * 2 * plan.gw * plan.nt * C::ATOMS));
               for (int a = 0; a < C::ATOMS; ++a)
-                tma_load_3d(sbase + C::OFF_Q + qslot * C::TILE + a * C::ATOM, &tmQ, bar(B_QF + qslot), a * 64, head,
-                            w.q.s0 + w.at.i * plan.nt * 2 + s * plan.nt);
+                tma_load_3d(sbase + C::OFF_Q + qslot * C::TILE + a * C::ATOM, &tmQ, bar(B_QF + qslot), a * 64,
+                            hk * plan.G + u.g0, u.s0 + u.token0 + s * plan.nt);
             }
             if (++qslot == 2) qslot = 0, qphase ^= 1;
           }
           if (!ok) break;
         }
-        for (int j = w.j0; j < w.j1; ++j) {
+        for (int j = j0; j < j1; ++j) {
           if (!(ok = mbar_wait_asleep(bar(empty + slot), phase, abort_flag, err))) break;
-          const int held = w.q.len - j * 128;  // keys of the tile and beyond
+          const int held = len - j * 128;  // keys of the tile and beyond
           const int boxes = held <= 0 ? 0 : held >= 128 ? 128 / p.box : (held + p.box - 1) / p.box;
           fence_proxy_async_smem();
           if (lane == 0) mbar_arrive_expect_tx(bar(full + slot), (uint32_t)(boxes * p.box * 128 * C::ATOMS));
@@ -225,8 +287,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_4d(dst + a * C::ATOM, map, bar(full + slot), a * 64, row, hk, page);
           }
           if (++slot == slots) slot = 0, phase ^= 1;
-          if (j + 1 < w.j1) page = lookup(j + 1, row);
+          if (j + 1 < j1) page = lookup(j + 1, row);
         }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_DE + us));
+        if (++us == kUnits) us = 0, up ^= 1;
       }
       // after a failed wait, let the copies in flight land before shared memory goes
       ok = __all_sync(0xffffffffu, ok);
@@ -235,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (keys)
           for (int s = 0; s < 2; ++s) mbar_drain(bar(B_QF + s), s < qslot ? qphase ^ 1 : qphase);
       }
-    } else if (any && warp == 1) {
+    } else {
       // ------------------------------------------------------------ products
       // One elected lane does it all: the compiler then knows that a single lane
       // issues the matrix instructions (9 cycles each; from a lane chosen by its
@@ -244,7 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // instructions run in the order of their issue.  A slot of K's or V's ring
       // and of Q is freed by a commit behind the last product that reads it.
       if (elect_one()) {
-        constexpr uint32_t ID_S = idesc_16(128, 128, false, false, F16);
+        // (bit 13: A, the queries, negated, for a scale below zero)
+        const uint32_t ID_S = idesc_16(128, 128, false, false, F16) | (p.scale < 0.f ? 1u << 13 : 0u);
         constexpr uint32_t ID_PV = idesc_16(128, DP, false, true, F16);
         constexpr uint32_t HI = sdesc_hi_sw128(1024);
         constexpr uint32_t SLOT = C::TILE >> 4;  // a slot, in a descriptor's units
@@ -259,15 +326,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mma_commit_one(bar(B_S + s));
         };
-        auto pv_product = [&](uint32_t s, uint32_t b_lo, uint32_t keys, uint32_t more) {  // more: to what O_s holds
+        // O_s += P_s V (more = 0: O_s = P_s V); with `early` the first 64 keys as
+        // soon as their weights are there.
+        uint32_t pphase = 0;  // bit 2 stream + half
+        auto pv_product = [&](uint32_t s, uint32_t b_lo, uint32_t keys, uint32_t more, bool early) -> bool {
           const uint32_t d = tm + C::TM_O + s * DP, a = tm + C::TM_S + s * 128;
+          if (!wait(B_P + 2 * s + (early ? 0 : 1), (pphase >> (2 * s + (early ? 0 : 1))) & 1u)) return false;
+          tc_fence_after();
           if (keys == 128) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) mma_ts_one(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, kk > 0 ? 1u : more);
+            for (int kk = 0; kk < 4; ++kk) mma_ts_one(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, kk > 0 ? 1u : more);
+            if (early) {
+              if (!wait(B_P + 2 * s + 1, (pphase >> (2 * s + 1)) & 1u)) return false;
+              tc_fence_after();
+            }
+#pragma unroll
+            for (int kk = 4; kk < 8; ++kk) mma_ts_one(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, 1u);
           } else {
+            if (early) {
+              if (!wait(B_P + 2 * s + 1, (pphase >> (2 * s + 1)) & 1u)) return false;
+              tc_fence_after();
+            }
             for (uint32_t kk = 0; kk * 16 < keys; ++kk)
               mma_ts_one(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, kk > 0 ? 1u : more);
           }
+          pphase ^= 3u << (2 * s);
+          return true;
         };
         // The last keys' tile: products run over whole steps of 16 keys (one at
         // least), with the rows from the last key to the steps' end zeroed.
@@ -283,11 +367,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           return keys;
         };
-        auto last_of = [&](const PagedWalk& x) {  // keys from the part's last key tile on, 128 at most
-          const int held = x.q.len - (x.j1 - 1) * 128;
+        auto last_of = [&](const UnitPart& x) {  // keys from the part's last key tile on, 128 at most
+          const int held = x.len - (x.j1 - 1) * 128;
           return held < 0 ? 0u : held > 128 ? 128u : (uint32_t)held;
         };
-        uint32_t kslot = 0, kphase = 0, vslot = 0, vphase = 0, qn = 0, pphase0 = 0, pphase1 = 0;
+        uint32_t kslot = 0, kphase = 0, vslot = 0, vphase = 0, qn = 0;
         bool ok = true;
         auto next_k = [&]() {
           if (++kslot == C::NK) kslot = 0, kphase ^= 1;
@@ -297,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // A unit of two row tiles: per key tile O_0, S_0, O_1, S_1, so that each
         // stream's softmax runs beside the other's products.
-        auto two_tiles = [&](const PagedWalk& x) {
+        auto two_tiles = [&](const UnitPart& x) -> bool {
           const uint32_t tiles = (uint32_t)(x.j1 - x.j0), last = last_of(x), q0 = qn & 1u, q1 = q0 ^ 1u;
           const uint32_t a0 = q_lo + q0 * SLOT, a1 = q_lo + q1 * SLOT;
           if (!wait(B_QF + q0, (qn >> 1) & 1u) || !wait(B_QF + q1, ((qn + 1) >> 1) & 1u)) return false;
@@ -312,15 +396,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (uint32_t t = 1; t < tiles; ++t) {
             if (!wait(B_KF + kslot, kphase) || !wait(B_VF + vslot, vphase)) return false;
             const uint32_t kb = k_lo + kslot * SLOT, vb = v_lo + vslot * SLOT;
-            if (!wait(B_P, pphase0)) return false;
-            pphase0 ^= 1u;
-            tc_fence_after();
-            pv_product(0, vb, 128, more);
+            if (!pv_product(0, vb, 128, more, true)) return false;
             s_product(0, a0, kb);
-            if (!wait(B_P + 1, pphase1)) return false;
-            pphase1 ^= 1u;
-            tc_fence_after();
-            pv_product(1, vb, 128, more);
+            if (!pv_product(1, vb, 128, more, true)) return false;
             mma_commit_one(bar(B_VE + vslot));
             s_product(1, a1, kb);
             mma_commit_one(bar(B_KE + kslot));
@@ -332,35 +410,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit_one(bar(B_QE + q1));
           if (!wait(B_VF + vslot, vphase)) return false;
           const uint32_t vb = v_lo + vslot * SLOT, keys = end_keys(vslot, last);
-          if (!wait(B_P, pphase0)) return false;
-          pphase0 ^= 1u;
-          tc_fence_after();
-          pv_product(0, vb, keys, more);
+          if (!pv_product(0, vb, keys, more, true)) return false;
           mma_commit_one(bar(B_O));
-          if (!wait(B_P + 1, pphase1)) return false;
-          pphase1 ^= 1u;
-          tc_fence_after();
-          pv_product(1, vb, keys, more);
+          if (!pv_product(1, vb, keys, more, true)) return false;
           mma_commit_one(bar(B_O + 1));
           mma_commit_one(bar(B_VE + vslot));
           next_v();
           return true;
         };
         // Units of one row tile: key tile i is stream i & 1's.  The S products
-        // run two tiles ahead (ws, si), into the next such unit too where its
-        // operands have landed, so that a unit's end leaves work to do.
-        PagedWalk ws, w;
-        ws.begin(plan, start);
-        bool smore = ws.seek(plan, p0, p1);
-        w = ws;
-        uint32_t si = 0, ahead = 0, busy = 0;  // ahead: units between w's and ws's; busy: streams with an S or a P
-        auto s_ahead = [&]() {
-          while (smore && ws.width == 1 && !((busy >> (si & 1u)) & 1u)) {
+        // run two tiles ahead (unit sd, tile si), into the next such unit too
+        // where its operands have landed, so that a unit's end leaves work to do.
+        uint32_t us = 0, up = 0;                      // the unit at work
+        uint32_t sd = 0, sdp = 0, si = 0, ahead = 0;  // the S products' unit; units between the two
+        uint32_t busy = 0;                            // streams with an S or a P
+        auto s_ahead = [&]() -> bool {
+          while (!((busy >> (si & 1u)) & 1u)) {
+            // another unit's description and operands are waited for only when
+            // nothing else is left to do
+            const bool patient = busy != 0 && ahead != 0;
+            if (patient && !mbar_test(bar(B_DF + sd), sdp)) return true;
+            if (!wait(B_DF + sd, sdp)) return false;
+            const UnitPart& u = units[sd];
+            if (!u.more || u.width == 2) return true;
             const uint32_t qs = qn & 1u, qp = (qn >> 1) & 1u;
-            // another unit's operands are waited for only when nothing else is left to do
-            if (busy != 0 && ahead != 0 &&
-                !((si > 0 || mbar_test(bar(B_QF + qs), qp)) && mbar_test(bar(B_KF + kslot), kphase)))
-              break;
+            if (patient && !((si > 0 || mbar_test(bar(B_QF + qs), qp)) && mbar_test(bar(B_KF + kslot), kphase)))
+              return true;
             if (si == 0 && !wait(B_QF + qs, qp)) return false;
             if (!wait(B_KF + kslot, kphase)) return false;
             tc_fence_after();
@@ -368,27 +443,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             mma_commit_one(bar(B_KE + kslot));
             next_k();
             busy |= 1u << (si & 1u);
-            if ((int)++si == ws.j1 - ws.j0) {
+            if ((int)++si == u.j1 - u.j0) {
               mma_commit_one(bar(B_QE + qs));
               ++qn;
               si = 0;
               ++ahead;
-              smore = ws.next(plan) && ws.seek(plan, p0, p1);
+              if (++sd == kUnits) sd = 0, sdp ^= 1u;
             }
           }
           return true;
         };
-        auto one_tile = [&](const PagedWalk& x) {
+        auto one_tile = [&](const UnitPart& x) -> bool {
           const uint32_t tiles = (uint32_t)(x.j1 - x.j0), last = last_of(x);
           for (uint32_t i = 0; i < tiles; ++i) {
             const uint32_t s = i & 1u;
             if (!s_ahead() || !wait(B_VF + vslot, vphase)) return false;
             const uint32_t keys = i + 1 == tiles ? end_keys(vslot, last) : 128u;
-            if (!wait(B_P + s, s ? pphase1 : pphase0)) return false;
-            pphase0 ^= s ^ 1u;
-            pphase1 ^= s;
-            tc_fence_after();
-            pv_product(s, v_lo + vslot * SLOT, keys, i < 2 ? 0u : 1u);
+            if (!pv_product(s, v_lo + vslot * SLOT, keys, i < 2 ? 0u : 1u, false)) return false;
             mma_commit_one(bar(B_VE + vslot));
             if (i + 2 >= tiles) mma_commit_one(bar(B_O + s));
             next_v();
@@ -397,20 +468,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           --ahead;
           return true;
         };
-        for (bool more = smore; ok && more; more = w.next(plan) && w.seek(plan, p0, p1)) {
-          if (w.width == 2) {
-            ok = two_tiles(w);
-            smore = ws.next(plan) && ws.seek(plan, p0, p1);
+        while (ok && wait(B_DF + us, up)) {
+          const UnitPart& u = units[us];
+          if (!u.more) break;
+          if (u.width == 2) {
+            ok = two_tiles(u);
+            if (++sd == kUnits) sd = 0, sdp ^= 1u;
           } else {
-            ok = one_tile(w);
+            ok = one_tile(u);
           }
+          if (!ok) break;
+          mbar_arrive(bar(B_DE + us));
+          if (++us == kUnits) us = 0, up ^= 1u;
         }
         mma_commit_one(bar(B_FIN));
         mbar_drain(bar(B_FIN), 0);
       }
       __syncwarp();
-    } else if (warp == 3 && lane == 0) {
-      paged_note_cut(plan, p.parts, start, p0, p1, border, (int)blockIdx.x);
     }
   } else {
     reg_alloc();
@@ -419,49 +493,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tm + lane_off + C::TM_S + s * 128, tO = tm + lane_off + C::TM_O + s * DP;
-    // weights 2^(s c1 - m); a scale below zero turns the scores' signs, and a
-    // zero one is taken as one too small to tell the scores apart (0 times a
-    // masked score would be NaN)
-    const bool neg = p.scale < 0.f;
+    // weights 2^(s c1 - m) (the S products carry the scale's sign); a scale of
+    // zero is taken as one too small to tell the scores apart (0 times a masked
+    // score would be NaN)
     const float c1 = fmaxf(fabsf(p.scale) * kLog2e, 1e-37f);
     constexpr float kBias = F16 ? 7.f : 0.f;
     const int i_row = r / plan.gw, g_row = r - i_row * plan.gw;
     uint32_t sphase = 0, ophase = 0, mphase = 0;
-    bool ok = true, more = any;
-    PagedWalk w;
-    if (any) {
-      w.begin(plan, start);
-      more = w.seek(plan, p0, p1);
-    }
-    for (; more; more = w.next(plan) && w.seek(plan, p0, p1)) {
+    uint32_t us = 0, up = 0;
+    bool ok = true;
+    auto next_unit = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_DE + us));
+      if (++us == kUnits) us = 0, up ^= 1u;
+    };
+    for (;;) {
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait_asleep(bar(B_DF + us), up, abort_flag, err)))) break;
+      const UnitPart& u = units[us];
+      if (!u.more) break;
       {
-        const bool wide = w.width == 2;
-        const int n = w.j1 - w.j0;
-        const int hk = w.at.head / plan.gblocks, gb = w.at.head - hk * plan.gblocks;
-        const int token = w.at.i * plan.nt * 2 + (wide ? s * plan.nt : 0) + i_row;
-        const int g = gb * plan.gw + g_row;
-        const bool row_ok = i_row < plan.nt && token < w.q.n && g < plan.G;
+        const bool wide = u.width == 2;
+        const int n = u.j1 - u.j0;
+        const int token = u.token0 + (wide ? s * plan.nt : 0) + i_row;
+        const bool row_ok = i_row < plan.nt && token < u.n && u.g0 + g_row < plan.G;
         const bool active = __any_sync(0xffffffffu, row_ok);
-        int last = w.q.len - 1;  // last key the row sees
-        if (plan.causal && w.q.last0 + token < last) last = w.q.last0 + token;
+        int last = u.len - 1;  // last key the row sees
+        if (plan.causal && u.last0 + token < last) last = u.last0 + token;
         if (!row_ok) last = -1;
+        last -= u.j0 * 128;  // counted from the part's first key
         float m_run = -INFINITY, l = 0.f;
         for (int t = wide ? 0 : s; t < n; t += wide ? 1 : 2) {
           if (!(ok = __all_sync(0xffffffffu, mbar_wait_asleep(bar(B_S + s), sphase, abort_flag, err)))) break;
           sphase ^= 1;
           if (active) {
             tc_fence_after();
-            const int k0 = (w.j0 + t) * 128;
+            const int k0 = t * 128;
             uint32_t x[4][32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, x[c]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld_wait(x[c]);
             auto sv = [&](int e) -> uint32_t& { return x[e >> 5][e & 31]; };
-            if (neg) {
-#pragma unroll
-              for (int e = 0; e < 128; ++e) sv(e) ^= 0x80000000u;
-            }
             if (__any_sync(0xffffffffu, row_ok && k0 + 127 > last)) {
               const int lim = last - k0;
 #pragma unroll
@@ -511,14 +583,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pk[c] = pack2<F16>(a, b);
               }
               tmem_st32(tS + h * 32, pk);
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(B_P + 2 * s + h));
             }
             const float2 total = split_f32(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])));
             l += total.x + total.y;
-            tmem_st_wait();
-            tc_fence_before();
+          } else if (lane < 2) {
+            mbar_arrive(bar(B_P + 2 * s + lane));
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(B_P + s));
         }
         if (!ok) break;
         // ---- the unit's end: O / l and the log-sum-exp, or partial results
@@ -538,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(bar(B_ML));
             if (!(ok = __all_sync(0xffffffffu, mbar_wait_asleep(bar(B_MD), mphase, abort_flag, err)))) break;
             mphase ^= 1;
+            next_unit();
             continue;
           }
           if (!(ok = __all_sync(0xffffffffu, mbar_wait_asleep(bar(B_ML), mphase, abort_flag, err)))) break;
@@ -559,12 +634,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (active) {
           tc_fence_after();
           const bool two = !wide && n > 1;
-          const int64_t tok = w.q.s0 + token, head = (int64_t)hk * plan.G + g;
-          const bool whole = w.whole();
+          const int64_t tok = u.s0 + token, head = (int64_t)u.hk * plan.G + u.g0 + g_row;
+          const bool whole = u.slot < 0;
           const float inv = lt == 0.f ? 0.f : whole ? 1.f / lt : 1.f;
           const float a0 = l == 0.f ? 0.f : f0 * inv, a1 = f1 * inv;
           T* o = static_cast<T*>(p.o) + (tok * p.H + head) * p.DV;
-          const int64_t prow = (int64_t)w.slot((int)blockIdx.x) * 256 + (wide ? s * 128 : 0) + r;
+          const int64_t prow = (int64_t)u.slot * 256 + (wide ? s * 128 : 0) + r;
           float* part = p.parts.out + prow * DP;
 #pragma unroll 1
           for (int c0 = 0; c0 < DP; c0 += 32) {
@@ -610,6 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!wide) mbar_arrive(bar(B_MD));
       }
+      next_unit();
     }
   }
 
