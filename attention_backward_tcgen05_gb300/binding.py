@@ -289,6 +289,10 @@ def fab_last_device_error(stream=None) -> int:
 # ------------------------------------------------------------------ norms + rotation, paged cache
 
 
+# A small call's time is its host's: these checks ask each tensor for each
+# property once.
+
+
 def _here(*tensors):
     """All the given tensors (None: skipped) are on the current device, which
     is where libfab launches; returns that device's index."""
@@ -300,10 +304,10 @@ def _here(*tensors):
 
 
 def _ptr(t, name, dtype, shape):
-    """Address of a contiguous tensor of that dtype and shape (None: 0)."""
+    """Address of a contiguous tensor of that dtype and shape (None: null)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, {dtype}, of shape {tuple(shape)}; "
                          f"got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
     return t.data_ptr()
@@ -313,7 +317,7 @@ def _ld(t, name, dtype, shape):
     """Elements between the rows of consecutive tokens of t, of shape
     (..., tokens, heads, width): heads contiguous inside a row, rows evenly
     spaced over all tokens."""
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     st = t.stride()
     heads, width = shape[-2], shape[-1]
@@ -328,19 +332,18 @@ def _ld(t, name, dtype, shape):
     return st[-3] if n > 1 else heads * width
 
 
-def _check_tables(cos, sin, wq, wk, DK, dtype):
-    """(rot, P) of the tables (None, None: no rotation)."""
-    rot, P = 0, 0
-    if cos is not None:
-        P, half = cos.shape
-        rot = 2 * half
-        _ptr(cos, "cos", torch.float32, cos.shape)
+def _tables(cos, sin, wq, wk, DK, dtype):
+    """(rot, P, addresses of wq, wk, cos, sin); without cos and sin no rotation."""
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
-    _ptr(sin, "sin", torch.float32, cos.shape if cos is not None else None)
-    _ptr(wq, "wq", dtype, (DK,))
-    _ptr(wk, "wk", dtype, (DK,))
-    return rot, P
+    w = _ptr(wq, "wq", dtype, (DK,)), _ptr(wk, "wk", dtype, (DK,))
+    if cos is None:
+        return 0, 0, (*w, None, None)
+    shape = cos.shape
+    if len(shape) != 2:
+        raise ValueError("cos, sin must be 2-D: (P,rot/2)")
+    f32 = torch.float32
+    return 2 * shape[1], shape[0], (*w, _ptr(cos, "cos", f32, shape), _ptr(sin, "sin", f32, shape))
 
 
 def _addr(t):
@@ -356,18 +359,24 @@ def _raw_stream(stream, dev):
 def fab_qk_norm_rope(q, k, v, wq, wk, cos, sin, pos, eps, interleaved, q_out, k_out, v_out, stream=None):
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q, k must be 4-D: (B,N,H,DK), (B,N,Hkv,DK)")
-    B, N, H, DK = q.shape
-    Hkv, DV = k.shape[2], DK if v is None else v.shape[-1]
+    qs = q.shape
+    B, N, H, DK = qs
+    Hkv = k.shape[2]
     dt = q.dtype
+    code = dtype_code(q)
     dev = _here(q, k, v, wq, wk, cos, sin, pos, q_out, k_out, v_out)
-    rot, P = _check_tables(cos, sin, wq, wk, DK, dt)
-    dims = fab_rope_dims(B, N, H, Hkv, DK, DV, rot, P, _ld(q, "q", dt, (B, N, H, DK)),
-                         _ld(k, "k", dt, (B, N, Hkv, DK)), 0 if v is None else _ld(v, "v", dt, (B, N, Hkv, DV)))
+    rot, P, tables = _tables(cos, sin, wq, wk, DK, dt)
+    DV, ldv, vp, vo = DK, 0, None, None
+    if v is not None:
+        DV = v.shape[-1]
+        ldv, vp = _ld(v, "v", dt, (B, N, Hkv, DV)), v.data_ptr()
+    if v_out is not None:
+        vo = _ptr(v_out, "v_out", dt, (B, Hkv, N, DV))
+    dims = fab_rope_dims(B, N, H, Hkv, DK, DV, rot, P, _ld(q, "q", dt, qs), _ld(k, "k", dt, (B, N, Hkv, DK)), ldv)
     _check(lib().fab_qk_norm_rope(
-        q.data_ptr(), k.data_ptr(), _addr(v), _addr(wq), _addr(wk), _addr(cos), _addr(sin),
-        _ptr(pos, "pos", torch.int32, (B, N)), float(eps), int(bool(interleaved)), dtype_code(q), ctypes.byref(dims),
-        _ptr(q_out, "q_out", dt, (B, H, N, DK)), _ptr(k_out, "k_out", dt, (B, Hkv, N, DK)),
-        _ptr(v_out, "v_out", dt, (B, Hkv, N, DV)), _raw_stream(stream, dev)), "fab_qk_norm_rope")
+        q.data_ptr(), k.data_ptr(), vp, *tables, _ptr(pos, "pos", torch.int32, (B, N)), eps, 1 if interleaved else 0,
+        code, ctypes.byref(dims), _ptr(q_out, "q_out", dt, (B, H, N, DK)), _ptr(k_out, "k_out", dt, (B, Hkv, N, DK)),
+        vo, _raw_stream(stream, dev)), "fab_qk_norm_rope")
 
 
 def fab_qk_norm_rope_backward_workspace_bytes(dims: fab_rope_dims) -> int:
@@ -391,14 +400,14 @@ def fab_qk_norm_rope_backward(dq, dk, dv, q, k, wq, wk, cos, sin, pos, eps, inte
         raise ValueError("dq, dk must be 4-D: (B,H,N,DK), (B,Hkv,N,DK)")
     B, H, N, DK = dq.shape
     dev = _here(dq, dk, dv, q, k, wq, wk, cos, sin, pos, workspace, gq, gk, gv, gwq, gwk)
-    rot, P = _check_tables(cos, sin, wq, wk, DK, gq.dtype)
+    rot, P, tables = _tables(cos, sin, wq, wk, DK, gq.dtype)
     dims = _rope_backward_dims(dq, dk, dv, q, k, wq, wk, rot, P, gq, gk, gv)
     f32 = torch.float32
     _check(lib().fab_qk_norm_rope_backward(
         _ptr(dq, "dq", f32, dq.shape), _ptr(dk, "dk", f32, (B, dims.Hkv, N, DK)),
         _ptr(dv, "dv", f32, (B, dims.Hkv, N, dims.DV)), None if wq is None else q.data_ptr(),
-        None if wk is None else k.data_ptr(), _addr(wq), _addr(wk), _addr(cos), _addr(sin),
-        _ptr(pos, "pos", torch.int32, (B, N)), float(eps), int(bool(interleaved)), dtype_code(gq),
+        None if wk is None else k.data_ptr(), *tables,
+        _ptr(pos, "pos", torch.int32, (B, N)), eps, 1 if interleaved else 0, dtype_code(gq),
         ctypes.byref(dims), _addr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(), gq.data_ptr(), gk.data_ptr(),
         _addr(gv), _ptr(gwq, "gwq", f32, (DK,)), _ptr(gwk, "gwk", f32, (DK,)), _raw_stream(stream, dev)),
@@ -431,13 +440,12 @@ def fab_paged_append(q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, 
     dims = _paged_dims(H, T, k_cache, v_cache, starts, lens, table)
     if k_cache.dtype != dt:
         raise ValueError(f"k_cache must be {dt}, got {k_cache.dtype}")
-    dims.rot, dims.P = _check_tables(cos, sin, wq, wk, DK, dt)
+    dims.rot, dims.P, tables = _tables(cos, sin, wq, wk, DK, dt)
     dims.ldq = _ld(q, "q", dt, (T, H, dims.DK))
     dims.ldk = _ld(k, "k", dt, (T, dims.Hkv, DK))
     dims.ldv = _ld(v, "v", dt, (T, dims.Hkv, dims.DV))
     _check(lib().fab_paged_append(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(wq), _addr(wk), _addr(cos), _addr(sin), float(eps),
-        int(bool(interleaved)), starts.data_ptr(), lens.data_ptr(), table.data_ptr(), dtype_code(q),
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), *tables, eps, 1 if interleaved else 0, starts.data_ptr(), lens.data_ptr(), table.data_ptr(), dtype_code(q),
         ctypes.byref(dims), _ptr(q_out, "q_out", dt, (T, H, DK)), k_cache.data_ptr(), v_cache.data_ptr(),
         _raw_stream(stream, dev)), "fab_paged_append")
 
@@ -484,9 +492,10 @@ def qk_norm_rope(q, k, v, wq=None, wk=None, cos=None, sin=None, pos=None, eps=1e
         raise ValueError("q, k must be 4-D: (B,N,H,DK), (B,N,Hkv,DK)")
     B, N, H, DK = q.shape
     with _on(stream):
-        qo = q.new_empty((B, H, N, DK))
-        ko = q.new_empty((B, k.shape[2], N, DK))
-        vo = None if v is None else q.new_empty((B, v.shape[2], N, v.shape[3]))
+        dt, dev = q.dtype, q.device
+        qo = torch.empty((B, H, N, DK), dtype=dt, device=dev)
+        ko = torch.empty((B, k.shape[2], N, DK), dtype=dt, device=dev)
+        vo = None if v is None else torch.empty((B, v.shape[2], N, v.shape[3]), dtype=dt, device=dev)
         fab_qk_norm_rope(q, k, v, wq, wk, cos, sin, pos, eps, interleaved, qo, ko, vo, stream)
     return qo, ko, vo
 
@@ -528,7 +537,7 @@ def paged_append(q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cach
     queries (T,H,DK), normalised and rotated as qk_norm_rope does; rows of
     padding tokens are left as allocated."""
     with _on(stream):
-        qo = q.new_empty(q.shape)
+        qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         fab_paged_append(q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, qo, k_cache, v_cache, stream)
     return qo
 
@@ -546,8 +555,9 @@ def paged_attention(q, k_cache, v_cache, starts, lens, table, causal=True, scale
     tokens are left as allocated."""
     scale = q.shape[-1] ** -0.5 if scale is None else scale
     with _on(stream):
-        o = q.new_empty((q.shape[0], q.shape[1], v_cache.shape[-1]))
-        lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+        T, H, dev = q.shape[0], q.shape[1], q.device
+        o = torch.empty((T, H, v_cache.shape[-1]), dtype=q.dtype, device=dev)
+        lse = torch.empty((H, T), dtype=torch.float32, device=dev)
         ws = alloc_paged(q, k_cache, v_cache, table)
         fab_paged_attention(q, k_cache, v_cache, starts, lens, table, causal, scale, ws, o, lse, stream)
     return o, lse
