@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(kWarps * 32) rope_rows_kernel(const RopeProble
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) rope_rows_backward_kernel(const RopeProblem p, int nq, int nk, int nv) {
   __shared__ float acc_s[kWarps][kMaxWidth];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int blk = (int)blockIdx.x;
   const int kind = blk < nq ? 0 : blk < nq + nk ? 1 : 2;
@@ -482,9 +483,10 @@ __global__ void __launch_bounds__(kVecThreads, sizeof(T) == 4 ? 4 : 5) rope_vec_
 // heads), the next nk k's, the rest v's; each of the former leaves its sum of
 // dw in partial[block].
 template <typename T, int L, bool IL>
-__global__ void __launch_bounds__(kVecThreads, sizeof(T) == 4 ? 3 : 4) rope_vec_backward_kernel(const RopeProblem p, int hb, int nq, int nk,
+__global__ void __launch_bounds__(kVecThreads, 3) rope_vec_backward_kernel(const RopeProblem p, int hb, int nq, int nk,
                                                                            int nv) {
   __shared__ float acc_s[kVecThreads / 32][16 * L];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int sub = threadIdx.x & (L - 1), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int blk = (int)blockIdx.x;
   const int kind = blk < nq ? 0 : blk < nq + nk ? 1 : 2;
@@ -511,6 +513,7 @@ __global__ void __launch_bounds__(kVecThreads, sizeof(T) == 4 ? 3 : 4) rope_vec_
     if (ca >= 0) wa.load(w0 + ca * 8);
     if (cb >= 0) wb.load(w0 + cb * 8);
   }
+  constexpr int A = sizeof(T) == 4 ? 1 : 2;  // rows on their way
   const float inv_d = 1.f / (float)D;
   const int64_t tokens = p.B * p.N, tblocks = (tokens + kVecThreads / L - 1) / (kVecThreads / L);
   const int64_t hblocks = (heads + hb - 1) / hb, items = tblocks * hblocks, dstep = p.N * D;
@@ -524,31 +527,36 @@ __global__ void __launch_bounds__(kVecThreads, sizeof(T) == 4 ? 3 : 4) rope_vec_
     const float* dy = dy0 + (b * heads * p.N + n) * D;
     const T* x = x0 + t * ldx;
     T* g = g0 + t * ldg;
-    Raw8<float> nga, ngb;
-    Raw8<T> nxa, nxb;
-    auto fetch = [&](int j) {
-      nga.zero();
-      ngb.zero();
-      nxa.zero();
-      nxb.zero();
-      if (oka) nga.load(dy + j * dstep + ca * 8);
-      if (okb) ngb.load(dy + j * dstep + cb * 8);
+    Raw8<float> nga[A], ngb[A];
+    Raw8<T> nxa[A], nxb[A];
+    auto fetch = [&](int j, int u) {
+      nga[u].zero();
+      ngb[u].zero();
+      nxa[u].zero();
+      nxb[u].zero();
+      if (j >= j1) return;
+      if (oka) nga[u].load(dy + j * dstep + ca * 8);
+      if (okb) ngb[u].load(dy + j * dstep + cb * 8);
       if (norm) {
-        if (oka) nxa.load(x + j * D + ca * 8);
-        if (okb) nxb.load(x + j * D + cb * 8);
+        if (oka) nxa[u].load(x + j * D + ca * 8);
+        if (okb) nxb[u].load(x + j * D + cb * 8);
       }
     };
-    fetch(j0);
+#pragma unroll
+    for (int u = 0; u < A; ++u) fetch(j0 + u, u);
     float c[8], s[8];  // (a lane past the last token turns zeros: by something finite)
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
     if (row_ok && half > 0) load_turn<IL>(p.cos, p.sin, place_of(p, t).pos, half, ca, cb, ta, tb, c, s);
-    for (int j = j0; j < j1; ++j) {
+    for (int jj = j0; jj < j1; jj += A)
+#pragma unroll
+    for (int u = 0; u < A; ++u) {
+      const int j = jj + u;
       float ga[8], gb[8];
-      nga.get(ga);
-      ngb.get(gb);
-      const Raw8<T> rxa = nxa, rxb = nxb;
-      if (j + 1 < j1) fetch(j + 1);
+      nga[u].get(ga);
+      ngb[u].get(gb);
+      const Raw8<T> rxa = nxa[u], rxb = nxb[u];
+      fetch(j + A, u);
       if (kind != 2) turn<IL, true>(ga, gb, c, s, ta, tb);
       if (norm) {
         float xa[8], xb[8], w[8];
@@ -582,8 +590,8 @@ __global__ void __launch_bounds__(kVecThreads, sizeof(T) == 4 ? 3 : 4) rope_vec_
           gb[i] = r * (gb[i] - xb[i] * dot);
         }
       }
-      if (oka) store8(g + j * D + ca * 8, ga);
-      if (okb) store8(g + j * D + cb * 8, gb);
+      if (oka && j < j1) store8(g + j * D + ca * 8, ga);
+      if (okb && j < j1) store8(g + j * D + cb * 8, gb);
     }
   }
   if (!norm) return;
@@ -614,6 +622,7 @@ __global__ void __launch_bounds__(kVecThreads, sizeof(T) == 4 ? 3 : 4) rope_vec_
 __global__ void __launch_bounds__(1024) rope_partial_sum_kernel(const float* partial, int nq, int nk, int D, float* gwq,
                                                                 float* gwk) {
   __shared__ float sum_s[32][33];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the rows are still being worked on
   float* gw = blockIdx.y == 0 ? gwq : gwk;
   if (gw == nullptr) return;
   const int rows = blockIdx.y == 0 ? nq : nk;
@@ -683,7 +692,7 @@ template <typename T, int L>
 cudaError_t rope_vec_backward(const RopeProblem& p, int* rows_q, int* rows_k, cudaStream_t s) {
   const int64_t tb = (p.B * p.N + kVecThreads / L - 1) / (kVecThreads / L);
   int64_t hb = 32;
-  while (hb > 1 && tb * ((p.H + hb - 1) / hb + (p.Hkv + hb - 1) / hb * 2) < 1216) hb /= 2;
+  while (hb > 1 && tb * ((p.H + hb - 1) / hb + (p.Hkv + hb - 1) / hb * 2) < 456) hb /= 2;
   // blocks in the ratio of the operands' bytes, about 8 an SM
   auto blocks = [&](int64_t heads, int64_t most) {
     const int64_t items = tb * ((heads + hb - 1) / hb);
@@ -736,9 +745,17 @@ cudaError_t rope_backward_t(const RopeProblem& p, cudaStream_t s) {
     }
   }
   if (e != cudaSuccess || (p.gwq == nullptr && p.gwk == nullptr)) return e;
-  rope_partial_sum_kernel<<<dim3((unsigned)((p.DK + 31) / 32), 2), 1024, 0, s>>>(p.partial, nq, nk, (int)p.DK, p.gwq,
-                                                                                 p.gwk);
-  return cudaPeekAtLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((p.DK + 31) / 32), 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rope_partial_sum_kernel, static_cast<const float*>(p.partial), nq, nk, (int)p.DK,
+                            p.gwq, p.gwk);
 }
 
 }  // namespace
