@@ -290,7 +290,7 @@ struct PagedCut {
   int last;       // the last CTA that holds a part of the unit in slot 2c + 1; 0: no such unit
   int s0, n;      // the unit: its sequence's tokens,
   int head, token0, rows;  // its head and tokens, how many rows
-  int pad;
+  int gaps;       // 1: pieces shorter than a key tile's work, some CTAs up to `last` may hold no part
 };
 
 // Partial results: rows of `dp` floats, and (maximum in log2 units, sum) pairs.
@@ -325,6 +325,7 @@ FAB_DEV void paged_note_part(const PagedPlan& p, const PagedWalk& w, const Paged
     cut->head = w.at.head;
     cut->token0 = w.at.i * p.nt * p.tiles;
     cut->rows = w.width * p.nt * p.gw;
+    cut->gaps = border.q < 4;
   }
 }
 
@@ -368,7 +369,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
           const int k = k0 + u;
           ml[u] = make_float2(-INFINITY, 0.f);
           v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (k <= cut.last && (k == c || parts.cuts[k].head_part)) {
+          if (k <= cut.last && (k == c || !cut.gaps || parts.cuts[k].head_part)) {
             const int64_t at = (int64_t)(k == c ? 2 * k + 1 : 2 * k) * parts.rows + row;
             ml[u] = parts.ml[at];
             v[u] = *reinterpret_cast<const float4*>(parts.out + at * parts.dp + c0);
@@ -397,23 +398,35 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
   }
 }
 
-// Enqueues the combine kernel behind an attention kernel of `grid` CTAs.
-template <typename T>
-cudaError_t launch_combine(const PagedPlan& plan, const PagedParts& parts, int grid, int DV, int H, T* o, float* lse,
-                           cudaStream_t s) {
-  if (grid < 2) return cudaSuccess;  // nothing is cut
-  const int rows = plan.tiles * plan.nt * plan.gw;
+// Launches a kernel that may start while the one before it in the stream still
+// runs, and waits for that one itself (griddepcontrol.wait) before it touches
+// memory: its launch and its first instructions cost no time of their own.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)((rows + 31) / 32));
-  cfg.blockDim = dim3(kCombineThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  if (parts.dp <= 64) return cudaLaunchKernelEx(&cfg, paged_combine_kernel<T, 16>, plan, parts, DV, H, o, lse);
-  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<T, 32>, plan, parts, DV, H, o, lse);
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+// Enqueues the combine kernel behind an attention kernel of `grid` CTAs.
+template <typename T>
+cudaError_t launch_combine(const PagedPlan& plan, const PagedParts& parts, int grid, int DV, int H, T* o, float* lse,
+                           cudaStream_t s) {
+  if (grid < 2) return cudaSuccess;  // nothing is cut
+  const int rows = plan.tiles * plan.nt * plan.gw;
+  const int per = kCombineThreads / (parts.dp <= 64 ? 16 : 32);  // rows of a block at once
+  const dim3 g((unsigned)(grid - 1), (unsigned)((rows + per - 1) / per));
+  if (parts.dp <= 64)
+    return launch_early(paged_combine_kernel<T, 16>, g, kCombineThreads, 0, s, plan, parts, DV, H, o, lse);
+  return launch_early(paged_combine_kernel<T, 32>, g, kCombineThreads, 0, s, plan, parts, DV, H, o, lse);
 }
 
 }  // namespace fab

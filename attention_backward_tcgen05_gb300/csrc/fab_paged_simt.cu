@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
   __shared__ PagedShared sh;
   const PagedPlan& plan = p.plan;
   const int lane = (int)lane_id(), warp = (int)warp_id();
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (launched early: lengths and operands from here on)
   if (blockIdx.x == 0) check_starts(plan.starts, plan.B, plan.T, (int)threadIdx.x, kThreads, &g_err_paged);
   int64_t mine;
   paged_total<kThreads>(plan, &sh, &mine);
@@ -384,8 +385,7 @@ cudaError_t launch_r(const PagedProblem& pr, int sms, cudaStream_t s) {
   if (units < grid && tiles < grid && units * tiles < grid) grid = (int)(units * tiles);
   cudaError_t err = cudaFuncSetAttribute(paged_simt_kernel<T, R, CPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
-  paged_simt_kernel<T, R, CPL><<<(unsigned)grid, kThreads, smem, s>>>(p);
-  err = cudaPeekAtLastError();
+  err = launch_early(paged_simt_kernel<T, R, CPL>, dim3((unsigned)grid), kThreads, (size_t)smem, s, p);
   if (err != cudaSuccess) return err;
   return launch_combine<T>(p.plan, p.parts, grid, p.DV, p.H, static_cast<T*>(pr.o), pr.lse, s);
 }

@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tmem_holder), 512);
     tmem_relinquish();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (launched early: lengths and operands from here on)
   if (blockIdx.x == 0) check_starts(plan.starts, plan.B, plan.T, (int)threadIdx.x, kThreads, err);
   int64_t mine;
   paged_total<kThreads>(plan, sh, &mine);
@@ -769,8 +770,7 @@ cudaError_t launch_d(const PagedProblem& pr, int sms, cudaStream_t s) {
   cudaError_t err =
       cudaFuncSetAttribute(paged_tc_kernel<DP, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (err != cudaSuccess) return err;
-  paged_tc_kernel<DP, F16><<<(unsigned)grid, kThreads, C::SMEM, s>>>(mq, mk, mv, p);
-  err = cudaPeekAtLastError();
+  err = launch_early(paged_tc_kernel<DP, F16>, dim3((unsigned)grid), kThreads, C::SMEM, s, mq, mk, mv, p);
   if (err != cudaSuccess) return err;
   return launch_combine<T>(p.plan, p.parts, grid, (int)pr.DV, (int)pr.H, static_cast<T*>(pr.o), pr.lse, s);
 }

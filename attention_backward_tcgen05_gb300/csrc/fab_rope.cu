@@ -375,6 +375,7 @@ template <typename T, int L, bool IL>
 __global__ void __launch_bounds__(kVecThreads, sizeof(T) == 4 ? 4 : 5) rope_vec_kernel(const RopeProblem p, int hb,
                                                                                      int bq, int bk) {
   constexpr int U = sizeof(T) == 4 ? 1 : 2;  // rows a step
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (p.starts != nullptr && blockIdx.x == 0 && blockIdx.y == 0)
     check_starts(p.starts, p.seqs, p.N, (int)threadIdx.x, (int)blockDim.x, &g_err_rope);
   const int sub = threadIdx.x & (L - 1);
