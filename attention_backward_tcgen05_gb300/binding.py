@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -296,10 +297,14 @@ def fab_last_device_error(stream=None) -> int:
 def _here(*tensors):
     """All the given tensors (None: skipped) are on the current device, which
     is where libfab launches; returns that device's index."""
-    dev = torch.cuda.current_device()
+    dev = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+            raise ValueError(f"tensors on {tensors[0].device} and {t.device}")
+    if dev < 0:
+        raise ValueError("the tensors must be CUDA tensors")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
     return dev
 
 
@@ -484,6 +489,16 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
+@functools.lru_cache(maxsize=256)
+def _rope_workspace(B, N, H, Hkv, DK):
+    return max(fab_qk_norm_rope_backward_workspace_bytes(fab_rope_dims(B, N, H, Hkv, DK, DK)), 16)
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_workspace(dtype, *dims):
+    return max(fab_paged_attention_workspace_bytes(fab_paged_dims(*dims), dtype), 16)
+
+
 def qk_norm_rope(q, k, v, wq=None, wk=None, cos=None, sin=None, pos=None, eps=1e-6, interleaved=False, stream=None):
     """Projection rows q (B,N,H,DK), k (B,N,Hkv,DK), v (B,N,Hkv,DV) or None to
     what forward() takes: q (B,H,N,DK), k (B,Hkv,N,DK) normalised per head
@@ -524,8 +539,7 @@ def qk_norm_rope_backward(dq, dk, dv, q, k, wq=None, wk=None, cos=None, sin=None
         gwk = None if wk is None else torch.empty((DK,), dtype=torch.float32, device=dq.device)
         ws = None
         if wq is not None or wk is not None:
-            wsb = fab_qk_norm_rope_backward_workspace_bytes(fab_rope_dims(B, N, H, Hkv, DK, DK))
-            ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dq.device)
+            ws = torch.empty(_rope_workspace(B, N, H, Hkv, DK), dtype=torch.uint8, device=dq.device)
         fab_qk_norm_rope_backward(dq, dk, dv, q, k, wq, wk, cos, sin, pos, eps, interleaved, ws, gq, gk, gv, gwq, gwk,
                                   stream)
     return gq, gk, gv, gwq, gwk
@@ -544,10 +558,10 @@ def paged_append(q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cach
 
 def alloc_paged(q, k_cache, v_cache, table):
     """A workspace (uint8 tensor) for fab_paged_attention calls of these sizes."""
-    dims = fab_paged_dims(table.shape[0], q.shape[0], q.shape[1], k_cache.shape[1], k_cache.shape[3], v_cache.shape[3],
-                          k_cache.shape[2], k_cache.shape[0], table.shape[1])
-    wsb = fab_paged_attention_workspace_bytes(dims, dtype_code(q))
-    return torch.empty(max(wsb, 16), dtype=torch.uint8, device=q.device)
+    pages, Hkv, page, DK = k_cache.shape
+    B, max_pages = table.shape
+    wsb = _paged_workspace(dtype_code(q), B, q.shape[0], q.shape[1], Hkv, DK, v_cache.shape[3], page, pages, max_pages)
+    return torch.empty(wsb, dtype=torch.uint8, device=q.device)
 
 
 def paged_attention(q, k_cache, v_cache, starts, lens, table, causal=True, scale=None, stream=None):

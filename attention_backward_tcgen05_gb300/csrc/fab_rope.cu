@@ -679,8 +679,9 @@ cudaError_t rope_vec(const RopeProblem& p, cudaStream_t s) {
   // heads a CTA walks over: as many as leave the SMs a few CTAs each
   int64_t hb = 32;
   while (hb > 1 && gx * blocks(hb) < 1216) hb /= 2;
+  while (blocks(hb) > 65535) hb *= 2;  // (a grid's limit)
   const int64_t bq = (p.H + hb - 1) / hb, bk = (p.Hkv + hb - 1) / hb;
-  if (gx > 2147483647ll || blocks(hb) > 65535) return cudaErrorInvalidValue;
+  if (gx > 2147483647ll) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)gx, (unsigned)blocks(hb));
   if (p.interleaved)
     rope_vec_kernel<T, L, true><<<grid, kVecThreads, 0, s>>>(p, (int)hb, (int)bq, (int)bk);

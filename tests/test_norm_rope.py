@@ -224,6 +224,17 @@ def test_widths_past_256_are_unsupported():
     assert call_backward(wide) == binding.FAB_ERR_UNSUPPORTED
 
 
+def test_binding_refuses_what_does_not_fit():
+    q, k, v = torch.zeros(2, 5, 4, 64), torch.zeros(2, 5, 2, 64), torch.zeros(2, 5, 2, 64)
+    for args in ((q, k, v), (q[0], k, v), (q, k[0], v)):  # CPU tensors, ranks
+        with pytest.raises(ValueError):
+            binding.qk_norm_rope(*args)
+    with pytest.raises(ValueError):
+        binding.qk_norm_rope_backward(q[0], k, v, q, k)
+    with pytest.raises(ValueError):
+        binding.qk_norm_rope_backward(q.transpose(1, 2), k.transpose(1, 2), None, q, k)
+
+
 # ------------------------------------------------------------------ GPU
 
 
@@ -322,6 +333,30 @@ def test_a_position_out_of_the_tables_is_reported(gpu):
         keep = torch.ones(a.shape[0], a.shape[2], dtype=torch.bool)
         keep[1, 3] = keep[0, 5] = False
         assert torch.equal(a.transpose(1, 2).cpu()[keep], b.transpose(1, 2).cpu()[keep])
+
+
+@pytest.mark.gpu
+def test_operands_that_do_not_match_are_refused(gpu):
+    x = make("bf16_d128")
+    a = dict(q=x["q"], k=x["k"], v=x["v"], wq=x["wq"], wk=x["wk"], cos=x["cos"], sin=x["sin"], pos=x["pos"])
+    for bad in (dict(k=x["k"].half()), dict(k=x["k"][:, :5]), dict(v=x["v"][:1]), dict(wq=x["wq"].float()),
+                dict(wq=x["wq"][:5]), dict(cos=x["cos"].double()), dict(sin=None), dict(sin=x["sin"][:5]),
+                dict(pos=x["pos"].long()), dict(pos=x["pos"][:, :5]), dict(pos=x["pos"].cpu()),
+                dict(q=x["q"].transpose(1, 2).contiguous().transpose(1, 2)),  # heads apart
+                dict(q=x["q"][:, :1].expand_as(x["q"])),                      # one row for all tokens
+                dict(cos=x["cos"][:, :3], sin=x["sin"][:, :3].contiguous())):
+        with pytest.raises((ValueError, binding.FabError)):
+            binding.qk_norm_rope(**{**a, **bad})
+
+
+@pytest.mark.gpu
+def test_many_heads(gpu):
+    # more blocks of heads than a grid's second dimension holds at first
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn((1, 1, 300000, 8), generator=g, device="cuda").to(torch.bfloat16)
+    k = torch.randn((1, 1, 2, 8), generator=g, device="cuda").to(torch.bfloat16)
+    qo, ko, _ = binding.qk_norm_rope(q, k, None)
+    assert torch.equal(qo[:, :, 0], q[:, 0]) and torch.equal(ko[:, :, 0], k[:, 0])
 
 
 @pytest.mark.gpu

@@ -86,6 +86,21 @@ def test_no_tokens_is_nothing_to_do():
     assert call_attention(paged_dims(T=0), q=None, o=None, lse=None) == binding.FAB_OK
 
 
+def test_binding_refuses_what_does_not_fit():
+    q = torch.zeros(3, 4, 64)
+    k, v = torch.zeros(5, 2, 16, 64), torch.zeros(5, 2, 16, 64)
+    starts, lens = torch.tensor([0, 3], dtype=torch.int32), torch.tensor([3], dtype=torch.int32)
+    table = torch.zeros(1, 2, dtype=torch.int32)
+    for args in ((q, k, v, starts, lens, table),        # not CUDA tensors
+                 (q[0], k, v, starts, lens, table),     # not 3-D
+                 (q, k[0], v, starts, lens, table),     # not 4-D
+                 (q, k, v, starts, lens, table[0])):    # not 2-D
+        with pytest.raises(ValueError):
+            binding.paged_attention(*args)
+        with pytest.raises(ValueError):
+            binding.paged_append(args[0], q[:, :2], q[:, :2], None, None, None, None, *args[3:], args[1], args[2])
+
+
 # ------------------------------------------------------------------ a paged batch
 
 
@@ -304,6 +319,62 @@ def test_padding_tokens_are_left_alone(gpu):
         assert (qo[6:] == 3).all() and torch.equal(qo[:6].flatten(1), a[:6])
         changed = (k.isnan() != before[0].isnan()) | ((k != before[0]) & ~k.isnan())
         assert changed.any(-1).sum() <= 6 * 2
+
+
+@pytest.mark.gpu
+def test_no_tokens(gpu):
+    # T = 0 through the binding, and sequences none of which has a new token
+    x = Batch([2], [20], 4, 2, 64, 64, 16, "bf16", seed=10)
+    q, k, v, starts, lens, table = x.cuda()
+    before = k.clone()
+    for n in (0, 2):
+        qn = q[:n]
+        starts.zero_()
+        o, lse = binding.paged_attention(qn, k, v, starts, lens, table, True, 0.125)
+        assert o.shape == (n, 4, 64) and lse.shape == (4, n)
+        binding.paged_append(qn, qn[:, :2], qn[:, :2], None, None, None, None, starts, lens, table, k, v)
+    assert torch.equal(k.nan_to_num(9), before.nan_to_num(9))
+
+
+@pytest.mark.gpu
+def test_operands_that_do_not_match_are_refused(gpu):
+    x = Batch([2], [20], 4, 2, 64, 64, 16, "bf16", seed=10)
+    q, k, v, starts, lens, table = x.cuda()
+    for bad in ((q.half(), k, v, starts, lens, table), (q.transpose(0, 1), k, v, starts, lens, table),
+                (q, k, v.half(), starts, lens, table), (q, k, v[:-1], starts, lens, table),
+                (q, k.transpose(1, 2), v, starts, lens, table), (q, k, v, starts.long(), lens, table),
+                (q, k, v, starts[:1], lens, table), (q, k, v, starts, lens, table[:, ::2]),
+                (q[:, :3], k, v, starts, lens, table), (q, k, v, starts, lens.cpu(), table),
+                (q[..., :32].contiguous(), k, v, starts, lens, table)):
+        with pytest.raises((ValueError, binding.FabError)):
+            binding.paged_attention(*bad)
+
+
+@pytest.mark.gpu
+def test_graphs_side_by_side(gpu):
+    # two captured steps, each with the workspace that its capture allocated, replayed on two streams at once
+    x = [Batch([1, 9], [900, 350], 8, 2, 128, 128, 16, "bf16", seed=s) for s in (20, 21)]
+    dev = [b.cuda() for b in x]
+    want = [binding.paged_attention(*d, True, 0.1) for d in dev]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for d in dev:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(binding.paged_attention(*d, True, 0.1))
+        graphs.append(g)
+    side = [torch.cuda.Stream() for _ in x]
+    for _ in range(20):
+        for o, lse in outs:
+            o.fill_(float("nan"))
+            lse.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, side):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (o, lse), (wo, wl) in zip(outs, want):
+            assert torch.equal(o, wo) and torch.equal(lse, wl)
 
 
 @pytest.mark.gpu
