@@ -80,13 +80,18 @@ struct PCfg {
   static constexpr uint32_t OFF_K = 2 * TILE;
   static constexpr uint32_t OFF_V = OFF_K + NK * TILE;
   static constexpr uint32_t OFF_BAR = OFF_V + NV * TILE;
-  static constexpr uint32_t OFF_MISC = OFF_BAR + 40 * 8;
+  static constexpr uint32_t OFF_MISC = OFF_BAR + 48 * 8;
   static constexpr uint32_t OFF_UNIT = OFF_MISC + 16;       // kUnits descriptions of units
   static constexpr uint32_t OFF_ML = OFF_UNIT + kUnits * 64;  // 128 (maximum, sum) pairs; the plan's scratch before
   static constexpr uint32_t USED = OFF_ML + 128 * 8;
   static constexpr uint32_t SMEM = USED > 118784 ? USED : 118784;  // one CTA owns the SM's tensor memory
-  static constexpr uint32_t TM_S = 0;    // + 128 * stream
-  static constexpr uint32_t TM_O = 256;  // + DP * stream
+  // Score tiles in tensor memory: one a stream, and at width 64, where the
+  // outputs leave room, a third: the streams then take turns with all three, and
+  // a stream's next S is there when its softmax comes for it.
+  static constexpr int NB = DP == 128 ? 2 : 3;
+  static constexpr uint32_t TM_S = 0;         // + 128 * buffer
+  static constexpr uint32_t TM_O = NB * 128;  // + DP * stream
+  static_assert(TM_O + 2 * DP <= 512, "tensor memory budget");
   static_assert(SMEM <= 232448, "shared memory budget");
   static_assert(sizeof(PagedShared) <= 1024, "plan scratch");
 };
@@ -98,15 +103,16 @@ enum : int {
   B_VE = 12,  // + slot: V free
   B_QF = 16,  // + slot: Q landed
   B_QE = 18,  // + slot: Q free
-  B_S = 20,   // + stream: S landed (and every product issued before it)
-  B_P = 22,   // + 2 stream + half: P's keys of that half written (and O rescaled where it had to be)
-  B_O = 26,   // + stream: the unit's last product of the stream finished
-  B_ML = 28,  // one-tile units: stream 1's maxima and sums are in shared memory
-  B_MD = 29,  // one-tile units: stream 0 has read stream 1's output
-  B_FIN = 30,
-  B_DF = 31,  // + slot: a unit is described
-  B_DE = 35,  // + slot: every warp is done with it
-  B_COUNT = 39
+  B_S = 20,   // + buffer: S landed
+  B_P = 23,   // + 2 buffer + half: P's keys of that half written (and O rescaled where it had to be)
+  B_PV = 29,  // + buffer: O += P V finished (three buffers only)
+  B_O = 32,   // + stream: the unit's last product of the stream finished
+  B_ML = 34,  // one-tile units: stream 1's maxima and sums are in shared memory
+  B_MD = 35,  // one-tile units: stream 0 has read stream 1's output
+  B_FIN = 36,
+  B_DF = 37,  // + slot: a unit is described
+  B_DE = 41,  // + slot: every warp is done with it
+  B_COUNT = 45
 };
 
 struct TcParams {
@@ -159,10 +165,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(B_QF + s), 1);
       mbar_init(bar(B_QE + s), 1);
+      mbar_init(bar(B_O + s), 1);
+    }
+    for (int s = 0; s < 3; ++s) {
       mbar_init(bar(B_S + s), 1);
       mbar_init(bar(B_P + 2 * s), 4);
       mbar_init(bar(B_P + 2 * s + 1), 4);
-      mbar_init(bar(B_O + s), 1);
+      mbar_init(bar(B_PV + s), 1);
     }
     mbar_init(bar(B_ML), 128);
     mbar_init(bar(B_MD), 128);
@@ -319,39 +328,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t q_lo = sdesc_lo(sbase + C::OFF_Q, 16), k_lo = sdesc_lo(sbase + C::OFF_K, 16);
         const uint32_t v_lo = sdesc_lo(sbase + C::OFF_V, C::ATOM);
         auto wait = [&](int i, uint32_t parity) { return mbar_wait_asleep(bar(i), parity, abort_flag, err); };
-        auto s_product = [&](uint32_t s, uint32_t a_lo, uint32_t b_lo) {
+        constexpr int NB = C::NB;
+        auto s_product = [&](uint32_t buf, uint32_t a_lo, uint32_t b_lo) {
 #pragma unroll
           for (int kk = 0; kk < DP / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * C::ATOM + (kk & 3) * 32) >> 4;
-            mma_ss_one(tm + C::TM_S + s * 128, a_lo + off, b_lo + off, HI, ID_S, kk > 0);
+            mma_ss_one(tm + C::TM_S + buf * 128, a_lo + off, b_lo + off, HI, ID_S, kk > 0);
           }
-          mma_commit_one(bar(B_S + s));
+          mma_commit_one(bar(B_S + buf));
         };
-        // O_s += P_s V (more = 0: O_s = P_s V); with `early` the first 64 keys as
-        // soon as their weights are there.
-        uint32_t pphase = 0;  // bit 2 stream + half
-        auto pv_product = [&](uint32_t s, uint32_t b_lo, uint32_t keys, uint32_t more, bool early) -> bool {
-          const uint32_t d = tm + C::TM_O + s * DP, a = tm + C::TM_S + s * 128;
-          if (!wait(B_P + 2 * s + (early ? 0 : 1), (pphase >> (2 * s + (early ? 0 : 1))) & 1u)) return false;
-          tc_fence_after();
+        // O_s += P V (more = 0: O_s = P V), P in a buffer; with `early` the first 64
+        // keys as soon as their weights are there.
+        uint32_t pphase = 0;  // bit 2 buffer + half
+        auto pv_product = [&](uint32_t s, uint32_t buf, uint32_t b_lo, uint32_t keys, uint32_t more, bool early) -> bool {
+          const uint32_t d = tm + C::TM_O + s * DP, a = tm + C::TM_S + buf * 128;
+          auto half = [&](uint32_t h) {
+            if (!wait(B_P + 2 * buf + h, (pphase >> (2 * buf + h)) & 1u)) return false;
+            tc_fence_after();
+            return true;
+          };
+          if (!half(early ? 0 : 1)) return false;
           if (keys == 128) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) mma_ts_one(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, kk > 0 ? 1u : more);
-            if (early) {
-              if (!wait(B_P + 2 * s + 1, (pphase >> (2 * s + 1)) & 1u)) return false;
-              tc_fence_after();
-            }
+            if (early && !half(1)) return false;
 #pragma unroll
             for (int kk = 4; kk < 8; ++kk) mma_ts_one(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, 1u);
           } else {
-            if (early) {
-              if (!wait(B_P + 2 * s + 1, (pphase >> (2 * s + 1)) & 1u)) return false;
-              tc_fence_after();
-            }
+            if (early && !half(1)) return false;
             for (uint32_t kk = 0; kk * 16 < keys; ++kk)
               mma_ts_one(d, a + kk * 8, b_lo + kk * 128, HI, ID_PV, kk > 0 ? 1u : more);
           }
-          pphase ^= 3u << (2 * s);
+          pphase ^= 3u << (2 * buf);
+          if (NB == 3) mma_commit_one(bar(B_PV + buf));
           return true;
         };
         // The last keys' tile: products run over whole steps of 16 keys (one at
@@ -380,6 +389,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto next_v = [&]() {
           if (++vslot == C::NV) vslot = 0, vphase ^= 1;
         };
+        uint32_t sbuf = 0, pbuf = 0;  // three buffers: the next S's and the next P's
+        auto next_buf = [&](uint32_t& b) {
+          if (++b == 3) b = 0;
+        };
         // A unit of two row tiles: per key tile O_0, S_0, O_1, S_1, so that each
         // stream's softmax runs beside the other's products.
         auto two_tiles = [&](const UnitPart& x) -> bool {
@@ -387,6 +400,45 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t a0 = q_lo + q0 * SLOT, a1 = q_lo + q1 * SLOT;
           if (!wait(B_QF + q0, (qn >> 1) & 1u) || !wait(B_QF + q1, ((qn + 1) >> 1) & 1u)) return false;
           qn += 2;
+          if constexpr (NB == 3) {
+            const uint32_t steps = 2 * tiles;
+            uint32_t si = 0;
+            auto next_s = [&]() -> bool {
+              if (!(si & 1u)) {
+                if (!wait(B_KF + kslot, kphase)) return false;
+                tc_fence_after();
+              }
+              s_product(sbuf, si & 1u ? a1 : a0, k_lo + kslot * SLOT);
+              next_buf(sbuf);
+              if (si & 1u) {
+                mma_commit_one(bar(B_KE + kslot));
+                next_k();
+              }
+              if (++si == steps) {
+                mma_commit_one(bar(B_QE + q0));
+                mma_commit_one(bar(B_QE + q1));
+              }
+              return true;
+            };
+            while (si < steps && si < 3)
+              if (!next_s()) return false;
+            uint32_t keys = 128;
+            for (uint32_t i = 0; i < steps; ++i) {
+              if (!(i & 1u)) {
+                if (!wait(B_VF + vslot, vphase)) return false;
+                if (i + 2 == steps) keys = end_keys(vslot, last);
+              }
+              if (!pv_product(i & 1u, pbuf, v_lo + vslot * SLOT, keys, i >= 2 ? 1u : 0u, true)) return false;
+              next_buf(pbuf);
+              if (i + 2 >= steps) mma_commit_one(bar(B_O + (i & 1u)));
+              if (i & 1u) {
+                mma_commit_one(bar(B_VE + vslot));
+                next_v();
+              }
+              if (si < steps && !next_s()) return false;
+            }
+            return true;
+          }
           if (!wait(B_KF + kslot, kphase)) return false;
           tc_fence_after();
           s_product(0, a0, k_lo + kslot * SLOT);
@@ -397,9 +449,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (uint32_t t = 1; t < tiles; ++t) {
             if (!wait(B_KF + kslot, kphase) || !wait(B_VF + vslot, vphase)) return false;
             const uint32_t kb = k_lo + kslot * SLOT, vb = v_lo + vslot * SLOT;
-            if (!pv_product(0, vb, 128, more, true)) return false;
+            if (!pv_product(0, 0, vb, 128, more, true)) return false;
             s_product(0, a0, kb);
-            if (!pv_product(1, vb, 128, more, true)) return false;
+            if (!pv_product(1, 1, vb, 128, more, true)) return false;
             mma_commit_one(bar(B_VE + vslot));
             s_product(1, a1, kb);
             mma_commit_one(bar(B_KE + kslot));
@@ -411,9 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit_one(bar(B_QE + q1));
           if (!wait(B_VF + vslot, vphase)) return false;
           const uint32_t vb = v_lo + vslot * SLOT, keys = end_keys(vslot, last);
-          if (!pv_product(0, vb, keys, more, true)) return false;
+          if (!pv_product(0, 0, vb, keys, more, true)) return false;
           mma_commit_one(bar(B_O));
-          if (!pv_product(1, vb, keys, more, true)) return false;
+          if (!pv_product(1, 1, vb, keys, more, true)) return false;
           mma_commit_one(bar(B_O + 1));
           mma_commit_one(bar(B_VE + vslot));
           next_v();
@@ -424,9 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // where its operands have landed, so that a unit's end leaves work to do.
         uint32_t us = 0, up = 0;                      // the unit at work
         uint32_t sd = 0, sdp = 0, si = 0, ahead = 0;  // the S products' unit; units between the two
-        uint32_t busy = 0;                            // streams with an S or a P
+        uint32_t busy = 0;                            // streams (three buffers: buffers) with an S or a P
         auto s_ahead = [&]() -> bool {
-          while (!((busy >> (si & 1u)) & 1u)) {
+          while (!((busy >> (NB == 3 ? sbuf : si & 1u)) & 1u)) {
             // another unit's description and operands are waited for only when
             // nothing else is left to do
             const bool patient = busy != 0 && ahead != 0;
@@ -440,10 +492,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (si == 0 && !wait(B_QF + qs, qp)) return false;
             if (!wait(B_KF + kslot, kphase)) return false;
             tc_fence_after();
-            s_product(si & 1u, q_lo + qs * SLOT, k_lo + kslot * SLOT);
+            const uint32_t buf = NB == 3 ? sbuf : si & 1u;
+            s_product(buf, q_lo + qs * SLOT, k_lo + kslot * SLOT);
+            next_buf(sbuf);
             mma_commit_one(bar(B_KE + kslot));
             next_k();
-            busy |= 1u << (si & 1u);
+            busy |= 1u << buf;
             if ((int)++si == u.j1 - u.j0) {
               mma_commit_one(bar(B_QE + qs));
               ++qn;
@@ -460,11 +514,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t s = i & 1u;
             if (!s_ahead() || !wait(B_VF + vslot, vphase)) return false;
             const uint32_t keys = i + 1 == tiles ? end_keys(vslot, last) : 128u;
-            if (!pv_product(s, v_lo + vslot * SLOT, keys, i < 2 ? 0u : 1u, false)) return false;
+            const uint32_t buf = NB == 3 ? pbuf : s;
+            if (!pv_product(s, buf, v_lo + vslot * SLOT, keys, i < 2 ? 0u : 1u, false)) return false;
+            next_buf(pbuf);
             mma_commit_one(bar(B_VE + vslot));
             if (i + 2 >= tiles) mma_commit_one(bar(B_O + s));
             next_v();
-            busy &= ~(1u << s);
+            busy &= ~(1u << buf);
           }
           --ahead;
           return true;
@@ -493,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s = (warp - 4) >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tm + lane_off + C::TM_S + s * 128, tO = tm + lane_off + C::TM_O + s * DP;
+    const uint32_t tO = tm + lane_off + C::TM_O + s * DP;
     // weights 2^(s c1 - m) (the S products carry the scale's sign); a scale of
     // zero is taken as one too small to tell the scores apart (0 times a masked
     // score would be NaN)
@@ -501,6 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr float kBias = F16 ? 7.f : 0.f;
     const int i_row = r / plan.gw, g_row = r - i_row * plan.gw;
     uint32_t sphase = 0, ophase = 0, mphase = 0;
+    uint32_t steps = 0;  // three buffers: steps of the units before
     uint32_t us = 0, up = 0;
     bool ok = true;
     auto next_unit = [&]() {
@@ -524,7 +581,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         last -= u.j0 * 128;  // counted from the part's first key
         float m_run = -INFINITY, l = 0.f;
         for (int t = wide ? 0 : s; t < n; t += wide ? 1 : 2) {
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait_asleep(bar(B_S + s), sphase, abort_flag, err)))) break;
+          const uint32_t step = steps + (wide ? 2 * t + s : t);
+          const uint32_t buf = C::NB == 3 ? step % 3u : (uint32_t)s;
+          const uint32_t tS = tm + lane_off + C::TM_S + buf * 128;
+          if (C::NB == 3) sphase = (step / 3u) & 1u;
+          if (!ok || !(ok = __all_sync(0xffffffffu, mbar_wait_asleep(bar(B_S + buf), sphase, abort_flag, err)))) break;
           sphase ^= 1;
           if (active) {
             tc_fence_after();
@@ -556,7 +617,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               m_run = tmax;
             }
             if (__any_sync(0xffffffffu, need)) {
-              // (every product into O_s was issued before this S, so it is done)
+              // two buffers: every product into O_s was issued before this S, so it
+              // is done; three: the last one is waited for
+              if (C::NB == 3)
+                ok = __all_sync(0xffffffffu, mbar_wait_asleep(bar(B_PV + (step - 2) % 3u), ((step - 2) / 3u) & 1u,
+                                                              abort_flag, err));
+              tc_fence_after();
 #pragma unroll 1
               for (int c0 = 0; c0 < DP; c0 += 32) {
                 uint32_t o[32];
@@ -587,15 +653,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st_wait();
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(bar(B_P + 2 * s + h));
+              if (lane == 0) mbar_arrive(bar(B_P + 2 * buf + h));
             }
             const float2 total = split_f32(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])));
             l += total.x + total.y;
           } else if (lane < 2) {
-            mbar_arrive(bar(B_P + 2 * s + lane));
+            mbar_arrive(bar(B_P + 2 * buf + lane));
           }
         }
         if (!ok) break;
+        steps += wide ? 2 * n : n;
         // ---- the unit's end: O / l and the log-sum-exp, or partial results
         const float ref = m_run == -INFINITY ? 0.f : m_run - kBias;
         const bool ran = wide || s < n;  // the stream had a key tile
