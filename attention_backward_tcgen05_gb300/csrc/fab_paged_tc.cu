@@ -104,7 +104,8 @@ enum : int {
   B_QF = 16,  // + slot: Q landed
   B_QE = 18,  // + slot: Q free
   B_S = 20,   // + buffer: S landed
-  B_P = 23,   // + 2 buffer + half: P's keys of that half written (and O rescaled where it had to be)
+  B_P = 23,   // + 2 buffer + half: P's keys of that half written (and O rescaled where it had to be);
+              // with three buffers only + 1, for both
   B_PV = 29,  // + buffer: O += P V finished (three buffers only)
   B_O = 32,   // + stream: the unit's last product of the stream finished
   B_ML = 34,  // one-tile units: stream 1's maxima and sums are in shared memory
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(B_VF + vslot, vphase)) return false;
                 if (i + 2 == steps) keys = end_keys(vslot, last);
               }
-              if (!pv_product(i & 1u, pbuf, v_lo + vslot * SLOT, keys, i >= 2 ? 1u : 0u, true)) return false;
+              if (!pv_product(i & 1u, pbuf, v_lo + vslot * SLOT, keys, i >= 2 ? 1u : 0u, false)) return false;
               next_buf(pbuf);
               if (i + 2 >= steps) mma_commit_one(bar(B_O + (i & 1u)));
               if (i & 1u) {
@@ -650,14 +651,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pk[c] = pack2<F16>(a, b);
               }
               tmem_st32(tS + h * 32, pk);
-              tmem_st_wait();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(B_P + 2 * buf + h));
+              if (C::NB == 2 || h == 1) {  // (three buffers: nothing waits for the first half alone)
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_P + 2 * buf + h));
+              }
             }
             const float2 total = split_f32(add_f32x2(add_f32x2(sum[0], sum[1]), add_f32x2(sum[2], sum[3])));
             l += total.x + total.y;
-          } else if (lane < 2) {
+          } else if (lane < 2 && (C::NB == 2 || lane == 1)) {
             mbar_arrive(bar(B_P + 2 * buf + lane));
           }
         }
