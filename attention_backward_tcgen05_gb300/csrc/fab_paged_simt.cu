@@ -16,8 +16,10 @@
 // takes R / 4 rows of one key; the output: a lane takes CPL columns of all R
 // rows, so a value is read from shared memory once for R rows.
 //
-// Bound by memory for a few rows a sequence, by shared-memory reads (5 for 16
-// multiply-adds of the scores, 5 for 64 of the output) for more.
+// Bound by shared-memory reads (5 for 16 multiply-adds of the scores, 5 for 64 of
+// the output) and by the latency of a tile's steps, which eight warps hide only
+// in part: f32, one sequence of 100,000 keys, 32 heads on 8, width 128 takes 282
+// us, 2.9 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -150,69 +152,84 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
 #pragma unroll
       for (int c = 0; c < CPL; ++c) acc[r][c] = 0.f;
 
-    // fetches this warp's 8 rows of key tile j into the ring's slot
-    auto fetch = [&](int j, int slot) {
-      const int mk = j * 64 + warp * kKeys + key;  // (every group of 8 lanes looks up the same 8 pages)
-      int64_t row = -1;
-      if (j < w.j1 && mk < w.q.len) {
-        const int at = (int)((uint32_t)mk / (uint32_t)p.page);
-        const int page = p.table[(int64_t)w.at.b * p.max_pages + at];
-        if (page >= 0 && page < p.pages)
-          row = ((int64_t)page * p.Hkv + hk) * p.page + (mk - at * p.page);
-        else
-          atomicOr(&g_err_paged, kErrIndex);  // (its key and value are zeros)
-      }
+    // row of the caches that holds this lane's key of tile j (every group of 8
+    // lanes looks up the same 8), or -1
+    auto lookup = [&](int j) -> int64_t {
+      if (j >= w.j1) return -1;
+      const int mk = j * 64 + warp * kKeys + key;
+      if (mk >= w.q.len) return -1;
+      const int at = (int)((uint32_t)mk / (uint32_t)p.page);
+      const int page = p.table[(int64_t)w.at.b * p.max_pages + at];
+      if (page >= 0 && page < p.pages) return ((int64_t)page * p.Hkv + hk) * p.page + (mk - at * p.page);
+      atomicOr(&g_err_paged, kErrIndex);  // (its key and value are zeros)
+      return -1;
+    };
+    // copies the 8 rows `row` names into the ring's slot, zeros for -1
+    auto fetch = [&](int64_t row, int slot) {
       uint8_t* kd = ring + slot * stage_bytes;
       uint8_t* vd = kd + kKeys * p.ks;
       if (p.vec) {
         // 16-byte pieces of keys, then of values; a row's pieces side by side
-        const int kp = p.DK * (int)sizeof(T) / 16, vp = p.DV * (int)sizeof(T) / 16, per = kp + vp;
-        for (int x = lane; x - lane < kKeys * per; x += 32) {
-          const int kk = x / per, c = x - kk * per;
+        const int kp = p.DK * (int)sizeof(T) / 16, per = kp + p.DV * (int)sizeof(T) / 16;
+        int kk = 0, c = lane;
+        for (int left = kKeys * per; left > 0; left -= 32) {
+          while (c >= per) c -= per, ++kk;
           const int64_t src = __shfl_sync(0xffffffffu, row, kk & 7);
-          if (x >= kKeys * per) continue;
-          const bool isk = c < kp;
-          const uint8_t* from = isk ? reinterpret_cast<const uint8_t*>(kc + (src < 0 ? 0 : src) * p.DK) + c * 16
-                                    : reinterpret_cast<const uint8_t*>(vc + (src < 0 ? 0 : src) * p.DV) + (c - kp) * 16;
-          cp_async16(smem_u32(isk ? kd + kk * p.ks + c * 16 : vd + kk * p.vs + (c - kp) * 16), from, src < 0 ? 0u : 16u);
+          if (kk < kKeys) {
+            const bool isk = c < kp;
+            const uint8_t* from = isk ? reinterpret_cast<const uint8_t*>(kc + (src < 0 ? 0 : src) * p.DK) + c * 16
+                                      : reinterpret_cast<const uint8_t*>(vc + (src < 0 ? 0 : src) * p.DV) + (c - kp) * 16;
+            cp_async16(smem_u32(isk ? kd + kk * p.ks + c * 16 : vd + kk * p.vs + (c - kp) * 16), from,
+                       src < 0 ? 0u : 16u);
+          }
+          c += 32;
         }
       } else {
         for (int kk = 0; kk < kKeys; ++kk) {
           const int64_t src = __shfl_sync(0xffffffffu, row, kk);
+          const T* kf = kc + (src < 0 ? 0 : src) * p.DK;
+          const T* vf = vc + (src < 0 ? 0 : src) * p.DV;
           T* kr = reinterpret_cast<T*>(kd + kk * p.ks);
           T* vr = reinterpret_cast<T*>(vd + kk * p.vs);
-          for (int d = lane; d < p.qs; d += 32) kr[d] = src >= 0 && d < p.DK ? kc[src * p.DK + d] : T(0.f);
-          for (int d = lane; d < p.DV; d += 32) vr[d] = src >= 0 ? vc[src * p.DV + d] : T(0.f);
+          for (int d = lane; d < p.qs; d += 32) kr[d] = src >= 0 && d < p.DK ? kf[d] : T(0.f);
+          for (int d = lane; d < p.DV; d += 32) vr[d] = src >= 0 ? vf[d] : T(0.f);
         }
       }
       cp_async_commit();
     };
 
     __syncwarp();
-    for (int s = 0; s + 1 < p.stages; ++s) fetch(w.j0 + s, s);
+    for (int s = 0; s + 1 < p.stages; ++s) fetch(lookup(w.j0 + s), s);
+    int64_t next = lookup(w.j0 + p.stages - 1);  // of the next fetch: looked up a tile ahead
     int slot = 0;
     for (int j = w.j0; j < w.j1; ++j) {
       {
         int ahead = slot + p.stages - 1;
         if (ahead >= p.stages) ahead -= p.stages;
-        fetch(j + p.stages - 1, ahead);
+        fetch(next, ahead);
+        next = lookup(j + p.stages);
       }
       cp_async_wait(p.stages - 1);
       __syncwarp();
       const T* kr = reinterpret_cast<const T*>(ring + slot * stage_bytes + key * p.ks);
       const T* vb = reinterpret_cast<const T*>(ring + slot * stage_bytes + kKeys * p.ks);
-      float s[RPL];
+      float s[RPL], s4[RPL][4];  // (four sums a score: a chain of multiply-adds is a quarter as long)
 #pragma unroll
-      for (int e = 0; e < RPL; ++e) s[e] = 0.f;
+      for (int e = 0; e < RPL; ++e) s4[e][0] = s4[e][1] = s4[e][2] = s4[e][3] = 0.f;
 #pragma unroll 4
       for (int d = 0; d < p.qs; d += 4) {
         const float4 kv = lds4(kr + d);
 #pragma unroll
         for (int e = 0; e < RPL; ++e) {
           const float4 qv = *reinterpret_cast<const float4*>(q_s + (rg * RPL + e) * p.qs + d);
-          s[e] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, s[e]))));
+          s4[e][0] = fmaf(qv.x, kv.x, s4[e][0]);
+          s4[e][1] = fmaf(qv.y, kv.y, s4[e][1]);
+          s4[e][2] = fmaf(qv.z, kv.z, s4[e][2]);
+          s4[e][3] = fmaf(qv.w, kv.w, s4[e][3]);
         }
       }
+#pragma unroll
+      for (int e = 0; e < RPL; ++e) s[e] = (s4[e][0] + s4[e][1]) + (s4[e][2] + s4[e][3]);
       const int mk = j * 64 + warp * kKeys + key;
       bool grew = false;
       float f[RPL];
@@ -329,12 +346,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
 
 constexpr int kSmemLimit = 232448 - 1024;  // (the plan's static part aside)
 
+// Rows of a tile: four or eight where a sequence has no more to give (a
+// decoding step of up to as many heads a key head), else 16, or 8 of wide values
+// (128 registers of outputs a lane).  Tiles of 4, 8, 16 rows, f32: one
+// sequence of 100,000 keys, 4 heads a key head 282, 345, 485 us; 16 sequences of
+// 1,000 to 4,000 keys, 8 heads 106, 77, 99 us; chunks of 60 tokens on 2,000
+// keys 359, 230, 175 us.
 int rows_of(const PagedProblem& pr) {
-  // four rows a tile where a sequence has no more to give (a decoding step of
-  // up to four heads a key head), else 16, or 8 of wide rows (128 registers of
-  // outputs a lane)
-  if (pr.T * (pr.H / pr.Hkv) <= 4 * pr.B) return 4;
-  return pr.DV > 128 ? 8 : 16;
+  const int64_t rows = pr.T * (pr.H / pr.Hkv);  // of a key head, all sequences
+  return rows <= 4 * pr.B ? 4 : rows <= 8 * pr.B || pr.DV > 128 ? 8 : 16;
 }
 int dp_of(const PagedProblem& pr) { return (int)(pr.DV + 3) / 4 * 4; }
 
@@ -394,7 +414,8 @@ template <typename T>
 cudaError_t launch_t(const PagedProblem& pr, int sms, cudaStream_t s) {
   const int R = rows_of(pr);
   if (pr.DV > 128) return R == 4 ? launch_r<T, 4, 8>(pr, sms, s) : launch_r<T, 8, 8>(pr, sms, s);
-  return R == 4 ? launch_r<T, 4, 4>(pr, sms, s) : launch_r<T, 16, 4>(pr, sms, s);
+  if (R == 16) return launch_r<T, 16, 4>(pr, sms, s);
+  return R == 4 ? launch_r<T, 4, 4>(pr, sms, s) : launch_r<T, 8, 4>(pr, sms, s);
 }
 
 }  // namespace
