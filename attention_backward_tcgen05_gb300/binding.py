@@ -450,9 +450,9 @@ def fab_paged_append(q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, 
     dims.ldk = _ld(k, "k", dt, (T, dims.Hkv, DK))
     dims.ldv = _ld(v, "v", dt, (T, dims.Hkv, dims.DV))
     _check(lib().fab_paged_append(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), *tables, eps, 1 if interleaved else 0, starts.data_ptr(), lens.data_ptr(), table.data_ptr(), dtype_code(q),
-        ctypes.byref(dims), _ptr(q_out, "q_out", dt, (T, H, DK)), k_cache.data_ptr(), v_cache.data_ptr(),
-        _raw_stream(stream, dev)), "fab_paged_append")
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), *tables, eps, 1 if interleaved else 0, starts.data_ptr(),
+        lens.data_ptr(), table.data_ptr(), dtype_code(q), ctypes.byref(dims), _ptr(q_out, "q_out", dt, (T, H, DK)),
+        k_cache.data_ptr(), v_cache.data_ptr(), _raw_stream(stream, dev)), "fab_paged_append")
 
 
 def fab_paged_attention_workspace_bytes(dims: fab_paged_dims, dtype: int) -> int:

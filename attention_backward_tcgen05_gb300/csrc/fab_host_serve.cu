@@ -24,7 +24,7 @@ bool fits(int64_t a, int64_t b, int64_t c, int64_t d) {
 }
 
 bool heads_ok(int64_t H, int64_t Hkv, int64_t DK, int64_t DV) {
-  return H > 0 && Hkv > 0 && DK > 0 && DV > 0 && H % Hkv == 0;
+  return H > 0 && H <= kMaxInt32 && Hkv > 0 && DK > 0 && DV > 0 && H % Hkv == 0;
 }
 
 bool rot_ok(int64_t rot, int64_t DK, int64_t P) {

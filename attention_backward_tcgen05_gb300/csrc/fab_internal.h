@@ -90,7 +90,7 @@ struct RopeProblem {
   const float *dq, *dk, *dv;
   void *gq, *gk, *gv;
   float *gwq, *gwk;
-  float* partial;  // workspace: rope_partial_rows rows of DK floats
+  float* partial;  // workspace: kRopePartialRows rows of DK floats
 };
 // Rows of partial sums of a backward call (q's and k's together at most).
 constexpr int64_t kRopePartialRows = 1280;

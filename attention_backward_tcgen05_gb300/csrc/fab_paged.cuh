@@ -318,7 +318,7 @@ FAB_DEV void paged_note_part(const PagedPlan& p, const PagedWalk& w, const Paged
   if (w.j0 > 0) cut->head_part = 1;
   if (w.j0 == 0 && w.j1 < w.ntiles) {
     int last = c + 1;
-    while (w.tiles_before(border(last + 1)) < w.ntiles) ++last;
+    while (last + 1 < (int)gridDim.x && w.tiles_before(border(last + 1)) < w.ntiles) ++last;
     cut->last = last;
     cut->s0 = w.q.s0;
     cut->n = w.q.n;

@@ -182,11 +182,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tmK);
     prefetch_tensormap(&tmV);
   }
-  if (warp == 3) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (launched early: lengths and operands from here on)
+  if (warp == 3) {  // (after the wait: a kernel before that is not done yet may still want tensor memory)
     tmem_alloc(smem_u32(tmem_holder), 512);
     tmem_relinquish();
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // (launched early: lengths and operands from here on)
   if (blockIdx.x == 0) check_starts(plan.starts, plan.B, plan.T, (int)threadIdx.x, kThreads, err);
   int64_t mine;
   paged_total<kThreads>(plan, sh, &mine);

@@ -218,7 +218,7 @@ FAB_EXPORT int fab_backward_noalloc(const void* q, const void* k, const void* v,
  * is f32, rounded once to the output's type. */
 typedef struct {
   int64_t B, N;          /* sequences, tokens in each */
-  int64_t H, Hkv;        /* query heads, key/value heads (H % Hkv == 0) */
+  int64_t H, Hkv;        /* query heads (< 2^31), key/value heads (H % Hkv == 0) */
   int64_t DK, DV;        /* query/key width, value width (<= 256) */
   int64_t rot;           /* rotated columns of q and k: even, 0 .. DK */
   int64_t P;             /* positions held by cos and sin (read when rot > 0) */
@@ -277,7 +277,7 @@ FAB_EXPORT int fab_qk_norm_rope_backward(const float* dq, const float* dk, const
  * computed for those tokens is meaningless. */
 typedef struct {
   int64_t B, T;          /* sequences, rows of new tokens (T may be 0) */
-  int64_t H, Hkv;        /* query heads, key/value heads (H % Hkv == 0) */
+  int64_t H, Hkv;        /* query heads (< 2^31), key/value heads (H % Hkv == 0) */
   int64_t DK, DV;        /* query/key width, value width (<= 256) */
   int64_t page;          /* rows of a page */
   int64_t pages;         /* pages of the cache */
@@ -290,8 +290,8 @@ typedef struct {
  * q_out [DK,H,T], norms and rotation as in fab_qk_norm_rope, each token at
  * its place in its sequence (token i of the n new ones is at position
  * lens[b] - n + i, which must be in 0 .. P-1).  q, k, v: [DK,H] rows of ldq, ...
- * elements by token, aligned to their element only.  No other row of the caches
- * or of q_out is touched.  A row of the cache that two tokens of one call map
+ * elements by token, aligned to their element only; q_out and the caches must not
+ * overlap them.  No other row of the caches or of q_out is touched.  A row of the cache that two tokens of one call map
  * to gets either of them. */
 FAB_EXPORT int fab_paged_append(const void* q, const void* k, const void* v, const void* wq, const void* wk,
                                 const float* cos, const float* sin, float eps, int interleaved, const int32_t* starts,
@@ -307,8 +307,10 @@ FAB_EXPORT size_t fab_paged_attention_workspace_bytes(const fab_paged_dims* dims
  * fab_forward_lse's top-left rule).  q [DK,H,T], o [DV,H,T]: `dtype`; lse f32
  * [T,H] (natural log), or NULL.  A token that sees no key gets o = 0 and
  * lse = +inf.  Cache rows from lens[b] on are never read into a result, whatever
- * they hold.  workspace: device, fab_paged_attention_workspace_bytes() bytes,
- * contents overwritten; calls that may overlap on the GPU need one each. */
+ * they hold; rows before it have to be finite: a later token's value takes part in
+ * an earlier one's sum with weight 0, which a NaN or an infinity survives.
+ * workspace: device, fab_paged_attention_workspace_bytes() bytes, contents
+ * overwritten; calls that may overlap on the GPU need one each. */
 FAB_EXPORT int fab_paged_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* starts,
                                    const int32_t* lens, const int32_t* table, int causal, float scale, int dtype,
                                    const fab_paged_dims* dims, void* workspace, size_t workspace_bytes, void* o,

@@ -178,7 +178,7 @@ def call_backward(dims, dq=A, dk=A, dv=A, q=A, k=A, wq=A, wk=A, cos=A, sin=A, po
 
 BAD_DIMS = [dict(B=0), dict(N=0), dict(N=-1), dict(H=3), dict(Hkv=0), dict(DK=0), dict(DV=0), dict(rot=-2),
             dict(rot=63), dict(rot=66), dict(P=0), dict(ldq=255), dict(ldk=127), dict(ldv=127), dict(ldq=1 << 60),
-            dict(B=1 << 30, N=1 << 30), dict(P=1 << 31)]
+            dict(B=1 << 30, N=1 << 30), dict(P=1 << 31), dict(B=1, N=1, H=1 << 31, DK=8, DV=8, rot=8, ldq=1 << 35)]
 
 
 @pytest.mark.parametrize("bad", BAD_DIMS, ids=str)

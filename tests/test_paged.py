@@ -41,7 +41,7 @@ def call_attention(dims, q=A, kc=A, vc=A, starts=A, lens=A, table=A, scale=1.0, 
 
 BAD_DIMS = [dict(B=0), dict(T=-1), dict(H=3), dict(Hkv=0), dict(DK=0), dict(DV=-8), dict(page=0), dict(pages=0),
             dict(max_pages=0), dict(T=1 << 31), dict(pages=1 << 31), dict(pages=1 << 30, page=1 << 20),
-            dict(B=1 << 30, max_pages=1 << 30)]
+            dict(B=1 << 30, max_pages=1 << 30), dict(T=1, H=1 << 31, DK=8, DV=8, rot=8, ldq=1 << 35)]
 
 
 @pytest.mark.parametrize("bad", BAD_DIMS, ids=str)
