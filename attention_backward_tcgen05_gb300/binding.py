@@ -290,41 +290,65 @@ def fab_last_device_error(stream=None) -> int:
 # ------------------------------------------------------------------ norms + rotation, paged cache
 
 
-# A small call's time is its host's: these checks ask each tensor for each
-# property once.
+# A small call's time is its host's.  What a call checks and hands over depends
+# on its tensors' layouts alone, so it is worked out once for each set of them
+# (`_layouts`, the functions under `functools.lru_cache`): a training step's
+# or a decoding loop's calls find it by one look-up.
 
 
-def _here(*tensors):
-    """All the given tensors (None: skipped) are on the current device, which
-    is where libfab launches; returns that device's index."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors on {tensors[0].device} and {t.device}")
-    if dev < 0:
+def _layouts(*tensors):
+    """(shape, strides, dtype, device) of each tensor; None of None."""
+    return tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.get_device()) for t in tensors])
+
+
+def _one_device(layouts):
+    """The device index that all the given layouts (None: skipped) share."""
+    devs = {x[3] for x in layouts if x is not None}
+    if min(devs) < 0:
         raise ValueError("the tensors must be CUDA tensors")
-    if dev != torch.cuda.current_device():
+    if len(devs) > 1:
+        raise ValueError(f"tensors on {sorted(f'cuda:{d}' for d in devs)}")
+    return devs.pop()
+
+
+def _current(dev):
+    """libfab launches on the current device: it has to be the tensors'."""
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"tensors on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
-    return dev
 
 
-def _ptr(t, name, dtype, shape):
-    """Address of a contiguous tensor of that dtype and shape (None: null)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous, {dtype}, of shape {tuple(shape)}; "
-                         f"got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
-    return t.data_ptr()
+def _whole(x, name, dtype, shape):
+    """Checks that a layout (None: skipped) is contiguous, of that dtype and shape."""
+    if x is None:
+        return
+    shape = tuple(shape)
+    ok = x[2] is dtype and x[0] == shape
+    if ok and 0 not in shape:
+        step = 1
+        for n, st in zip(reversed(shape), reversed(x[1])):
+            ok = ok and (n == 1 or st == step)
+            step *= n
+    if not ok:
+        raise ValueError(f"{name} must be contiguous, {dtype}, of shape {shape}; "
+                         f"got {x[2]} {tuple(x[0])} strides {x[1]}")
 
 
-def _ld(t, name, dtype, shape):
-    """Elements between the rows of consecutive tokens of t, of shape
+def _outputs(dev, *checks):
+    """Each (tensor or None, name, dtype, shape) is whole and on device dev."""
+    for t, name, dtype, shape in checks:
+        if t is not None:
+            _whole((t.shape, t.stride(), t.dtype, dev), name, dtype, shape)
+            if t.get_device() != dev:
+                raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{dev}")
+
+
+def _ld(x, name, dtype, shape):
+    """Elements between the rows of consecutive tokens of a layout of shape
     (..., tokens, heads, width): heads contiguous inside a row, rows evenly
     spaced over all tokens."""
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    st = t.stride()
+    if x[2] is not dtype or x[0] != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {x[2]} {tuple(x[0])}")
+    st = x[1]
     heads, width = shape[-2], shape[-1]
     if (st[-1] != 1 and width > 1) or (st[-2] != width and heads > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous, got strides {st}")
@@ -338,17 +362,35 @@ def _ld(t, name, dtype, shape):
 
 
 def _tables(cos, sin, wq, wk, DK, dtype):
-    """(rot, P, addresses of wq, wk, cos, sin); without cos and sin no rotation."""
+    """(rot, P) of the tables' layouts, checked with the weights'; without cos and sin no rotation."""
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
-    w = _ptr(wq, "wq", dtype, (DK,)), _ptr(wk, "wk", dtype, (DK,))
+    _whole(wq, "wq", dtype, (DK,))
+    _whole(wk, "wk", dtype, (DK,))
     if cos is None:
-        return 0, 0, (*w, None, None)
-    shape = cos.shape
+        return 0, 0
+    shape = cos[0]
     if len(shape) != 2:
         raise ValueError("cos, sin must be 2-D: (P,rot/2)")
-    f32 = torch.float32
-    return 2 * shape[1], shape[0], (*w, _ptr(cos, "cos", f32, shape), _ptr(sin, "sin", f32, shape))
+    _whole(cos, "cos", torch.float32, shape)
+    _whole(sin, "sin", torch.float32, shape)
+    return 2 * shape[1], shape[0]
+
+
+def _code(dtype):
+    try:
+        return {torch.float32: FAB_F32, torch.bfloat16: FAB_BF16, torch.float16: FAB_F16}[dtype]
+    except KeyError:
+        raise ValueError(f"unsupported dtype {dtype}: float32, bfloat16 or float16") from None
+
+
+def _bytes(workspace, dev):
+    """Bytes of a workspace (None: 0), which has to be on device dev."""
+    if workspace is None:
+        return 0
+    if workspace.get_device() != dev:
+        raise ValueError(f"the workspace is on {workspace.device}, the other tensors on cuda:{dev}")
+    return workspace.numel() * workspace.element_size()
 
 
 def _addr(t):
@@ -361,122 +403,186 @@ def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def fab_qk_norm_rope(q, k, v, wq, wk, cos, sin, pos, eps, interleaved, q_out, k_out, v_out, stream=None):
-    if q.dim() != 4 or k.dim() != 4:
+@functools.lru_cache(maxsize=1024)
+def _rope_plan(layouts):
+    """(dims, their reference, dtype code, device) of a fab_qk_norm_rope call on
+    q, k, v, wq, wk, cos, sin, pos."""
+    q, k, v, wq, wk, cos, sin, pos = layouts
+    if len(q[0]) != 4 or len(k[0]) != 4:
         raise ValueError("q, k must be 4-D: (B,N,H,DK), (B,N,Hkv,DK)")
-    qs = q.shape
-    B, N, H, DK = qs
-    Hkv = k.shape[2]
-    dt = q.dtype
-    code = dtype_code(q)
-    dev = _here(q, k, v, wq, wk, cos, sin, pos, q_out, k_out, v_out)
-    rot, P, tables = _tables(cos, sin, wq, wk, DK, dt)
-    DV, ldv, vp, vo = DK, 0, None, None
+    B, N, H, DK = q[0]
+    Hkv = k[0][2]
+    dt = q[2]
+    code = _code(dt)
+    dev = _one_device(layouts)
+    rot, P = _tables(cos, sin, wq, wk, DK, dt)
+    DV, ldv = DK, 0
     if v is not None:
-        DV = v.shape[-1]
-        ldv, vp = _ld(v, "v", dt, (B, N, Hkv, DV)), v.data_ptr()
-    if v_out is not None:
-        vo = _ptr(v_out, "v_out", dt, (B, Hkv, N, DV))
-    dims = fab_rope_dims(B, N, H, Hkv, DK, DV, rot, P, _ld(q, "q", dt, qs), _ld(k, "k", dt, (B, N, Hkv, DK)), ldv)
+        DV = v[0][-1]
+        ldv = _ld(v, "v", dt, (B, N, Hkv, DV))
+    _whole(pos, "pos", torch.int32, (B, N))
+    dims = fab_rope_dims(B, N, H, Hkv, DK, DV, rot, P, _ld(q, "q", dt, q[0]), _ld(k, "k", dt, (B, N, Hkv, DK)), ldv)
+    return dims, ctypes.byref(dims), code, dev
+
+
+def _rope_call(plan, q, k, v, wq, wk, cos, sin, pos, eps, interleaved, q_out, k_out, v_out, stream):
+    dev = plan[3]
+    _current(dev)
     _check(lib().fab_qk_norm_rope(
-        q.data_ptr(), k.data_ptr(), vp, *tables, _ptr(pos, "pos", torch.int32, (B, N)), eps, 1 if interleaved else 0,
-        code, ctypes.byref(dims), _ptr(q_out, "q_out", dt, (B, H, N, DK)), _ptr(k_out, "k_out", dt, (B, Hkv, N, DK)),
-        vo, _raw_stream(stream, dev)), "fab_qk_norm_rope")
+        q.data_ptr(), k.data_ptr(), _addr(v), _addr(wq), _addr(wk), _addr(cos), _addr(sin), _addr(pos), eps,
+        1 if interleaved else 0, plan[2], plan[1], q_out.data_ptr(), k_out.data_ptr(), _addr(v_out),
+        _raw_stream(stream, dev)), "fab_qk_norm_rope")
+
+
+def fab_qk_norm_rope(q, k, v, wq, wk, cos, sin, pos, eps, interleaved, q_out, k_out, v_out, stream=None):
+    plan = _rope_plan(_layouts(q, k, v, wq, wk, cos, sin, pos))
+    d, dt = plan[0], q.dtype
+    _outputs(plan[3], (q_out, "q_out", dt, (d.B, d.H, d.N, d.DK)), (k_out, "k_out", dt, (d.B, d.Hkv, d.N, d.DK)),
+             (v_out, "v_out", dt, (d.B, d.Hkv, d.N, d.DV)))
+    _rope_call(plan, q, k, v, wq, wk, cos, sin, pos, eps, interleaved, q_out, k_out, v_out, stream)
 
 
 def fab_qk_norm_rope_backward_workspace_bytes(dims: fab_rope_dims) -> int:
     return lib().fab_qk_norm_rope_backward_workspace_bytes(ctypes.byref(dims))
 
 
-def _rope_backward_dims(dq, dk, dv, q, k, wq, wk, rot, P, gq, gk, gv):
-    B, H, N, DK = dq.shape
-    Hkv, DV = dk.shape[1], DK if dv is None else dv.shape[-1]
-    dt = gq.dtype
-    qs, ks = (B, N, H, DK), (B, N, Hkv, DK)
-    return fab_rope_dims(B, N, H, Hkv, DK, DV, rot, P, 0 if wq is None else _ld(q, "q", dt, qs),
-                         0 if wk is None else _ld(k, "k", dt, ks), 0, _ld(gq, "gq", dt, qs), _ld(gk, "gk", dt, ks),
-                         0 if gv is None else _ld(gv, "gv", dt, (B, N, Hkv, DV)))
+@functools.lru_cache(maxsize=1024)
+def _rope_backward_plan(layouts, dt, out):
+    """(dims, their reference, dtype code, device, workspace bytes) of a
+    fab_qk_norm_rope_backward call on dq, dk, dv, q, k, wq, wk, cos, sin, pos.
+    out: the layouts of gq, gk, gv, or None: one row holds all three."""
+    dq, dk, dv, q, k, wq, wk, cos, sin, pos = layouts
+    if len(dq[0]) != 4 or len(dk[0]) != 4:
+        raise ValueError("dq, dk must be 4-D: (B,H,N,DK), (B,Hkv,N,DK)")
+    B, H, N, DK = dq[0]
+    Hkv, DV = dk[0][1], DK if dv is None else dv[0][-1]
+    dev = _one_device(layouts if out is None else layouts + out)
+    rot, P = _tables(cos, sin, wq, wk, DK, dt)
+    f32 = torch.float32
+    _whole(dq, "dq", f32, dq[0])
+    _whole(dk, "dk", f32, (B, Hkv, N, DK))
+    _whole(dv, "dv", f32, (B, Hkv, N, DV))
+    _whole(pos, "pos", torch.int32, (B, N))
+    if (wq is not None and q is None) or (wk is not None and k is None):
+        raise ValueError("q and k are needed where wq and wk are given")
+    qs, ks, vs = (B, N, H, DK), (B, N, Hkv, DK), (B, N, Hkv, DV)
+    ldq, ldk = 0 if wq is None else _ld(q, "q", dt, qs), 0 if wk is None else _ld(k, "k", dt, ks)
+    if out is None:
+        ldg = [H * DK + Hkv * DK + (0 if dv is None else Hkv * DV)] * 3
+    else:
+        ldg = [0 if x is None else _ld(x, *to) for x, to in zip(out, (("gq", dt, qs), ("gk", dt, ks), ("gv", dt, vs)))]
+    dims = fab_rope_dims(B, N, H, Hkv, DK, DV, rot, P, ldq, ldk, 0, *ldg)
+    return dims, ctypes.byref(dims), _code(dt), dev, fab_qk_norm_rope_backward_workspace_bytes(dims)
+
+
+def _rope_backward_call(plan, dq, dk, dv, q, k, wq, wk, cos, sin, pos, eps, interleaved, ws, wsb, gq, gk, gv, gwq, gwk,
+                        stream):
+    dev = plan[3]
+    _current(dev)
+    _check(lib().fab_qk_norm_rope_backward(
+        dq.data_ptr(), dk.data_ptr(), _addr(dv), None if wq is None else q.data_ptr(),
+        None if wk is None else k.data_ptr(), _addr(wq), _addr(wk), _addr(cos), _addr(sin), _addr(pos), eps,
+        1 if interleaved else 0, plan[2], plan[1], _addr(ws), wsb, gq.data_ptr(), gk.data_ptr(), _addr(gv), _addr(gwq),
+        _addr(gwk), _raw_stream(stream, dev)), "fab_qk_norm_rope_backward")
 
 
 def fab_qk_norm_rope_backward(dq, dk, dv, q, k, wq, wk, cos, sin, pos, eps, interleaved, workspace, gq, gk, gv, gwq,
                               gwk, stream=None):
     """q and k are read only where wq and wk are given (None otherwise is fine)."""
-    if dq.dim() != 4 or dk.dim() != 4:
-        raise ValueError("dq, dk must be 4-D: (B,H,N,DK), (B,Hkv,N,DK)")
-    B, H, N, DK = dq.shape
-    dev = _here(dq, dk, dv, q, k, wq, wk, cos, sin, pos, workspace, gq, gk, gv, gwq, gwk)
-    rot, P, tables = _tables(cos, sin, wq, wk, DK, gq.dtype)
-    dims = _rope_backward_dims(dq, dk, dv, q, k, wq, wk, rot, P, gq, gk, gv)
-    f32 = torch.float32
-    _check(lib().fab_qk_norm_rope_backward(
-        _ptr(dq, "dq", f32, dq.shape), _ptr(dk, "dk", f32, (B, dims.Hkv, N, DK)),
-        _ptr(dv, "dv", f32, (B, dims.Hkv, N, dims.DV)), None if wq is None else q.data_ptr(),
-        None if wk is None else k.data_ptr(), *tables,
-        _ptr(pos, "pos", torch.int32, (B, N)), eps, 1 if interleaved else 0, dtype_code(gq),
-        ctypes.byref(dims), _addr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), gq.data_ptr(), gk.data_ptr(),
-        _addr(gv), _ptr(gwq, "gwq", f32, (DK,)), _ptr(gwk, "gwk", f32, (DK,)), _raw_stream(stream, dev)),
-        "fab_qk_norm_rope_backward")
+    plan = _rope_backward_plan(_layouts(dq, dk, dv, q, k, wq, wk, cos, sin, pos), gq.dtype, _layouts(gq, gk, gv))
+    f32, DK = torch.float32, plan[0].DK
+    _outputs(plan[3], (gwq, "gwq", f32, (DK,)), (gwk, "gwk", f32, (DK,)))
+    _rope_backward_call(plan, dq, dk, dv, q, k, wq, wk, cos, sin, pos, eps, interleaved, workspace,
+                        _bytes(workspace, plan[3]), gq, gk, gv, gwq, gwk, stream)
 
 
-def _paged_dims(H, T, k_cache, v_cache, starts, lens, table):
-    """dims of a paged call, its cache and its int32 arrays checked."""
-    if k_cache.dim() != 4 or v_cache.dim() != 4 or table.dim() != 2:
+def _paged_dims(H, T, dt, k_cache, v_cache, starts, lens, table):
+    """dims of a paged call, the layouts of its cache and its int32 arrays checked."""
+    if len(k_cache[0]) != 4 or len(v_cache[0]) != 4 or len(table[0]) != 2:
         raise ValueError("k_cache, v_cache must be 4-D (pages,Hkv,page,width), table 2-D (B,max_pages)")
-    pages, Hkv, page, DK = k_cache.shape
-    DV = v_cache.shape[3]
-    B, max_pages = table.shape
-    _ptr(k_cache, "k_cache", k_cache.dtype, k_cache.shape)
-    _ptr(v_cache, "v_cache", k_cache.dtype, (pages, Hkv, page, DV))
+    pages, Hkv, page, DK = k_cache[0]
+    DV = v_cache[0][3]
+    B, max_pages = table[0]
+    _whole(k_cache, "k_cache", dt, k_cache[0])
+    _whole(v_cache, "v_cache", dt, (pages, Hkv, page, DV))
     i32 = torch.int32
-    _ptr(starts, "starts", i32, (B + 1,))
-    _ptr(lens, "lens", i32, (B,))
-    _ptr(table, "table", i32, (B, max_pages))
+    _whole(starts, "starts", i32, (B + 1,))
+    _whole(lens, "lens", i32, (B,))
+    _whole(table, "table", i32, (B, max_pages))
     return fab_paged_dims(B, T, H, Hkv, DK, DV, page, pages, max_pages)
+
+
+@functools.lru_cache(maxsize=1024)
+def _append_plan(layouts):
+    """(dims, their reference, dtype code, device) of a fab_paged_append call on
+    q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cache."""
+    q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cache = layouts
+    if len(q[0]) != 3 or len(k[0]) != 3 or len(v[0]) != 3:
+        raise ValueError("q, k, v must be 3-D: (T,H,DK), (T,Hkv,DK), (T,Hkv,DV)")
+    T, H, DK = q[0]
+    dt = q[2]
+    code, dev = _code(dt), _one_device(layouts)
+    dims = _paged_dims(H, T, dt, k_cache, v_cache, starts, lens, table)
+    dims.rot, dims.P = _tables(cos, sin, wq, wk, DK, dt)
+    dims.ldq = _ld(q, "q", dt, (T, H, dims.DK))
+    dims.ldk = _ld(k, "k", dt, (T, dims.Hkv, DK))
+    dims.ldv = _ld(v, "v", dt, (T, dims.Hkv, dims.DV))
+    return dims, ctypes.byref(dims), code, dev
+
+
+def _append_call(plan, q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, q_out, k_cache, v_cache,
+                 stream):
+    dev = plan[3]
+    _current(dev)
+    _check(lib().fab_paged_append(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(wq), _addr(wk), _addr(cos), _addr(sin), eps,
+        1 if interleaved else 0, starts.data_ptr(), lens.data_ptr(), table.data_ptr(), plan[2], plan[1],
+        q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _raw_stream(stream, dev)), "fab_paged_append")
 
 
 def fab_paged_append(q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, q_out, k_cache, v_cache,
                      stream=None):
-    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
-        raise ValueError("q, k, v must be 3-D: (T,H,DK), (T,Hkv,DK), (T,Hkv,DV)")
-    T, H, DK = q.shape
-    dt = q.dtype
-    dev = _here(q, k, v, wq, wk, cos, sin, starts, lens, table, q_out, k_cache, v_cache)
-    dims = _paged_dims(H, T, k_cache, v_cache, starts, lens, table)
-    if k_cache.dtype != dt:
-        raise ValueError(f"k_cache must be {dt}, got {k_cache.dtype}")
-    dims.rot, dims.P, tables = _tables(cos, sin, wq, wk, DK, dt)
-    dims.ldq = _ld(q, "q", dt, (T, H, dims.DK))
-    dims.ldk = _ld(k, "k", dt, (T, dims.Hkv, DK))
-    dims.ldv = _ld(v, "v", dt, (T, dims.Hkv, dims.DV))
-    _check(lib().fab_paged_append(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), *tables, eps, 1 if interleaved else 0, starts.data_ptr(),
-        lens.data_ptr(), table.data_ptr(), dtype_code(q), ctypes.byref(dims), _ptr(q_out, "q_out", dt, (T, H, DK)),
-        k_cache.data_ptr(), v_cache.data_ptr(), _raw_stream(stream, dev)), "fab_paged_append")
+    plan = _append_plan(_layouts(q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cache))
+    _outputs(plan[3], (q_out, "q_out", q.dtype, q.shape))
+    _append_call(plan, q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, q_out, k_cache, v_cache,
+                 stream)
 
 
 def fab_paged_attention_workspace_bytes(dims: fab_paged_dims, dtype: int) -> int:
     return lib().fab_paged_attention_workspace_bytes(ctypes.byref(dims), int(dtype))
 
 
+@functools.lru_cache(maxsize=1024)
+def _paged_plan(layouts):
+    """(dims, their reference, dtype code, device, workspace bytes) of a
+    fab_paged_attention call on q, k_cache, v_cache, starts, lens, table."""
+    q, k_cache, v_cache, starts, lens, table = layouts
+    if len(q[0]) != 3:
+        raise ValueError("q must be 3-D: (T,H,DK)")
+    T, H, DK = q[0]
+    dt = q[2]
+    code, dev = _code(dt), _one_device(layouts)
+    dims = _paged_dims(H, T, dt, k_cache, v_cache, starts, lens, table)
+    _whole(q, "q", dt, (T, H, dims.DK))
+    return dims, ctypes.byref(dims), code, dev, fab_paged_attention_workspace_bytes(dims, code)
+
+
+def _paged_call(plan, q, k_cache, v_cache, starts, lens, table, causal, scale, ws, wsb, o, lse, stream):
+    dev = plan[3]
+    _current(dev)
+    _check(lib().fab_paged_attention(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), starts.data_ptr(), lens.data_ptr(), table.data_ptr(),
+        1 if causal else 0, float(scale), plan[2], plan[1], _addr(ws), wsb, o.data_ptr(), _addr(lse),
+        _raw_stream(stream, dev)), "fab_paged_attention")
+
+
 def fab_paged_attention(q, k_cache, v_cache, starts, lens, table, causal, scale, workspace, o, lse, stream=None):
     """lse may be None."""
-    if q.dim() != 3:
-        raise ValueError("q must be 3-D: (T,H,DK)")
-    T, H, DK = q.shape
-    dt = q.dtype
-    dev = _here(q, k_cache, v_cache, starts, lens, table, workspace, o, lse)
-    dims = _paged_dims(H, T, k_cache, v_cache, starts, lens, table)
-    if k_cache.dtype != dt:
-        raise ValueError(f"k_cache must be {dt}, got {k_cache.dtype}")
-    _check(lib().fab_paged_attention(
-        _ptr(q, "q", dt, (T, H, dims.DK)), k_cache.data_ptr(), v_cache.data_ptr(), starts.data_ptr(),
-        lens.data_ptr(), table.data_ptr(), int(bool(causal)), float(scale), dtype_code(q), ctypes.byref(dims),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(o, "o", dt, (T, H, dims.DV)),
-        _ptr(lse, "lse", torch.float32, (H, T)), _raw_stream(stream, dev)), "fab_paged_attention")
-
-
-# ------------------------------------------------------------------ conveniences (torch allocates, libfab computes)
+    plan = _paged_plan(_layouts(q, k_cache, v_cache, starts, lens, table))
+    T, H = q.shape[:2]
+    _outputs(plan[3], (o, "o", q.dtype, (T, H, plan[0].DV)), (lse, "lse", torch.float32, (H, T)))
+    _paged_call(plan, q, k_cache, v_cache, starts, lens, table, causal, scale, workspace, _bytes(workspace, plan[3]), o,
+                lse, stream)
 
 
 def _on(stream):
@@ -489,29 +595,18 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
-@functools.lru_cache(maxsize=256)
-def _rope_workspace(B, N, H, Hkv, DK):
-    return max(fab_qk_norm_rope_backward_workspace_bytes(fab_rope_dims(B, N, H, Hkv, DK, DK)), 16)
-
-
-@functools.lru_cache(maxsize=256)
-def _paged_workspace(dtype, *dims):
-    return max(fab_paged_attention_workspace_bytes(fab_paged_dims(*dims), dtype), 16)
-
-
 def qk_norm_rope(q, k, v, wq=None, wk=None, cos=None, sin=None, pos=None, eps=1e-6, interleaved=False, stream=None):
     """Projection rows q (B,N,H,DK), k (B,N,Hkv,DK), v (B,N,Hkv,DV) or None to
     what forward() takes: q (B,H,N,DK), k (B,Hkv,N,DK) normalised per head
     (where weights are given) and rotated (where tables are), v (B,Hkv,N,DV)."""
-    if q.dim() != 4 or k.dim() != 4:
-        raise ValueError("q, k must be 4-D: (B,N,H,DK), (B,N,Hkv,DK)")
-    B, N, H, DK = q.shape
+    plan = _rope_plan(_layouts(q, k, v, wq, wk, cos, sin, pos))
     with _on(stream):
+        B, N, H, DK = q.shape
         dt, dev = q.dtype, q.device
         qo = torch.empty((B, H, N, DK), dtype=dt, device=dev)
         ko = torch.empty((B, k.shape[2], N, DK), dtype=dt, device=dev)
         vo = None if v is None else torch.empty((B, v.shape[2], N, v.shape[3]), dtype=dt, device=dev)
-        fab_qk_norm_rope(q, k, v, wq, wk, cos, sin, pos, eps, interleaved, qo, ko, vo, stream)
+        _rope_call(plan, q, k, v, wq, wk, cos, sin, pos, eps, interleaved, qo, ko, vo, stream)
     return qo, ko, vo
 
 
@@ -522,26 +617,26 @@ def qk_norm_rope_backward(dq, dk, dv, q, k, wq=None, wk=None, cos=None, sin=None
     or None, gwq, gwk float32 (DK,) or None).  gq, gk and gv are in `dtype`
     (None: q's) and are views of one row of H*DK + Hkv*DK + Hkv*DV values a
     token: gq._base is the gradient of a fused projection."""
-    if dq.dim() != 4 or dk.dim() != 4:
-        raise ValueError("dq, dk must be 4-D: (B,H,N,DK), (B,Hkv,N,DK)")
-    B, H, N, DK = dq.shape
-    Hkv = dk.shape[1]
     dtype = q.dtype if dtype is None else dtype
-    nq, nk, nv = H * DK, Hkv * DK, 0 if dv is None else dv.shape[1] * dv.shape[3]
+    plan = _rope_backward_plan(_layouts(dq, dk, dv, q, k, wq, wk, cos, sin, pos), dtype, None)
+    B, H, N, DK = dq.shape
+    Hkv, row, dev = dk.shape[1], plan[0].ldgq, dq.device
     with _on(stream):
-        g = torch.empty((B, N, nq + nk + nv), dtype=dtype, device=dq.device)
-        gq = g.as_strided((B, N, H, DK), (N * g.shape[2], g.shape[2], DK, 1))
-        gk = g.as_strided((B, N, Hkv, DK), (N * g.shape[2], g.shape[2], DK, 1), nq)
+        g = torch.empty((B, N, row), dtype=dtype, device=dev)
+        gq = g.as_strided((B, N, H, DK), (N * row, row, DK, 1))
+        gk = g.as_strided((B, N, Hkv, DK), (N * row, row, DK, 1), H * DK)
         gv = None
         if dv is not None:
-            gv = g.as_strided((B, N, dv.shape[1], dv.shape[3]), (N * g.shape[2], g.shape[2], dv.shape[3], 1), nq + nk)
-        gwq = None if wq is None else torch.empty((DK,), dtype=torch.float32, device=dq.device)
-        gwk = None if wk is None else torch.empty((DK,), dtype=torch.float32, device=dq.device)
-        ws = None
+            DV = dv.shape[3]
+            gv = g.as_strided((B, N, Hkv, DV), (N * row, row, DV, 1), (H + Hkv) * DK)
+        gwq = None if wq is None else torch.empty((DK,), dtype=torch.float32, device=dev)
+        gwk = None if wk is None else torch.empty((DK,), dtype=torch.float32, device=dev)
+        ws, wsb = None, 0
         if wq is not None or wk is not None:
-            ws = torch.empty(_rope_workspace(B, N, H, Hkv, DK), dtype=torch.uint8, device=dq.device)
-        fab_qk_norm_rope_backward(dq, dk, dv, q, k, wq, wk, cos, sin, pos, eps, interleaved, ws, gq, gk, gv, gwq, gwk,
-                                  stream)
+            wsb = plan[4]
+            ws = torch.empty((wsb,), dtype=torch.uint8, device=dev)
+        _rope_backward_call(plan, dq, dk, dv, q, k, wq, wk, cos, sin, pos, eps, interleaved, ws, wsb, gq, gk, gv, gwq,
+                            gwk, stream)
     return gq, gk, gv, gwq, gwk
 
 
@@ -550,9 +645,11 @@ def paged_append(q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cach
     """Puts the new tokens' keys and values into the caches and returns their
     queries (T,H,DK), normalised and rotated as qk_norm_rope does; rows of
     padding tokens are left as allocated."""
+    plan = _append_plan(_layouts(q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cache))
     with _on(stream):
         qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        fab_paged_append(q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, qo, k_cache, v_cache, stream)
+        _append_call(plan, q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, qo, k_cache, v_cache,
+                     stream)
     return qo
 
 
@@ -560,23 +657,24 @@ def alloc_paged(q, k_cache, v_cache, table):
     """A workspace (uint8 tensor) for fab_paged_attention calls of these sizes."""
     pages, Hkv, page, DK = k_cache.shape
     B, max_pages = table.shape
-    wsb = _paged_workspace(dtype_code(q), B, q.shape[0], q.shape[1], Hkv, DK, v_cache.shape[3], page, pages, max_pages)
+    dims = fab_paged_dims(B, q.shape[0], q.shape[1], Hkv, DK, v_cache.shape[3], page, pages, max_pages)
+    wsb = fab_paged_attention_workspace_bytes(dims, dtype_code(q))
     return torch.empty(wsb, dtype=torch.uint8, device=q.device)
 
 
 def paged_attention(q, k_cache, v_cache, starts, lens, table, causal=True, scale=None, stream=None):
     """Returns (o (T,H,DV) in q's dtype, lse (H,T) float32); rows of padding
     tokens are left as allocated."""
-    scale = q.shape[-1] ** -0.5 if scale is None else scale
+    plan = _paged_plan(_layouts(q, k_cache, v_cache, starts, lens, table))
+    T, H, DK = q.shape
+    scale = DK ** -0.5 if scale is None else scale
     with _on(stream):
-        T, H, dev = q.shape[0], q.shape[1], q.device
-        o = torch.empty((T, H, v_cache.shape[-1]), dtype=q.dtype, device=dev)
+        dev, wsb = q.device, plan[4]
+        o = torch.empty((T, H, v_cache.shape[3]), dtype=q.dtype, device=dev)
         lse = torch.empty((H, T), dtype=torch.float32, device=dev)
-        ws = alloc_paged(q, k_cache, v_cache, table)
-        fab_paged_attention(q, k_cache, v_cache, starts, lens, table, causal, scale, ws, o, lse, stream)
+        ws = torch.empty((wsb,), dtype=torch.uint8, device=dev)
+        _paged_call(plan, q, k_cache, v_cache, starts, lens, table, causal, scale, ws, wsb, o, lse, stream)
     return o, lse
-
-
 
 
 def forward(q, k, v, mask=None, causal=False, scale=None, stream=None):
