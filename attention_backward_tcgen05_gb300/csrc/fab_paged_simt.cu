@@ -87,9 +87,16 @@ FAB_DEV float4 lds4(const T* p) {
   }
 }
 
+// Of a pair of values in each of two lanes, `bit` apart: the lane whose bit is
+// set gets the sum of both lanes' second, the other that of their first.
+FAB_DEV float halve(bool set, float first, float second, int bit) {
+  const float keep = set ? second : first, give = set ? first : second;
+  return keep + __shfl_xor_sync(0xffffffffu, give, bit);
+}
+
 template <typename T, int R, int CPL>
 __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_constant__ SimtParams p) {
-  static_assert(R % 4 == 0 && CPL % 4 == 0, "");
+  static_assert((R == 4 || R == 8 || R == 16) && CPL % 4 == 0, "");
   constexpr int RPL = R / 4;  // rows a lane scores
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ PagedShared sh;
@@ -117,7 +124,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
   uint8_t* ring = ring0 + warp * p.stages * stage_bytes;
   float* acc_s = reinterpret_cast<float*>(ring0);            // at a unit's end: [warp][R][dp]
   float2* ml_s = reinterpret_cast<float2*>(acc_s + kWarps * R * p.parts.dp);  // [warp][R]
-  const int key = lane & 7, rg = lane >> 3;  // scores: this lane's key, its rows rg * RPL ..
+  const int key = lane & 7, rg = lane >> 3;  // this lane's key, its rows rg * RPL ..
+  // sums: DG lanes share a block of 4 rows and 4 keys, every DG-th piece of 4 columns each
+  constexpr int DG = 64 / R;
+  const int kg = (lane >> 2) & 1, dg = rg % (DG / 4) * 4 + (lane & 3);
+  const float* q_r = q_s + rg / (DG / 4) * 4 * p.qs;
   const T* kc = static_cast<const T*>(p.k);
   const T* vc = static_cast<const T*>(p.v);
 
@@ -211,25 +222,47 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
       }
       cp_async_wait(p.stages - 1);
       __syncwarp();
-      const T* kr = reinterpret_cast<const T*>(ring + slot * stage_bytes + key * p.ks);
+      const uint8_t* kb = ring + slot * stage_bytes + kg * 4 * p.ks;
       const T* vb = reinterpret_cast<const T*>(ring + slot * stage_bytes + kKeys * p.ks);
-      float s[RPL], s4[RPL][4];  // (four sums a score: a chain of multiply-adds is a quarter as long)
+      float part[4][4];  // [row][key] over this lane's columns
 #pragma unroll
-      for (int e = 0; e < RPL; ++e) s4[e][0] = s4[e][1] = s4[e][2] = s4[e][3] = 0.f;
-#pragma unroll 4
-      for (int d = 0; d < p.qs; d += 4) {
-        const float4 kv = lds4(kr + d);
+      for (int e = 0; e < 4; ++e) part[e][0] = part[e][1] = part[e][2] = part[e][3] = 0.f;
+#pragma unroll 2
+      for (int d = dg * 4; d < p.qs; d += DG * 4) {
+        float4 kv[4];
 #pragma unroll
-        for (int e = 0; e < RPL; ++e) {
-          const float4 qv = *reinterpret_cast<const float4*>(q_s + (rg * RPL + e) * p.qs + d);
-          s4[e][0] = fmaf(qv.x, kv.x, s4[e][0]);
-          s4[e][1] = fmaf(qv.y, kv.y, s4[e][1]);
-          s4[e][2] = fmaf(qv.z, kv.z, s4[e][2]);
-          s4[e][3] = fmaf(qv.w, kv.w, s4[e][3]);
+        for (int k = 0; k < 4; ++k) kv[k] = lds4(reinterpret_cast<const T*>(kb + k * p.ks) + d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 qv = *reinterpret_cast<const float4*>(q_r + e * p.qs + d);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            part[e][k] = fmaf(qv.x, kv[k].x, fmaf(qv.y, kv[k].y, fmaf(qv.z, kv[k].z, fmaf(qv.w, kv[k].w, part[e][k]))));
         }
       }
+      __syncwarp();
+      // the lanes of a block sum theirs up, each keeping half of what is left: a
+      // key for each of four lanes, then rows
+      float s[RPL];
+      {
+        const bool b0 = lane & 1, b1 = lane & 2, b3 = lane & 8, b4 = lane & 16;
+        float two[4][2], one[4];
 #pragma unroll
-      for (int e = 0; e < RPL; ++e) s[e] = (s4[e][0] + s4[e][1]) + (s4[e][2] + s4[e][3]);
+        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) two[e][k] = halve(b1, part[e][k], part[e][2 + k], 2);
+          one[e] = halve(b0, two[e][0], two[e][1], 1);
+        }
+        if constexpr (RPL == 4) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[e] = one[e];
+        } else if constexpr (RPL == 2) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) s[e] = halve(b3, one[e], one[2 + e], 8);
+        } else {
+          s[0] = halve(b3, halve(b4, one[0], one[2], 16), halve(b4, one[1], one[3], 16), 8);
+        }
+      }
       const int mk = j * 64 + warp * kKeys + key;
       bool grew = false;
       float f[RPL];
