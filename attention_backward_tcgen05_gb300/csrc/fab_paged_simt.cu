@@ -10,16 +10,20 @@
 // The work is shared out as on the tensor cores (fab_paged.cuh), with tiles of
 // R rows and key tiles of 64.  Each of a CTA's eight warps owns 8 keys of every
 // key tile, from the copy to the sum: it fetches their rows into a ring of its
-// own with asynchronous copies, keeps a running maximum and sum of its own, and
-// adds its keys' share to an output of its own, so that the loop has no barrier
-// for the block.  The warps' shares meet at the unit's end.  Scores: a lane
-// takes R / 4 rows of one key; the output: a lane takes CPL columns of all R
-// rows, so a value is read from shared memory once for R rows.
+// own with bulk copies (a lane a row), keeps a running maximum and sum of its
+// own, and adds its keys' share to an output of its own, so that the loop has no
+// barrier for the block.  The warps' shares meet at the unit's end.  Scores: 64 / R
+// lanes share a block of 4 rows and 4 keys, each summing its part of the
+// columns (8 reads of shared memory for 64 multiply-adds), and add up by
+// shuffles that leave each lane R / 4 rows of one key; the output: a lane takes
+// CPL columns of all R rows, so a value is read from shared memory once for R
+// rows.
 //
-// Bound by shared-memory reads (5 for 16 multiply-adds of the scores, 5 for 64 of
-// the output) and by the latency of a tile's steps, which eight warps hide only
-// in part: f32, one sequence of 100,000 keys, 32 heads on 8, width 128 takes 282
-// us, 2.9 TB/s.
+// Few rows a sequence: bound by memory (f32, one sequence of 100,000 keys, 32
+// heads on 8, width 128: 153 us, 5.4 TB/s).  More: by the latency of a tile's
+// steps, of which two warps a scheduler hide only a part (chunks of 60 tokens on
+// 2,000 keys 107 us).  Copies of 16 bytes by every lane in place of the bulk copies
+// took 249 and 142 us: a third of the instructions and more was theirs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -38,7 +42,8 @@ __device__ uint32_t g_err_paged;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kKeys = 8;  // keys of a tile that a warp owns
+constexpr int kKeys = 8;    // keys of a tile that a warp owns
+constexpr int kStages = 4;  // of a warp's ring, at most
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -51,24 +56,12 @@ struct SimtParams {
   int ks, vs;          // bytes of a key and a value row in the ring (multiples of 16)
   int qs;              // floats of a query row in shared memory (a multiple of 4, zero past DK)
   int stages;          // of a warp's ring
-  int vec;             // rows come in whole aligned 16-byte pieces
+  int bulk;            // rows come in whole aligned 16-byte pieces
   float c1;            // scale log2 e
   const void *q, *k, *v;
   void* o;
   float* lse;
 };
-
-FAB_DEV void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {  // bytes 16, or 0: zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-FAB_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// Waits for all but the latest n (0 .. 3) groups.
-FAB_DEV void cp_async_wait(int n) {
-  if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else asm volatile("cp.async.wait_group 3;" ::: "memory");
-}
 
 FAB_DEV float to_f32(float x) { return x; }
 FAB_DEV float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -100,8 +93,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
   constexpr int RPL = R / 4;  // rows a lane scores
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ PagedShared sh;
+  __shared__ uint64_t bars[kWarps][kStages];  // a ring slot's rows have landed
+  __shared__ uint32_t abort_s;
+  volatile uint32_t* abort_flag = &abort_s;
   const PagedPlan& plan = p.plan;
   const int lane = (int)lane_id(), warp = (int)warp_id();
+  if (lane < kStages) mbar_init(smem_u32(&bars[warp][lane]), 1);
+  if (threadIdx.x == 0) abort_s = 0u;
+  fence_mbar_init();
   asm volatile("griddepcontrol.wait;" ::: "memory");  // (launched early: lengths and operands from here on)
   if (blockIdx.x == 0) check_starts(plan.starts, plan.B, plan.T, (int)threadIdx.x, kThreads, &g_err_paged);
   int64_t mine;
@@ -132,13 +131,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
   const T* kc = static_cast<const T*>(p.k);
   const T* vc = static_cast<const T*>(p.v);
 
+  int in = 0, out = 0;      // the ring's slots to fill and to work on next
+  uint32_t out_phase = 0;
   PagedWalk w;
   w.begin(plan, start);
   for (bool more = w.seek(plan, p0, p1); more; more = w.next(plan) && w.seek(plan, p0, p1)) {
     const int hk = w.at.head / plan.gblocks, gb = w.at.head - hk * plan.gblocks;
     const int token0 = w.at.i * plan.nt;
     // the unit's queries, zero where there is no row
+    fence_proxy_async_smem();  // (the rings held the shares of the unit before)
     __syncthreads();
+    if (*abort_flag) break;
     for (int x = (int)threadIdx.x; x < R * p.qs; x += kThreads) {
       const int r = x / p.qs, d = x - r * p.qs, i = r / plan.gw, g = gb * plan.gw + r - i * plan.gw;
       float v = 0.f;
@@ -175,25 +178,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
       atomicOr(&g_err_paged, kErrIndex);  // (its key and value are zeros)
       return -1;
     };
-    // copies the 8 rows `row` names into the ring's slot, zeros for -1
-    auto fetch = [&](int64_t row, int slot) {
-      uint8_t* kd = ring + slot * stage_bytes;
+    // copies the 8 rows `row` names into the ring's next slot, zeros for -1
+    auto fetch = [&](int64_t row) {
+      uint8_t* kd = ring + in * stage_bytes;
       uint8_t* vd = kd + kKeys * p.ks;
-      if (p.vec) {
-        // 16-byte pieces of keys, then of values; a row's pieces side by side
-        const int kp = p.DK * (int)sizeof(T) / 16, per = kp + p.DV * (int)sizeof(T) / 16;
-        int kk = 0, c = lane;
-        for (int left = kKeys * per; left > 0; left -= 32) {
-          while (c >= per) c -= per, ++kk;
-          const int64_t src = __shfl_sync(0xffffffffu, row, kk & 7);
-          if (kk < kKeys) {
-            const bool isk = c < kp;
-            const uint8_t* from = isk ? reinterpret_cast<const uint8_t*>(kc + (src < 0 ? 0 : src) * p.DK) + c * 16
-                                      : reinterpret_cast<const uint8_t*>(vc + (src < 0 ? 0 : src) * p.DV) + (c - kp) * 16;
-            cp_async16(smem_u32(isk ? kd + kk * p.ks + c * 16 : vd + kk * p.vs + (c - kp) * 16), from,
-                       src < 0 ? 0u : 16u);
-          }
-          c += 32;
+      if (p.bulk) {
+        // a lane a row: lanes 0 .. 7 the keys, 8 .. 15 the values
+        const uint32_t kbytes = p.DK * (int)sizeof(T), vbytes = p.DV * (int)sizeof(T);
+        const uint32_t here = __ballot_sync(0xffffffffu, row >= 0) & 0xffu, bar = smem_u32(&bars[warp][in]);
+        for (uint32_t gone = here ^ 0xffu; gone != 0; gone &= gone - 1) {
+          const int kk = __ffs((int)gone) - 1;
+          for (uint32_t x = lane * 16; x < kbytes; x += 512) st_shared_v4(smem_u32(kd + kk * p.ks) + x, 0u, 0u, 0u, 0u);
+          for (uint32_t x = lane * 16; x < vbytes; x += 512) st_shared_v4(smem_u32(vd + kk * p.vs) + x, 0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+        }
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)__popc(here) * (kbytes + vbytes));
+        __syncwarp();
+        if (lane < 16 && row >= 0) {
+          if (lane < 8)
+            bulk_load(smem_u32(kd + key * p.ks), kc + row * p.DK, kbytes, bar);
+          else
+            bulk_load(smem_u32(vd + key * p.vs), vc + row * p.DV, vbytes, bar);
         }
       } else {
         for (int kk = 0; kk < kKeys; ++kk) {
@@ -206,24 +211,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
           for (int d = lane; d < p.DV; d += 32) vr[d] = src >= 0 ? vf[d] : T(0.f);
         }
       }
-      cp_async_commit();
+      if (++in == p.stages) in = 0;
     };
 
     __syncwarp();
-    for (int s = 0; s + 1 < p.stages; ++s) fetch(lookup(w.j0 + s), s);
-    int64_t next = lookup(w.j0 + p.stages - 1);  // of the next fetch: looked up a tile ahead
-    int slot = 0;
+    const int ahead = p.stages - 1;  // tiles on their way
+    for (int s = 0; s < ahead && w.j0 + s < w.j1; ++s) fetch(lookup(w.j0 + s));
+    int64_t next = lookup(w.j0 + ahead);  // of the next fetch: looked up a tile ahead
     for (int j = w.j0; j < w.j1; ++j) {
-      {
-        int ahead = slot + p.stages - 1;
-        if (ahead >= p.stages) ahead -= p.stages;
-        fetch(next, ahead);
+      if (j + ahead < w.j1) {
+        fetch(next);
         next = lookup(j + p.stages);
       }
-      cp_async_wait(p.stages - 1);
+      if (p.bulk && !__all_sync(0xffffffffu, mbar_wait_asleep(smem_u32(&bars[warp][out]), out_phase, abort_flag,
+                                                              &g_err_paged))) {
+        // give up: let what is on its way land before shared memory goes
+        for (int left = (j + p.stages < w.j1 ? j + p.stages : w.j1) - j; left > 0; --left) {
+          mbar_drain(smem_u32(&bars[warp][out]), out_phase);
+          if (++out == p.stages) out = 0, out_phase ^= 1u;
+        }
+        break;
+      }
       __syncwarp();
-      const uint8_t* kb = ring + slot * stage_bytes + kg * 4 * p.ks;
-      const T* vb = reinterpret_cast<const T*>(ring + slot * stage_bytes + kKeys * p.ks);
+      const uint8_t* kb = ring + out * stage_bytes + kg * 4 * p.ks;
+      const uint8_t* vb = ring + out * stage_bytes + kKeys * p.ks;
       float part[4][4];  // [row][key] over this lane's columns
 #pragma unroll
       for (int e = 0; e < 4; ++e) part[e][0] = part[e][1] = part[e][2] = part[e][3] = 0.f;
@@ -300,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
       }
 #pragma unroll
       for (int kk = 0; kk < kKeys; ++kk) {
-        const T* vr = reinterpret_cast<const T*>(reinterpret_cast<const uint8_t*>(vb) + kk * p.vs);
+        const T* vr = reinterpret_cast<const T*>(vb + kk * p.vs);
 #pragma unroll
         for (int c = 0; c < CPL; c += 4) {
           const int col = (c / 4) * 128 + lane * 4;
@@ -321,10 +332,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
         }
       }
       __syncwarp();  // the slot and the weights may be written again
-      if (++slot == p.stages) slot = 0;
+      if (++out == p.stages) out = 0, out_phase ^= 1u;
     }
     // ---- the unit's end: the warps' shares
-    cp_async_wait(0);
 #pragma unroll
     for (int e = 0; e < RPL; ++e)
 #pragma unroll
@@ -353,22 +363,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
 #pragma unroll
       for (int v = 0; v < kWarps; ++v) top = fmaxf(top, ml_s[v * R + r].x);
       const float ref = top == -INFINITY ? 0.f : top;
-      float sum = 0.f, out = 0.f;
+      float sum = 0.f, val = 0.f;
 #pragma unroll
       for (int v = 0; v < kWarps; ++v) {
         const float2 ml = ml_s[v * R + r];
         if (ml.y == 0.f) continue;  // (no key: its output is zero)
         const float f = exp2f(ml.x - ref);
         sum += f * ml.y;
-        out += f * acc_s[(v * R + r) * dp + col];
+        val += f * acc_s[(v * R + r) * dp + col];
       }
       const int64_t t = w.q.s0 + token0 + i, h = (int64_t)hk * plan.G + g;
       if (whole) {
-        if (col < p.DV) paged_store(static_cast<T*>(p.o) + (t * p.H + h) * p.DV + col, sum == 0.f ? 0.f : out / sum);
+        if (col < p.DV) paged_store(static_cast<T*>(p.o) + (t * p.H + h) * p.DV + col, sum == 0.f ? 0.f : val / sum);
         if (col == 0 && p.lse != nullptr) p.lse[h * plan.T + t] = sum == 0.f ? INFINITY : (ref + log2f(sum)) * kLn2;
       } else {
         const int64_t at = (int64_t)w.slot((int)blockIdx.x) * p.parts.rows + r;
-        p.parts.out[at * dp + col] = out;
+        p.parts.out[at * dp + col] = val;
         if (col == 0) p.parts.ml[at] = make_float2(ref, sum);
       }
     }
@@ -421,7 +431,7 @@ cudaError_t launch_r(const PagedProblem& pr, int sms, cudaStream_t s) {
   p.qs = (p.DK + 3) / 4 * 4;
   p.ks = (p.qs * e + 15) / 16 * 16 + 16;  // (16 more: eight keys' rows start in different banks)
   p.vs = (dp_of(pr) * e + 15) / 16 * 16;
-  p.vec = p.DK * e % 16 == 0 && p.DV * e % 16 == 0;
+  p.bulk = p.DK * e % 16 == 0 && p.DV * e % 16 == 0;
   p.c1 = pr.scale * kLog2e;
   p.q = pr.q;
   p.k = pr.k;
@@ -431,7 +441,7 @@ cudaError_t launch_r(const PagedProblem& pr, int sms, cudaStream_t s) {
   const int fixed = (R * p.qs + kWarps * (kKeys + 1) * R) * 4, stage = kWarps * kKeys * (p.ks + p.vs);
   const int end = kWarps * R * (p.parts.dp + 2) * 4;  // the warps' shares, over the rings
   p.stages = (kSmemLimit - fixed) / stage;
-  p.stages = p.stages > 4 ? 4 : p.stages < 1 ? 1 : p.stages;
+  p.stages = p.stages > kStages ? kStages : p.stages < 1 ? 1 : p.stages;
   const int smem = fixed + (p.stages * stage > end ? p.stages * stage : end);
   const int64_t units = (pr.T / p.plan.nt + pr.B) * p.plan.heads, tiles = (p.plan.max_keys + 63) / 64;
   int grid = sms < kPagedMaxGrid ? sms : kPagedMaxGrid;
