@@ -75,12 +75,12 @@ struct PCfg {
   static constexpr int ATOMS = DP / 64;
   static constexpr uint32_t ATOM = 128 * 128;  // 128 rows of 128 swizzled bytes
   static constexpr uint32_t TILE = ATOMS * ATOM;
-  static constexpr int NK = DP == 128 ? 2 : 4, NV = DP == 128 ? 3 : 4;  // ring slots
+  static constexpr int NQ = DP == 128 ? 2 : 4, NK = NQ, NV = DP == 128 ? 3 : 4;  // ring slots
   static constexpr uint32_t OFF_Q = 0;
-  static constexpr uint32_t OFF_K = 2 * TILE;
+  static constexpr uint32_t OFF_K = NQ * TILE;
   static constexpr uint32_t OFF_V = OFF_K + NK * TILE;
   static constexpr uint32_t OFF_BAR = OFF_V + NV * TILE;
-  static constexpr uint32_t OFF_MISC = OFF_BAR + 48 * 8;
+  static constexpr uint32_t OFF_MISC = OFF_BAR + 52 * 8;
   static constexpr uint32_t OFF_UNIT = OFF_MISC + 16;       // kUnits descriptions of units
   static constexpr uint32_t OFF_ML = OFF_UNIT + kUnits * 64;  // 128 (maximum, sum) pairs; the plan's scratch before
   static constexpr uint32_t USED = OFF_ML + 128 * 8;
@@ -102,18 +102,18 @@ enum : int {
   B_VF = 8,   // + slot: V landed
   B_VE = 12,  // + slot: V free
   B_QF = 16,  // + slot: Q landed
-  B_QE = 18,  // + slot: Q free
-  B_S = 20,   // + buffer: S landed
-  B_P = 23,   // + 2 buffer + half: P's keys of that half written (and O rescaled where it had to be);
+  B_QE = 20,  // + slot: Q free
+  B_S = 24,   // + buffer: S landed
+  B_P = 27,   // + 2 buffer + half: P's keys of that half written (and O rescaled where it had to be);
               // with three buffers only + 1, for both
-  B_PV = 29,  // + buffer: O += P V finished (three buffers only)
-  B_O = 32,   // + stream: the unit's last product of the stream finished
-  B_ML = 34,  // one-tile units: stream 1's maxima and sums are in shared memory
-  B_MD = 35,  // one-tile units: stream 0 has read stream 1's output
-  B_FIN = 36,
-  B_DF = 37,  // + slot: a unit is described
-  B_DE = 41,  // + slot: every warp is done with it
-  B_COUNT = 45
+  B_PV = 33,  // + buffer: O += P V finished (three buffers only)
+  B_O = 36,   // + stream: the unit's last product of the stream finished
+  B_ML = 38,  // one-tile units: stream 1's maxima and sums are in shared memory
+  B_MD = 39,  // one-tile units: stream 0 has read stream 1's output
+  B_FIN = 40,
+  B_DF = 41,  // + slot: a unit is described
+  B_DE = 45,  // + slot: every warp is done with it
+  B_COUNT = 49
 };
 
 struct TcParams {
@@ -160,14 +160,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(B_KE + s), 1);
       mbar_init(bar(B_VF + s), 1);
       mbar_init(bar(B_VE + s), 1);
+      mbar_init(bar(B_QF + s), 1);
+      mbar_init(bar(B_QE + s), 1);
       mbar_init(bar(B_DF + s), 1);
       mbar_init(bar(B_DE + s), 3 + 8);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(B_QF + s), 1);
-      mbar_init(bar(B_QE + s), 1);
-      mbar_init(bar(B_O + s), 1);
-    }
+    mbar_init(bar(B_O), 1);
+    mbar_init(bar(B_O + 1), 1);
     for (int s = 0; s < 3; ++s) {
       mbar_init(bar(B_S + s), 1);
       mbar_init(bar(B_P + 2 * s), 4);
@@ -280,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_3d(sbase + C::OFF_Q + qslot * C::TILE + a * C::ATOM, &tmQ, bar(B_QF + qslot), a * 64,
                             hk * plan.G + u.g0, u.s0 + u.token0 + s * plan.nt);
             }
-            if (++qslot == 2) qslot = 0, qphase ^= 1;
+            if (++qslot == C::NQ) qslot = 0, qphase ^= 1;
           }
           if (!ok) break;
         }
@@ -310,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok && lane == 0) {
         for (int s = 0; s < slots; ++s) mbar_drain(bar(full + s), s < slot ? phase ^ 1 : phase);
         if (keys)
-          for (int s = 0; s < 2; ++s) mbar_drain(bar(B_QF + s), s < qslot ? qphase ^ 1 : qphase);
+          for (int s = 0; s < C::NQ; ++s) mbar_drain(bar(B_QF + s), s < qslot ? qphase ^ 1 : qphase);
       }
     } else {
       // ------------------------------------------------------------ products
@@ -397,9 +396,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A unit of two row tiles: per key tile O_0, S_0, O_1, S_1, so that each
         // stream's softmax runs beside the other's products.
         auto two_tiles = [&](const UnitPart& x) -> bool {
-          const uint32_t tiles = (uint32_t)(x.j1 - x.j0), last = last_of(x), q0 = qn & 1u, q1 = q0 ^ 1u;
+          const uint32_t tiles = (uint32_t)(x.j1 - x.j0), last = last_of(x);
+          const uint32_t q0 = qn % C::NQ, q1 = (qn + 1) % C::NQ;
           const uint32_t a0 = q_lo + q0 * SLOT, a1 = q_lo + q1 * SLOT;
-          if (!wait(B_QF + q0, (qn >> 1) & 1u) || !wait(B_QF + q1, ((qn + 1) >> 1) & 1u)) return false;
+          if (!wait(B_QF + q0, (qn / C::NQ) & 1u) || !wait(B_QF + q1, ((qn + 1) / C::NQ) & 1u)) return false;
           qn += 2;
           if constexpr (NB == 3) {
             const uint32_t steps = 2 * tiles;
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!wait(B_DF + sd, sdp)) return false;
             const UnitPart& u = units[sd];
             if (!u.more || u.width == 2) return true;
-            const uint32_t qs = qn & 1u, qp = (qn >> 1) & 1u;
+            const uint32_t qs = qn % C::NQ, qp = (qn / C::NQ) & 1u;
             if (patient && !((si > 0 || mbar_test(bar(B_QF + qs), qp)) && mbar_test(bar(B_KF + kslot), kphase)))
               return true;
             if (si == 0 && !wait(B_QF + qs, qp)) return false;
