@@ -392,9 +392,9 @@ constexpr int kSmemLimit = 232448 - 1024;  // (the plan's static part aside)
 // Rows of a tile: four or eight where a sequence has no more to give (a
 // decoding step of up to as many heads a key head), else 16, or 8 of wide values
 // (128 registers of outputs a lane).  Tiles of 4, 8, 16 rows, f32: one
-// sequence of 100,000 keys, 4 heads a key head 282, 345, 485 us; 16 sequences of
-// 1,000 to 4,000 keys, 8 heads 106, 77, 99 us; chunks of 60 tokens on 2,000
-// keys 359, 230, 175 us.
+// sequence of 100,000 keys, 4 heads a key head 152, 193, 278 us; 16 sequences of
+// 1,000 to 4,000 keys, 8 heads 73, 50, 63 us; chunks of 60 tokens on 2,000 keys
+// 191, 133, 107 us.
 int rows_of(const PagedProblem& pr) {
   const int64_t rows = pr.T * (pr.H / pr.Hkv);  // of a key head, all sequences
   return rows <= 4 * pr.B ? 4 : rows <= 8 * pr.B || pr.DV > 128 ? 8 : 16;
