@@ -34,7 +34,7 @@
 // 64 sequences of 64 to 4,095 keys 98 us, 5.7 TB/s; one of 131,000 keys 89 us,
 // 6.0 TB/s.  Chunks: the tensor core; two of 2,048 tokens behind 14,336 keys
 // 625 to 690 us as the power cap allows, 1.5 to 1.65 PFLOP/s (the pipe is 78%
-// active; a plain library product of bf16 sustains 1.75).  At width 64 the
+// active; a plain library product of bf16 sustains 1.69).  At width 64 the
 // exponentials: the 16,384 of a 128 x 128 tile take 1,024 cycles, its products
 // about 630; chunks of 2,048 tokens behind 6,000 keys 216 us, 1.1 PFLOP/s.
 // Short calls: the chain of start, plan, page number, copy, product, softmax,
