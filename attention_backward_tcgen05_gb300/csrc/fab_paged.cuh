@@ -34,6 +34,8 @@ struct PagedPlan {
   int heads;           // Hkv * gblocks
   int nt, tiles;       // tokens of a tile, tiles of a unit (1 or 2)
   int kt;              // keys of a key tile
+  int snap;            // a unit of two tiles is not cut within so many key tiles of its ends
+  int whole;           // 1: every unit counts the same and none is cut (then nothing is left to join)
 };
 
 struct PagedSeq {
@@ -86,6 +88,7 @@ struct PagedShared {
 
 // Length on the line of unit i.
 FAB_DEV int paged_length(const PagedPlan& p, const PagedSeq& q, int i) {
+  if (p.whole) return 1;
   const int width = paged_width(p, q, i);
   return paged_step(width) * paged_key_tiles(p, q, i) + paged_lead(width);
 }
@@ -228,10 +231,14 @@ struct PagedWalk {
   int width, ntiles;   // of the present unit
   int j0, j1;          // its key tiles that lie in the piece
   int units;           // of a head of the sequence
+  int snap;
+  bool uncut;
 
   FAB_DEV void load(const PagedPlan& p) {
     width = paged_width(p, q, at.i);
     ntiles = paged_key_tiles(p, q, at.i);
+    uncut = p.whole != 0;
+    snap = p.snap;
   }
   FAB_DEV void begin(const PagedPlan& p, const PagedPlace& start) {
     at = start;
@@ -239,12 +246,20 @@ struct PagedWalk {
     units = paged_units(p, q);
     load(p);
   }
-  // Key tiles of the present unit before `pos` on the line.
+  // Key tiles of the present unit before `pos` on the line.  A border near an end of
+  // a unit of two row tiles moves there: two parts written and joined cost more
+  // than a few key tiles (width 128, two key tiles: a prompt of 4 x 2,048 tokens 132
+  // -> 127 us, chunks of 500 to 900 tokens 35.7 -> 30.8; width 64, one: mixed chunks 55.1 ->
+  // 54.4, with two 55.4).
   FAB_DEV int tiles_before(int64_t pos) const {
+    if (uncut) return pos > at.u0 ? ntiles : 0;
     const int64_t d = pos - at.u0 - paged_lead(width);
     if (d <= 0) return 0;
     if (d >= (int64_t)paged_step(width) * ntiles) return ntiles;
-    return width == 2 ? ((int)d + 3) / 4 : ((int)d + 2) / 3;
+    if (width == 1) return ((int)d + 2) / 3;
+    const int t = ((int)d + 3) / 4;
+    if (2 * t < ntiles) return t <= snap ? 0 : t;
+    return ntiles - t <= snap ? ntiles : t;
   }
   // The part of the piece [p0, p1) that lies in the present unit.
   FAB_DEV bool piece(int64_t p0, int64_t p1) {
@@ -255,7 +270,7 @@ struct PagedWalk {
   }
   // The next unit (its j0, j1 are not set); false at the end of the line.
   FAB_DEV bool next(const PagedPlan& p) {
-    at.u0 += (int64_t)paged_step(width) * ntiles + paged_lead(width);
+    at.u0 += uncut ? 1 : (int64_t)paged_step(width) * ntiles + paged_lead(width);
     if (++at.i == units) {
       at.i = 0;
       if (++at.head == p.heads) {
@@ -416,11 +431,30 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sm
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
+// Sets plan.whole and returns the grid.  Short calls are not cut: a CTA then walks
+// `few` key tiles more, but nothing is left to join and a launch is saved.
+// Decoding: units of up to `few` key tiles, two to a CTA at most; chunks, whose
+// parts are of whole 128-row tiles: up to 16 key tiles, one unit to a CTA.  Cut and whole,
+// bf16, width 128: one sequence of 500 keys 12.6 and 11.5 us, of 1,000 15.6 and
+// 14.8, of 2,000 18.2 and 22.4; 36 sequences of up to 500 (288 units) 25.8 and 20.8,
+// 64 of up to 1,000 (512 units) 40.7 and 48.5; chunks of 50 to 400 tokens behind
+// up to 500 keys 25.0 and 16.6, behind up to 2,000 29.7 and 26.4.  f32: one sequence of
+// 200 keys 13.2 and 14.6, of 500 19.2 and 21.6.
+inline int paged_grid(PagedPlan* plan, int sms, int few) {
+  const int64_t units = (plan->T / (plan->nt * plan->tiles) + plan->B) * plan->heads;  // at most
+  const int64_t tiles = (plan->max_keys + plan->kt - 1) / plan->kt;                    // of a unit, at most
+  const int most = sms < kPagedMaxGrid ? sms : kPagedMaxGrid;
+  const bool chunks = plan->tiles == 2 && plan->T > plan->B * plan->nt;
+  plan->whole = chunks ? tiles <= 16 && units <= most : tiles <= few && units <= 2 * most;
+  const int64_t pieces = plan->whole ? units : 2 * units * (tiles < most ? tiles : most);  // that are worth a CTA
+  return (int)(pieces < most ? pieces : most);
+}
+
 // Enqueues the combine kernel behind an attention kernel of `grid` CTAs.
 template <typename T>
 cudaError_t launch_combine(const PagedPlan& plan, const PagedParts& parts, int grid, int DV, int H, T* o, float* lse,
                            cudaStream_t s) {
-  if (grid < 2) return cudaSuccess;  // nothing is cut
+  if (grid < 2 || plan.whole) return cudaSuccess;  // nothing is cut
   const int rows = plan.tiles * plan.nt * plan.gw;
   const int per = kCombineThreads / (parts.dp <= 64 ? 16 : 32);  // rows of a block at once
   const dim3 g((unsigned)(grid - 1), (unsigned)((rows + per - 1) / per));

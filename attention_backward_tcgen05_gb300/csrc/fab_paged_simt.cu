@@ -44,6 +44,7 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kKeys = 8;    // keys of a tile that a warp owns
 constexpr int kStages = 4;  // of a warp's ring, at most
+constexpr int kFewTiles = 4;  // key tiles of a unit that one CTA walks (paged_grid)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -443,9 +444,8 @@ cudaError_t launch_r(const PagedProblem& pr, int sms, cudaStream_t s) {
   p.stages = (kSmemLimit - fixed) / stage;
   p.stages = p.stages > kStages ? kStages : p.stages < 1 ? 1 : p.stages;
   const int smem = fixed + (p.stages * stage > end ? p.stages * stage : end);
-  const int64_t units = (pr.T / p.plan.nt + pr.B) * p.plan.heads, tiles = (p.plan.max_keys + 63) / 64;
-  int grid = sms < kPagedMaxGrid ? sms : kPagedMaxGrid;
-  if (units < grid && tiles < grid && units * tiles < grid) grid = (int)(units * tiles);
+  p.plan.snap = 0;
+  const int grid = paged_grid(&p.plan, sms, kFewTiles);
   cudaError_t err = cudaFuncSetAttribute(paged_simt_kernel<T, R, CPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
   err = launch_early(paged_simt_kernel<T, R, CPL>, dim3((unsigned)grid), kThreads, (size_t)smem, s, p);

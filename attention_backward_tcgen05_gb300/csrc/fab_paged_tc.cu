@@ -64,6 +64,7 @@ constexpr float kRescaleThreshold = 8.f;  // log2 units
 constexpr int kThreads = 384;
 
 constexpr int kUnits = 4;  // units described ahead
+constexpr int kFewTiles = 8;  // key tiles of a unit that one CTA walks (paged_grid)
 
 // A unit's part of a CTA's piece of the line, for every warp.
 struct UnitPart {
@@ -842,11 +843,8 @@ cudaError_t launch_d(const PagedProblem& pr, int sms, cudaStream_t s) {
     const cuuint32_t box[4] = {64, (cuuint32_t)p.box, 1, 1};
     if (!make_map(v ? &mv : &mk, F16, 4, v ? pr.v : pr.k, dims, str, box)) return cudaErrorInvalidValue;
   }
-  // no more CTAs than there can be pieces of one key tile
-  const int64_t units = (pr.T / (2 * p.plan.nt) + pr.B) * p.plan.heads;
-  const int64_t tiles = (p.plan.max_keys + 127) / 128 * 2;
-  int grid = sms < kPagedMaxGrid ? sms : kPagedMaxGrid;
-  if (units < grid && tiles < grid && units * tiles < grid) grid = (int)(units * tiles);
+  p.plan.snap = DP / 64;
+  const int grid = paged_grid(&p.plan, sms, kFewTiles);
   cudaError_t err =
       cudaFuncSetAttribute(paged_tc_kernel<DP, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (err != cudaSuccess) return err;

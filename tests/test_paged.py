@@ -234,6 +234,20 @@ def test_attention(gpu, name, causal):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("name", ATTENTION)
+def test_attention_with_a_wide_table(gpu, name, causal):
+    # room for 5000 keys a sequence: the work of short calls is then cut over the
+    # SMs too, and joined
+    new, held, *rest = ATTENTION[name]
+    x = Batch(new, held, *rest, seed=1 + sum(map(ord, name)))
+    x.table = torch.nn.functional.pad(x.table, (0, 5000 // x.page), value=-7)
+    scale = rest[2] ** -0.5
+    o, lse = binding.paged_attention(*x.cuda(), causal, scale)
+    x.check(o, lse, causal, scale)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("scale", [0.0, -0.1, 1.5])
 def test_attention_scales(gpu, scale):
     # zero, negative and large scales; the last makes scores of some tens
@@ -585,5 +599,7 @@ def test_drawn_batches(gpu):
         if sum(new) == 0:
             new[0], held[0] = 1, 1 + held[0]
         x = Batch(new, held, Hkv * G, Hkv, DK, DV, page, dtype, seed=i, std=r.choice([0.3, 1.0, 2.0]))
+        if i % 2:
+            x.table = torch.nn.functional.pad(x.table, (0, 5000 // page), value=-7)
         o, lse = binding.paged_attention(*x.cuda(), causal, DK ** -0.5)
         x.check(o, lse, causal, DK ** -0.5)
