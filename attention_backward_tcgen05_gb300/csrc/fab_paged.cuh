@@ -16,6 +16,8 @@
 // workspace, at most two to a CTA, which paged_combine_kernel joins.
 #pragma once
 
+#include <type_traits>
+
 #include "fab_device.cuh"
 #include "fab_internal.h"
 
@@ -308,13 +310,20 @@ struct PagedCut {
   int gaps;       // 1: pieces shorter than a key tile's work, some CTAs up to `last` may hold no part
 };
 
-// Partial results: rows of `dp` floats, and (maximum in log2 units, sum) pairs.
+// Partial results: outputs, and (maximum in log2 units, sum) pairs by row.  The
+// outputs of a unit of two row tiles lie by 4 columns, then by row, as the writers'
+// lanes are rows (mixed chunks 53.7 -> 51.5 us); those of one, which may have few
+// rows, row by row (one sequence of 131,000 keys 89.5 us, the other way 99.5).
 struct PagedParts {
   float* out;
   float2* ml;
   PagedCut* cuts;
-  int rows, dp;  // rows of a slot, floats of a row
+  int rows, dp;  // rows of a slot, columns (a multiple of 4)
 };
+FAB_DEV float4* paged_part(const PagedParts& x, int64_t slot, int width, int row, int c4) {
+  const int n4 = x.dp / 4;
+  return reinterpret_cast<float4*>(x.out) + slot * (n4 * x.rows) + (width == 2 ? c4 * x.rows + row : row * n4 + c4);
+}
 inline size_t paged_parts_bytes(int rows, int dp) {
   return (size_t)(2 * kPagedMaxGrid) * rows * (dp + 2) * sizeof(float) + kPagedMaxGrid * sizeof(PagedCut);
 }
@@ -351,12 +360,14 @@ FAB_DEV void paged_store(__half* p, float x) { *p = __float2half_rn(x); }
 constexpr int kCombineThreads = 256;
 
 // Joins the cut unit whose first part CTA blockIdx.x holds, if there is one:
-// out = sum 2^(m_i - M) out_i / sum 2^(m_i - M) l_i over its parts.  LPR lanes
-// share a row, four columns at a time; blockIdx.y of gridDim.y shares the rows.
-// Launched while the attention kernel still runs; waits for it first.
+// out = sum 2^(m_i - M) out_i / sum 2^(m_i - M) l_i over its parts.  Of a unit of two
+// row tiles (16-bit types, DV a multiple of 8) a thread takes 8 columns of a row and its neighbours the next rows,
+// as the parts lie; of one, LPR lanes share a row, four columns at a time.
+// blockIdx.y of gridDim.y shares the work.  Launched while the attention kernel
+// still runs; waits for it first.
 template <typename T, int LPR>
-__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedPlan p, const PagedParts parts, int DV,
-                                                                        int H, T* o, float* lse) {
+__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedPlan p, const PagedParts parts,
+                                                                        int DV, int H, T* o, float* lse) {
   constexpr int RPB = kCombineThreads / LPR;  // rows a block takes at once
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = (int)blockIdx.x;
@@ -365,6 +376,59 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
   const int sub = (int)threadIdx.x % LPR;
   const int tile_rows = p.nt * p.gw;
   const int hk = cut.head / p.gblocks, gb = cut.head - hk * p.gblocks;
+  if (sizeof(T) == 2 && cut.rows > tile_rows) {  // (f32's units have one row tile)
+    const int64_t left = (int64_t)(cut.n - cut.token0) * p.gw;
+    const int live = left < cut.rows ? (int)left : cut.rows;  // rows that belong to a token
+    const int nc8 = DV / 8, items = (live + 31) / 32 * 32 * nc8;
+    for (int x = (int)blockIdx.y * kCombineThreads + (int)threadIdx.x; x < items; x += (int)gridDim.y * kCombineThreads) {
+      const int rblk = x / (32 * nc8), c8 = x / 32 - rblk * nc8, at = rblk * 32 + x % 32;
+      if (at >= live) continue;
+      const int tile = at >= tile_rows ? 1 : 0, r = at - tile * tile_rows, i = r / p.gw;
+      const int token = cut.token0 + tile * p.nt + i, g = gb * p.gw + r - i * p.gw;
+      if (token >= cut.n || g >= p.G) continue;
+      const int row = tile * (parts.rows / 2) + r;
+      float m = -INFINITY, l = 0.f, acc[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+      constexpr int U = 4;  // parts whose loads are in flight
+      for (int k0 = c; k0 <= cut.last; k0 += U) {
+        float2 ml[U];
+        float4 v[U][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int k = k0 + u;
+          ml[u] = make_float2(-INFINITY, 0.f);
+          v[u][0] = v[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k <= cut.last && (k == c || !cut.gaps || parts.cuts[k].head_part)) {
+            const int64_t slot = k == c ? 2 * k + 1 : 2 * k;
+            ml[u] = parts.ml[slot * parts.rows + row];
+            v[u][0] = *paged_part(parts, slot, 2, row, c8 * 2);
+            v[u][1] = *paged_part(parts, slot, 2, row, c8 * 2 + 1);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (ml[u].y == 0.f) continue;  // nothing to add, whatever the row holds
+          const float top = fmaxf(m, ml[u].x);
+          const float a = m == -INFINITY ? 0.f : exp2f(m - top), b = exp2f(ml[u].x - top);
+          const float add[8] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w,
+                                v[u][1].x, v[u][1].y, v[u][1].z, v[u][1].w};
+          l = l * a + ml[u].y * b;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] = acc[e] * a + add[e] * b;
+          m = top;
+        }
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int64_t t = cut.s0 + token, h = (int64_t)hk * p.G + g;
+      constexpr bool f16 = std::is_same<T, __half>::value;
+      *reinterpret_cast<uint4*>(o + (t * H + h) * DV + c8 * 8) =
+          make_uint4(pack2<f16>(acc[0] * inv, acc[1] * inv), pack2<f16>(acc[2] * inv, acc[3] * inv),
+                     pack2<f16>(acc[4] * inv, acc[5] * inv), pack2<f16>(acc[6] * inv, acc[7] * inv));
+      if (lse != nullptr && c8 == 0) lse[h * p.T + t] = l == 0.f ? INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
+    return;
+  }
   for (int x = (int)blockIdx.y * RPB + (int)threadIdx.x / LPR; x < cut.rows; x += (int)gridDim.y * RPB) {
     const int tile = x >= tile_rows ? 1 : 0, r = x - tile * tile_rows, i = r / p.gw;
     const int token = cut.token0 + tile * p.nt + i, g = gb * p.gw + r - i * p.gw;
@@ -446,6 +510,7 @@ inline int paged_grid(PagedPlan* plan, int sms, int few) {
   const int most = sms < kPagedMaxGrid ? sms : kPagedMaxGrid;
   const bool chunks = plan->tiles == 2 && plan->T > plan->B * plan->nt;
   plan->whole = chunks ? tiles <= 16 && units <= most : tiles <= few && units <= 2 * most;
+  if (units >= most) return most;
   const int64_t pieces = plan->whole ? units : 2 * units * (tiles < most ? tiles : most);  // that are worth a CTA
   return (int)(pieces < most ? pieces : most);
 }
@@ -455,7 +520,8 @@ template <typename T>
 cudaError_t launch_combine(const PagedPlan& plan, const PagedParts& parts, int grid, int DV, int H, T* o, float* lse,
                            cudaStream_t s) {
   if (grid < 2 || plan.whole) return cudaSuccess;  // nothing is cut
-  const int rows = plan.tiles * plan.nt * plan.gw;
+  // (as many blocks as a unit of one row tile has use for, which one of two has too)
+  const int rows = plan.nt * plan.gw;
   const int per = kCombineThreads / (parts.dp <= 64 ? 16 : 32);  // rows of a block at once
   const dim3 g((unsigned)(grid - 1), (unsigned)((rows + per - 1) / per));
   if (parts.dp <= 64)

@@ -378,9 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
         if (col < p.DV) paged_store(static_cast<T*>(p.o) + (t * p.H + h) * p.DV + col, sum == 0.f ? 0.f : val / sum);
         if (col == 0 && p.lse != nullptr) p.lse[h * plan.T + t] = sum == 0.f ? INFINITY : (ref + log2f(sum)) * kLn2;
       } else {
-        const int64_t at = (int64_t)w.slot((int)blockIdx.x) * p.parts.rows + r;
-        p.parts.out[at * dp + col] = val;
-        if (col == 0) p.parts.ml[at] = make_float2(ref, sum);
+        const int64_t slot = w.slot((int)blockIdx.x);
+        reinterpret_cast<float*>(paged_part(p.parts, slot, 1, r, col / 4))[col % 4] = val;
+        if (col == 0) p.parts.ml[slot * p.parts.rows + r] = make_float2(ref, sum);
       }
     }
     if (threadIdx.x == 0) paged_note_part(plan, w, border, (int)blockIdx.x, &cut);

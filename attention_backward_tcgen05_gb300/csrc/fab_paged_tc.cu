@@ -721,8 +721,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float inv = lt == 0.f ? 0.f : whole ? 1.f / lt : 1.f;
           const float a0 = l == 0.f ? 0.f : f0 * inv, a1 = f1 * inv;
           T* o = static_cast<T*>(p.o) + (tok * p.H + head) * p.DV;
-          const int64_t prow = (int64_t)u.slot * 256 + (wide ? s * 128 : 0) + r;
-          float* part = p.parts.out + prow * DP;
+          const int prow = (wide ? s * 128 : 0) + r;
+          float4* part = paged_part(p.parts, u.slot, u.width, prow, 0);
+          const int next4 = wide ? 256 : 1;  // from 4 columns to the next
 #pragma unroll 1
           for (int c0 = 0; c0 < DP; c0 += 32) {
             uint32_t x[32];
@@ -754,12 +755,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<uint4*>(part + c0 + e) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                part[(c0 + e) / 4 * next4] = make_float4(__uint_as_float(x[e]), __uint_as_float(x[e + 1]),
+                                                         __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
             }
           }
           if (row_ok) {
             if (!whole)
-              p.parts.ml[prow] = make_float2(mt, lt);
+              p.parts.ml[(int64_t)u.slot * 256 + prow] = make_float2(mt, lt);
             else if (p.lse != nullptr)
               p.lse[head * plan.T + tok] = lt == 0.f ? INFINITY : (mt + log2f(lt)) * kLn2;
           }
