@@ -365,9 +365,12 @@ def test_operands_that_do_not_match_are_refused(gpu):
 
 
 @pytest.mark.gpu
-def test_graphs_side_by_side(gpu):
+@pytest.mark.parametrize("room", [0, 5000], ids=["as_is", "wide_table"])  # whole units, work cut over the SMs
+def test_graphs_side_by_side(gpu, room):
     # two captured steps, each with the workspace that its capture allocated, replayed on two streams at once
     x = [Batch([1, 9], [900, 350], 8, 2, 128, 128, 16, "bf16", seed=s) for s in (20, 21)]
+    for b in x:
+        b.table = torch.nn.functional.pad(b.table, (0, room // b.page), value=-7)
     dev = [b.cuda() for b in x]
     want = [binding.paged_attention(*d, True, 0.1) for d in dev]
     torch.cuda.synchronize()
@@ -511,7 +514,8 @@ def test_served_as_trained(gpu):
 
 
 @pytest.mark.gpu
-def test_captured_step_follows_lengths(gpu):
+@pytest.mark.parametrize("room", [0, 5000], ids=["as_is", "wide_table"])  # whole units, work cut over the SMs
+def test_captured_step_follows_lengths(gpu, room):
     # a captured decoding step replayed with longer sequences and other pages
     H, Hkv, D, page, B = 8, 2, 128, 16, 3
     g = torch.Generator().manual_seed(13)
@@ -522,7 +526,8 @@ def test_captured_step_follows_lengths(gpu):
     row = torch.randn((B, (H + 2 * Hkv) * D), generator=g).to(torch.bfloat16).cuda()
     starts = torch.arange(B + 1, dtype=torch.int32, device="cuda")
     lens = torch.tensor([1, 1, 1], dtype=torch.int32, device="cuda")
-    table = torch.randperm(60, generator=g).to(torch.int32).view(B, 20).cuda()
+    table = torch.randperm(60, generator=g).to(torch.int32).view(B, 20)
+    table = torch.nn.functional.pad(table, (0, room // page), value=-7).cuda()
 
     def step():
         q, k, v = row.split([H * D, Hkv * D, Hkv * D], -1)
@@ -547,8 +552,11 @@ def test_captured_step_follows_lengths(gpu):
 
 
 @pytest.mark.gpu
-def test_two_streams_with_workspaces_of_their_own(gpu):
+@pytest.mark.parametrize("room", [0, 5000], ids=["as_is", "wide_table"])  # whole units, work cut over the SMs
+def test_two_streams_with_workspaces_of_their_own(gpu, room):
     x = [Batch([1, 9], [900, 350], 8, 2, 128, 128, 16, "bf16", seed=s) for s in (20, 21)]
+    for b in x:
+        b.table = torch.nn.functional.pad(b.table, (0, room // b.page), value=-7)
     dev = [b.cuda() for b in x]
     want = [binding.paged_attention(*d, True, 0.1) for d in dev]
     torch.cuda.synchronize()
