@@ -553,6 +553,37 @@ def test_captured_step_follows_lengths(gpu, room):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("room", [0, 5000], ids=["as_is", "wide_table"])  # whole units, work cut over the SMs
+def test_captured_behind_a_fork_and_a_copy(gpu, room):
+    # the call's operands come from another branch of the graph and from a copy
+    # right before it; what follows reads its result at once
+    x = Batch([1, 9, 70], [900, 350, 200], 8, 2, 128, 128, 16, "bf16", seed=22)
+    x.table = torch.nn.functional.pad(x.table, (0, room // x.page), value=-7)
+    q, k, v, starts, lens, table = x.cuda()
+    want, wl = binding.paged_attention(q, k, v, starts, lens, table, True, 0.1)
+    qs, ks = torch.zeros_like(q), torch.zeros_like(k)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            ks.copy_(k)
+        qs.add_(q)
+        main.wait_stream(side)
+        qs.copy_(q)
+        o, lse = binding.paged_attention(qs, ks, v, starts, lens, table, True, 0.1)
+        twice = o + o
+        qs.zero_()
+        ks.zero_()
+    for _ in range(10):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(lse, wl) and torch.equal(twice, want + want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("room", [0, 5000], ids=["as_is", "wide_table"])  # whole units, work cut over the SMs
 def test_two_streams_with_workspaces_of_their_own(gpu, room):
     x = [Batch([1, 9], [900, 350], 8, 2, 128, 128, 16, "bf16", seed=s) for s in (20, 21)]
     for b in x:
