@@ -564,6 +564,7 @@ def _paged_plan(layouts):
     code, dev = _code(dt), _one_device(layouts)
     dims = _paged_dims(H, T, dt, k_cache, v_cache, starts, lens, table)
     _whole(q, "q", dt, (T, H, dims.DK))
+    _current(dev)  # (the workspace's size goes by the current device)
     return dims, ctypes.byref(dims), code, dev, fab_paged_attention_workspace_bytes(dims, code)
 
 
@@ -577,7 +578,7 @@ def _paged_call(plan, q, k_cache, v_cache, starts, lens, table, causal, scale, w
 
 
 def fab_paged_attention(q, k_cache, v_cache, starts, lens, table, causal, scale, workspace, o, lse, stream=None):
-    """lse may be None."""
+    """lse may be None, and workspace where its size is 0."""
     plan = _paged_plan(_layouts(q, k_cache, v_cache, starts, lens, table))
     T, H = q.shape[:2]
     _outputs(plan[3], (o, "o", q.dtype, (T, H, plan[0].DV)), (lse, "lse", torch.float32, (H, T)))
@@ -672,7 +673,7 @@ def paged_attention(q, k_cache, v_cache, starts, lens, table, causal=True, scale
         dev, wsb = q.device, plan[4]
         o = torch.empty((T, H, v_cache.shape[3]), dtype=q.dtype, device=dev)
         lse = torch.empty((H, T), dtype=torch.float32, device=dev)
-        ws = torch.empty((wsb,), dtype=torch.uint8, device=dev)
+        ws = torch.empty((wsb,), dtype=torch.uint8, device=dev) if wsb > 0 else None
         _paged_call(plan, q, k_cache, v_cache, starts, lens, table, causal, scale, ws, wsb, o, lse, stream)
     return o, lse
 

@@ -267,7 +267,8 @@ FAB_API int fab_paged_attention(const void* q, const void* k_cache, const void* 
   if (!widths_ok(dims->DK, dims->DV)) return FAB_ERR_UNSUPPORTED;
   if (dims->T == 0) return FAB_OK;
   PagedProblem p = paged_problem(dims, dtype);
-  if (!aligned(workspace, 16) || workspace_bytes < paged_workspace_bytes(p)) return FAB_ERR_WORKSPACE;
+  const size_t need = paged_workspace_bytes(p);
+  if (need > 0 && (!aligned(workspace, 16) || workspace_bytes < need)) return FAB_ERR_WORKSPACE;
   p.scale = scale;
   p.causal = causal ? 1 : 0;
   p.q = q;

@@ -515,6 +515,22 @@ inline int paged_grid(PagedPlan* plan, int sms, int few) {
   return (int)(pieces < most ? pieces : most);
 }
 
+// SMs of the current device, 0 without one.
+inline int paged_sms() {
+  int dev = 0, sms = 0;
+  const bool ok = cudaGetDevice(&dev) == cudaSuccess &&
+                  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+  return ok ? sms : 0;
+}
+
+// Workspace of a call on the current device: none where no unit is cut.
+inline size_t paged_workspace(PagedPlan plan, int few, int rows, int dp) {
+  const int sms = paged_sms();
+  plan.whole = 0;
+  if (sms > 0) paged_grid(&plan, sms, few);
+  return plan.whole ? 0 : paged_parts_bytes(rows, dp);
+}
+
 // Enqueues the combine kernel behind an attention kernel of `grid` CTAs.
 template <typename T>
 cudaError_t launch_combine(const PagedPlan& plan, const PagedParts& parts, int grid, int DV, int H, T* o, float* lse,

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
   const PagedPlace start = sh.at;
   PagedCut cut{0, 0, 0, 0, 0, 0, 0, 0};
   if (p0 >= p1) {
-    if (threadIdx.x == 0) p.parts.cuts[blockIdx.x] = cut;
+    if (threadIdx.x == 0 && !plan.whole) p.parts.cuts[blockIdx.x] = cut;
     return;
   }
 
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
     }
     if (threadIdx.x == 0) paged_note_part(plan, w, border, (int)blockIdx.x, &cut);
   }
-  if (threadIdx.x == 0) p.parts.cuts[blockIdx.x] = cut;
+  if (threadIdx.x == 0 && !plan.whole) p.parts.cuts[blockIdx.x] = cut;
 }
 
 constexpr int kSmemLimit = 232448 - 1024;  // (the plan's static part aside)
@@ -402,23 +402,30 @@ int rows_of(const PagedProblem& pr) {
 }
 int dp_of(const PagedProblem& pr) { return (int)(pr.DV + 3) / 4 * 4; }
 
+PagedPlan plan_of(const PagedProblem& pr) {
+  const int R = rows_of(pr);
+  PagedPlan p{};
+  p.starts = pr.starts;
+  p.lens = pr.lens;
+  p.B = pr.B;
+  p.T = pr.T;
+  const int64_t most = pr.max_pages * pr.page;
+  p.max_keys = most < 2147483647ll - 256 ? most : 2147483647ll - 256;  // (lengths are 32-bit)
+  p.causal = pr.causal;
+  p.G = (int)(pr.H / pr.Hkv);
+  p.gw = p.G < R ? p.G : R;
+  p.gblocks = (p.G + p.gw - 1) / p.gw;
+  p.heads = (int)pr.Hkv * p.gblocks;
+  p.nt = R / p.gw;
+  p.tiles = 1;
+  p.kt = 64;
+  return p;
+}
+
 template <typename T, int R, int CPL>
 cudaError_t launch_r(const PagedProblem& pr, int sms, cudaStream_t s) {
   SimtParams p;
-  p.plan.starts = pr.starts;
-  p.plan.lens = pr.lens;
-  p.plan.B = pr.B;
-  p.plan.T = pr.T;
-  const int64_t most = pr.max_pages * pr.page;
-  p.plan.max_keys = most < 2147483647ll - 256 ? most : 2147483647ll - 256;  // (lengths are 32-bit)
-  p.plan.causal = pr.causal;
-  p.plan.G = (int)(pr.H / pr.Hkv);
-  p.plan.gw = p.plan.G < R ? p.plan.G : R;
-  p.plan.gblocks = (p.plan.G + p.plan.gw - 1) / p.plan.gw;
-  p.plan.heads = (int)pr.Hkv * p.plan.gblocks;
-  p.plan.nt = R / p.plan.gw;
-  p.plan.tiles = 1;
-  p.plan.kt = 64;
+  p.plan = plan_of(pr);
   p.parts = paged_parts(pr.workspace, R, dp_of(pr));
   p.table = pr.table;
   p.max_pages = pr.max_pages;
@@ -444,7 +451,6 @@ cudaError_t launch_r(const PagedProblem& pr, int sms, cudaStream_t s) {
   p.stages = (kSmemLimit - fixed) / stage;
   p.stages = p.stages > kStages ? kStages : p.stages < 1 ? 1 : p.stages;
   const int smem = fixed + (p.stages * stage > end ? p.stages * stage : end);
-  p.plan.snap = 0;
   const int grid = paged_grid(&p.plan, sms, kFewTiles);
   cudaError_t err = cudaFuncSetAttribute(paged_simt_kernel<T, R, CPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
@@ -463,13 +469,13 @@ cudaError_t launch_t(const PagedProblem& pr, int sms, cudaStream_t s) {
 
 }  // namespace
 
-size_t paged_simt_workspace_bytes(const PagedProblem& p) { return paged_parts_bytes(16, dp_of(p)); }
+size_t paged_simt_workspace_bytes(const PagedProblem& p) {
+  return paged_workspace(plan_of(p), kFewTiles, 16, dp_of(p));
+}
 
 cudaError_t launch_paged_simt(const PagedProblem& p, cudaStream_t s) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return cudaErrorInvalidValue;
+  const int sms = paged_sms();
+  if (sms == 0) return cudaErrorInvalidValue;
   if (p.dtype == FAB_BF16) return launch_t<__nv_bfloat16>(p, sms, s);
   if (p.dtype == FAB_F16) return launch_t<__half>(p, sms, s);
   return launch_t<float>(p, sms, s);

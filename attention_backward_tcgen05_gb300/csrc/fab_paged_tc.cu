@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++slot == kUnits) slot = 0, phase ^= 1;
           more = w.next(plan) && w.seek(plan, p0, p1);
         }
-        p.parts.cuts[blockIdx.x] = cut;
+        if (!plan.whole) p.parts.cuts[blockIdx.x] = cut;
       }
       __syncwarp();
     } else if (warp != 1) {
@@ -811,6 +811,7 @@ PagedPlan plan_of(const PagedProblem& pr) {
   p.nt = 128 / p.gw;
   p.tiles = 2;
   p.kt = 128;
+  p.snap = padded_width(pr) / 64;
   return p;
 }
 
@@ -845,7 +846,6 @@ cudaError_t launch_d(const PagedProblem& pr, int sms, cudaStream_t s) {
     const cuuint32_t box[4] = {64, (cuuint32_t)p.box, 1, 1};
     if (!make_map(v ? &mv : &mk, F16, 4, v ? pr.v : pr.k, dims, str, box)) return cudaErrorInvalidValue;
   }
-  p.plan.snap = DP / 64;
   const int grid = paged_grid(&p.plan, sms, kFewTiles);
   cudaError_t err =
       cudaFuncSetAttribute(paged_tc_kernel<DP, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -868,13 +868,13 @@ bool paged_tc_supported(const PagedProblem& p) {
   return p.Hkv * p.page * D * 2 < lim && p.H * p.DK * 2 < lim && p.H < (1ll << 31);
 }
 
-size_t paged_tc_workspace_bytes(const PagedProblem& p) { return paged_parts_bytes(256, padded_width(p)); }
+size_t paged_tc_workspace_bytes(const PagedProblem& p) {
+  return paged_workspace(plan_of(p), kFewTiles, 256, padded_width(p));
+}
 
 cudaError_t launch_paged_tc(const PagedProblem& p, cudaStream_t s) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return cudaErrorInvalidValue;
+  const int sms = paged_sms();
+  if (sms == 0) return cudaErrorInvalidValue;
   if (padded_width(p) == 128)
     return p.dtype == FAB_F16 ? launch_d<128, true>(p, sms, s) : launch_d<128, false>(p, sms, s);
   return p.dtype == FAB_F16 ? launch_d<64, true>(p, sms, s) : launch_d<64, false>(p, sms, s);

@@ -298,7 +298,9 @@ FAB_EXPORT int fab_paged_append(const void* q, const void* k, const void* v, con
                                 const int32_t* lens, const int32_t* table, int dtype, const fab_paged_dims* dims,
                                 void* q_out, void* k_cache, void* v_cache, fab_stream stream);
 
-/* Device workspace bytes of fab_paged_attention; 0 for bad dims. */
+/* Device workspace bytes of fab_paged_attention on the current device; 0 for bad
+ * dims, and for short calls that need none (of few sequences whose rows of the
+ * table hold few keys; workspace may then be NULL). */
 FAB_EXPORT size_t fab_paged_attention_workspace_bytes(const fab_paged_dims* dims, int dtype);
 
 /* Attention of the new tokens over their sequences' caches: token i of the n

@@ -72,10 +72,12 @@ def test_attention_refuses_arguments(bad):
 
 
 def test_workspace_and_width_refusals():
-    need = binding.fab_paged_attention_workspace_bytes(paged_dims(), binding.FAB_BF16)
-    assert need > 0 and binding.fab_paged_attention_workspace_bytes(paged_dims(), 4) == 0
-    assert call_attention(paged_dims(), wsb=need - 1) == binding.FAB_ERR_WORKSPACE
-    assert call_attention(paged_dims(), ws=A + 4) == binding.FAB_ERR_WORKSPACE
+    long = paged_dims(max_pages=3000)
+    need = binding.fab_paged_attention_workspace_bytes(long, binding.FAB_BF16)
+    assert need > 0 and binding.fab_paged_attention_workspace_bytes(long, 4) == 0
+    assert call_attention(long, wsb=need - 1) == binding.FAB_ERR_WORKSPACE
+    assert call_attention(long, ws=A + 4) == binding.FAB_ERR_WORKSPACE
+    assert call_attention(long, ws=None, wsb=0) == binding.FAB_ERR_WORKSPACE
     wide = paged_dims(DK=264, ldq=4096, ldk=4096)
     assert call_append(wide) == binding.FAB_ERR_UNSUPPORTED
     assert call_attention(wide) == binding.FAB_ERR_UNSUPPORTED
@@ -308,6 +310,23 @@ def test_nan_stays_in_its_row(gpu):
         o, lse = binding.paged_attention(*x.cuda(), True, 0.125)
         assert o[2].isnan().all()
         assert lse[:, :2].isfinite().all() and lse[:, 3].isfinite().all() and o[3].isfinite().all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_short_calls_need_no_workspace(gpu, dtype):
+    x = Batch([1, 2], [100, 60], 8, 2, 64, 64, 16, dtype, seed=31)
+    d = x.cuda()
+    assert binding.alloc_paged(d[0], d[1], d[2], d[5]).numel() == 0
+    o, lse = torch.empty_like(d[0]), torch.empty((8, 3), dtype=torch.float32, device="cuda")
+    binding.fab_paged_attention(*d, True, 0.125, None, o, lse)
+    x.check(o, lse, True, 0.125)
+    x.table = torch.nn.functional.pad(x.table, (0, 300), value=-7)
+    d = x.cuda()
+    with pytest.raises(binding.FabError):
+        binding.fab_paged_attention(*d, True, 0.125, None, o, lse)
+    binding.fab_paged_attention(*d, True, 0.125, binding.alloc_paged(d[0], d[1], d[2], d[5]), o, lse)
+    x.check(o, lse, True, 0.125)
 
 
 @pytest.mark.gpu
