@@ -547,6 +547,9 @@ __global__ void __launch_bounds__(kVecThreads, 3) rope_vec_backward_kernel(const
     };
 #pragma unroll
     for (int u = 0; u < A; ++u) fetch(j0 + u, u);
+    // A row that is not there (past the last token, past the last head) adds
+    // zeros to dw: by r = 0, as at eps = 0 its 1 / sqrt would be infinite.
+    const int live = row_ok ? j1 : j0;
     float c[8], s[8];  // (a lane past the last token turns zeros: by something finite)
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
@@ -568,7 +571,8 @@ __global__ void __launch_bounds__(kVecThreads, 3) rope_vec_backward_kernel(const
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss += xa[i] * xa[i] + xb[i] * xb[i];
-        const float r = rsqrtf(group_sum<L>(ss) * inv_d + p.eps);
+        const float mean = group_sum<L>(ss) * inv_d;
+        const float r = j < live ? rsqrtf(mean + p.eps) : 0.f;
         float dot = 0.f;
         wa.get(w);
 #pragma unroll
