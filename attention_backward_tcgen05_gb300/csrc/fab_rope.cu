@@ -385,8 +385,10 @@ __global__ void __launch_bounds__(kVecThreads, sizeof(T) == 4 ? 4 : 5) rope_vec_
   const int by = (int)blockIdx.y;
   const int kind = by < bq ? 0 : by < bq + bk ? 1 : 2;
   const int heads = kind == 0 ? (int)p.H : (int)p.Hkv;
+  // its heads are j0 .. j0 + nj - 1; j counts from j0, so that offsets from the
+  // 64-bit addresses of head j0 fit 32 bits however long a token's row is
   const int j0 = (by - (kind == 0 ? 0 : kind == 1 ? bq : bq + bk)) * hb;
-  const int j1 = j0 + hb < heads ? j0 + hb : heads;
+  const int nj = heads - j0 < hb ? heads - j0 : hb;
   const int D = (int)(kind == 2 ? p.DV : p.DK);
   const int half = kind == 2 ? 0 : (int)p.rot / 2;
   int ca, cb;
@@ -395,20 +397,20 @@ __global__ void __launch_bounds__(kVecThreads, sizeof(T) == 4 ? 4 : 5) rope_vec_
   const bool row_ok = t < p.B * p.N;
   const bool oka = row_ok && ca >= 0, okb = row_ok && cb >= 0;
   const T* x0 = static_cast<const T*>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
-                t * (kind == 0 ? p.ldq : kind == 1 ? p.ldk : p.ldv);
+                t * (kind == 0 ? p.ldq : kind == 1 ? p.ldk : p.ldv) + (int64_t)j0 * D;
   Raw8<T> na[U], nb[U];
   auto fetch = [&](int j) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       na[u].zero();
       nb[u].zero();
-      if (j + u < j1) {
+      if (j + u < nj) {
         if (oka) na[u].load(x0 + (j + u) * D + ca * 8);
         if (okb) nb[u].load(x0 + (j + u) * D + cb * 8);
       }
     }
   };
-  fetch(j0);
+  fetch(0);
   const T* w0 = static_cast<const T*>(kind == 0 ? p.wq : kind == 1 ? p.wk : nullptr);
   const bool norm = w0 != nullptr;
   Raw8<T> wa, wb;
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(kVecThreads, sizeof(T) == 4 ? 4 : 5) rope_vec_
 #pragma unroll
   for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
   if (row_ok && half > 0) load_turn<IL>(p.cos, p.sin, at.pos, half, ca, cb, ta, tb, c, s);
-  // where this token's rows go: head j at y0 + j * ystep
+  // where this token's rows go: head j0 + j at y0 + j * ystep
   T* y0 = nullptr;
   int64_t ystep = 0;
   if (p.starts == nullptr) {
@@ -438,13 +440,14 @@ __global__ void __launch_bounds__(kVecThreads, sizeof(T) == 4 ? 4 : 5) rope_vec_
     y0 = static_cast<T*>(kind == 1 ? p.k_out : p.v_out) + (at.page * p.Hkv * p.page + at.slot) * D;
     ystep = p.page * D;
   }
+  y0 += j0 * ystep;
   const bool store = row_ok && at.live && (p.starts == nullptr || kind == 0 || at.page >= 0);
   const float inv_d = 1.f / (float)D;
-  for (int j = j0; j < j1; j += U) {
+  for (int j = 0; j < nj; j += U) {
     Raw8<T> ra[U], rb[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) ra[u] = na[u], rb[u] = nb[u];
-    if (j + U < j1) fetch(j + U);
+    if (j + U < nj) fetch(j + U);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (kind != 2) {
@@ -465,12 +468,12 @@ __global__ void __launch_bounds__(kVecThreads, sizeof(T) == 4 ? 4 : 5) rope_vec_
           for (int i = 0; i < 8; ++i) b[i] *= r * w[i];
         }
         turn<IL, false>(a, b, c, s, ta, tb);
-        if (store && j + u < j1) {
+        if (store && j + u < nj) {
           T* y = y0 + (j + u) * ystep;
           if (oka) store8(y + ca * 8, a);
           if (okb) store8(y + cb * 8, b);
         }
-      } else if (store && j + u < j1) {  // values move as they are
+      } else if (store && j + u < nj) {  // values move as they are
         T* y = y0 + (j + u) * ystep;
 #pragma unroll
         for (int i = 0; i < (int)(sizeof(T) / 2); ++i) {
@@ -522,14 +525,15 @@ __global__ void __launch_bounds__(kVecThreads, 3) rope_vec_backward_kernel(const
   const int64_t hblocks = (heads + hb - 1) / hb, items = tblocks * hblocks, dstep = p.N * D;
   for (int64_t it = blk - first_blk; it < items; it += blocks) {
     const int64_t tbk = it / hblocks;
-    const int j0 = (int)(it - tbk * hblocks) * hb, j1 = j0 + hb < heads ? j0 + hb : heads;
+    // heads j0 .. j0 + nj - 1; j counts from j0, as in rope_vec_kernel
+    const int j0 = (int)(it - tbk * hblocks) * hb, nj = heads - j0 < hb ? heads - j0 : hb;
     const int64_t t = tbk * (kVecThreads / L) + threadIdx.x / L;
     const bool row_ok = t < tokens;
     const bool oka = row_ok && ca >= 0, okb = row_ok && cb >= 0;
     const int64_t b = t / p.N, n = t - b * p.N;
-    const float* dy = dy0 + (b * heads * p.N + n) * D;
-    const T* x = x0 + t * ldx;
-    T* g = g0 + t * ldg;
+    const float* dy = dy0 + (b * heads * p.N + n) * D + j0 * dstep;
+    const T* x = x0 + t * ldx + (int64_t)j0 * D;
+    T* g = g0 + t * ldg + (int64_t)j0 * D;
     Raw8<float> nga[A], ngb[A];
     Raw8<T> nxa[A], nxb[A];
     auto fetch = [&](int j, int u) {
@@ -537,7 +541,7 @@ __global__ void __launch_bounds__(kVecThreads, 3) rope_vec_backward_kernel(const
       ngb[u].zero();
       nxa[u].zero();
       nxb[u].zero();
-      if (j >= j1) return;
+      if (j >= nj) return;
       if (oka) nga[u].load(dy + j * dstep + ca * 8);
       if (okb) ngb[u].load(dy + j * dstep + cb * 8);
       if (norm) {
@@ -546,15 +550,15 @@ __global__ void __launch_bounds__(kVecThreads, 3) rope_vec_backward_kernel(const
       }
     };
 #pragma unroll
-    for (int u = 0; u < A; ++u) fetch(j0 + u, u);
+    for (int u = 0; u < A; ++u) fetch(u, u);
     // A row that is not there (past the last token, past the last head) adds
     // zeros to dw: by r = 0, as at eps = 0 its 1 / sqrt would be infinite.
-    const int live = row_ok ? j1 : j0;
+    const int live = row_ok ? nj : 0;
     float c[8], s[8];  // (a lane past the last token turns zeros: by something finite)
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
     if (row_ok && half > 0) load_turn<IL>(p.cos, p.sin, place_of(p, t).pos, half, ca, cb, ta, tb, c, s);
-    for (int jj = j0; jj < j1; jj += A)
+    for (int jj = 0; jj < nj; jj += A)
 #pragma unroll
     for (int u = 0; u < A; ++u) {
       const int j = jj + u;
@@ -597,8 +601,8 @@ __global__ void __launch_bounds__(kVecThreads, 3) rope_vec_backward_kernel(const
           gb[i] = r * (gb[i] - xb[i] * dot);
         }
       }
-      if (oka && j < j1) store8(g + j * D + ca * 8, ga);
-      if (okb && j < j1) store8(g + j * D + cb * 8, gb);
+      if (oka && j < nj) store8(g + j * D + ca * 8, ga);
+      if (okb && j < nj) store8(g + j * D + cb * 8, gb);
     }
   }
   if (!norm) return;

@@ -1,6 +1,6 @@
 """Query/key norms with rotation and their gradient where the kernels step and
-loop: rows that are not there beside rows that are.  Against the formulas in 64
-bits, computed on the GPU.
+loop: rows that are not there beside rows that are, heads by the million.
+Against the formulas in 64 bits, computed on the GPU.
 
 Tolerances as in test_norm_rope.py; a weight's gradient adds `depth` values one
 after another at most, each addition within half a step of what it adds up.
@@ -65,6 +65,29 @@ def check_gradient(x, d, il, dt, eps, depth):
     assert torch.equal(gv, d["dv"].transpose(1, 2).to(dt))
 
 
+def launch(dtype, tokens, H, Hkv, D, rot, il):
+    """What the 16-byte kernels' launches make of a call: the forward's heads a
+    CTA and rows a step, the gradient's (items, blocks, heads an item) of q and of k."""
+    R = rot // 8
+    slots = (D // 8 + 1) // 2 if il else R // 2 + (D // 8 - R + 1) // 2
+    L = 4 if slots <= 4 else 8 if slots <= 8 else 16
+    tb = -(-tokens // (128 // L))
+    hb = 32
+    while hb > 1 and tb * (-(-H // hb) + 2 * -(-Hkv // hb)) < 1216:
+        hb //= 2
+    gb = 32
+    while gb > 1 and tb * (-(-H // gb) + 2 * -(-Hkv // gb)) < 456:
+        gb //= 2
+    items = [tb * -(-h // gb) for h in (H, Hkv)]
+    blocks = [min(n, -(-1216 * h // (H + 2 * Hkv))) for n, h in zip(items, (H, Hkv))]
+    return hb, 1 if dtype == "f32" else 2, [(n, b, gb) for n, b in zip(items, blocks)]
+
+
+def depths(items):
+    """A lane's rows, lanes, warps, rows of partial sums, lanes."""
+    return [-(-n // b) * gb + 3 + 4 + -(-b // 32) + 5 for n, b, gb in items]
+
+
 # ------------------------------------------------------------------ no epsilon
 
 # dtype, B, N, H, Hkv, D, rot, interleaved, gap: single heads beside an empty
@@ -92,3 +115,36 @@ def test_without_epsilon(gpu, case):
     check_forward(x, il, dt, 0.0)
     tokens = case[1] * case[2]
     check_gradient(x, d, il, dt, 0.0, [tokens * h / 8 + 64 for h in case[3:5]])
+
+
+# ------------------------------------------------------------------ a token's row past 2^31 elements
+
+
+@pytest.mark.gpu
+def test_a_row_past_31_bits(gpu):
+    # one token of 2^25 + 2 heads of width 64: offsets inside its row pass 2^31
+    H, Hkv, D = (1 << 25) + 2, 2, 64
+    assert H * D > 1 << 31
+    x, d, il, dt = inputs("bf16", 1, 1, H, Hkv, D, 64)
+    q, k, v = binding.qk_norm_rope(x["q"], x["k"], x["v"])
+    assert torch.equal(q[0, :, 0], x["q"][0, 0]) and torch.equal(k[0, :, 0], x["k"][0, 0])
+    del q
+    gq, gk, _, _, _ = binding.qk_norm_rope_backward(d["dq"], d["dk"], None, x["q"], x["k"])
+    assert torch.equal(gq[0, 0], d["dq"][0, :, 0].to(dt)) and torch.equal(gk[0, 0], d["dk"][0, :, 0].to(dt))
+    del gq
+    q, k, v = binding.qk_norm_rope(**x)
+    gq, _, _, gwq, _ = binding.qk_norm_rope_backward(d["dq"], d["dk"], None, x["q"], x["k"], x["wq"], x["wk"], x["cos"],
+                                                     x["sin"], x["pos"])
+    cos, sin = at(x)
+    dw, terms = torch.zeros(D, dtype=torch.float64, device="cuda"), torch.zeros(D, dtype=torch.float64, device="cuda")
+    step = 1 << 21
+    for h0 in range(0, H, step):
+        part = slice(h0, h0 + step)
+        rows = x["q"][:, :, part]
+        want, bound = ref_forward(rows, x["wq"], cos, sin, il, 1e-6)
+        within(q[:, part], want.movedim(2, 1), bound.movedim(2, 1), dt, f"q from head {h0}")
+        want, bound, w, t = ref_backward(d["dq"][:, part].movedim(1, 2), rows, x["wq"], cos, sin, il, 1e-6)
+        within(gq[:, :, part], want, bound, dt, f"gq from head {h0}")
+        dw, terms = dw + w, terms + t
+    _, _, items = launch("bf16", 1, H, Hkv, D, 64, il)
+    assert ((gwq.double() - dw).abs() <= (64 + depths(items)[0]) * U32 * terms).all()
