@@ -452,7 +452,9 @@ cudaError_t launch_r(const PagedProblem& pr, int sms, cudaStream_t s) {
   p.stages = p.stages > kStages ? kStages : p.stages < 1 ? 1 : p.stages;
   const int smem = fixed + (p.stages * stage > end ? p.stages * stage : end);
   const int grid = paged_grid(&p.plan, sms, kFewTiles);
-  cudaError_t err = cudaFuncSetAttribute(paged_simt_kernel<T, R, CPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (the limit is the kernel's, for all threads of the process: every call sets the same, whatever it needs itself)
+  cudaError_t err =
+      cudaFuncSetAttribute(paged_simt_kernel<T, R, CPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (err != cudaSuccess) return err;
   err = launch_early(paged_simt_kernel<T, R, CPL>, dim3((unsigned)grid), kThreads, (size_t)smem, s, p);
   if (err != cudaSuccess) return err;

@@ -10,6 +10,8 @@ of f32, and the result is rounded once.
 import ctypes
 import math
 import random
+import sys
+import threading
 
 import pytest
 import torch
@@ -661,3 +663,39 @@ def test_drawn_batches(gpu):
             x.table = torch.nn.functional.pad(x.table, (0, 5000 // page), value=-7)
         o, lse = binding.paged_attention(*x.cuda(), causal, DK ** -0.5)
         x.check(o, lse, causal, DK ** -0.5)
+
+
+@pytest.mark.gpu
+def test_threads_of_several_widths(gpu):
+    # widths whose calls on the CUDA cores share a kernel and need different amounts of shared memory,
+    # from threads of their own: in the C entry points, where they run at the same time
+    x = [Batch([1], [20], 1, 1, D, D, 16, "f32", seed=D) for D in (32, 64, 96, 128) for _ in range(2)]
+    dev, refused, out = [b.cuda() for b in x], [0] * len(x), []
+    streams = [torch.cuda.Stream() for _ in x]
+    for b in x:
+        out.append((torch.empty(b.q.shape, device="cuda"), torch.empty((1, 1), device="cuda")))
+    torch.cuda.synchronize()
+
+    def calls(i):
+        b, (q, k, v, starts, lens, table), (o, lse) = x[i], dev[i], out[i]
+        dims = binding.fab_paged_dims(1, 1, 1, 1, b.DK, b.DV, b.page, b.pages, table.shape[1])
+        args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), starts.data_ptr(), lens.data_ptr(), table.data_ptr(), 1, 0.1,
+                binding.FAB_F32, ctypes.byref(dims), None, 0, o.data_ptr(), lse.data_ptr(), streams[i].cuda_stream)
+        call = binding.lib().fab_paged_attention
+        for _ in range(3000):
+            refused[i] += call(*args) != binding.FAB_OK
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(len(x))]
+    every = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(every)
+    torch.cuda.synchronize()
+    assert refused == [0] * len(x)
+    for b, (o, lse) in zip(x, out):
+        b.check(o, lse, True, 0.1)
