@@ -390,6 +390,8 @@ def _bytes(workspace, dev):
         return 0
     if workspace.get_device() != dev:
         raise ValueError(f"the workspace is on {workspace.device}, the other tensors on cuda:{dev}")
+    if not workspace.is_contiguous():  # (its elements' bytes are not then those from its address on)
+        raise ValueError(f"the workspace must be contiguous, got strides {workspace.stride()}")
     return workspace.numel() * workspace.element_size()
 
 

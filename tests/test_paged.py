@@ -105,6 +105,15 @@ def test_binding_refuses_what_does_not_fit():
             binding.paged_append(args[0], q[:, :2], q[:, :2], None, None, None, None, *args[3:], args[1], args[2])
 
 
+@pytest.mark.parametrize("workspace", [torch.empty(64, dtype=torch.uint8)[::2], torch.empty(1).expand(1 << 20),
+                                       torch.empty(8, 8)[:, :4]], ids=["strided", "expanded", "columns"])
+def test_binding_refuses_a_workspace_with_gaps(workspace):
+    # as many elements as are asked for, but not the bytes behind its address (device -1: the CPU's)
+    with pytest.raises(ValueError):
+        binding._bytes(workspace, -1)
+    assert binding._bytes(workspace.contiguous(), -1) == workspace.numel() * workspace.element_size()
+
+
 # ------------------------------------------------------------------ a paged batch
 
 
@@ -699,3 +708,24 @@ def test_threads_of_several_widths(gpu):
     assert refused == [0] * len(x)
     for b, (o, lse) in zip(x, out):
         b.check(o, lse, True, 0.1)
+
+
+@pytest.mark.gpu
+def test_workspaces_with_gaps_are_refused(gpu):
+    x = Batch([1, 2], [100, 60], 8, 2, 64, 64, 16, "bf16", seed=31)
+    x.table = torch.nn.functional.pad(x.table, (0, 300), value=-7)
+    d = x.cuda()
+    o, lse = torch.empty_like(d[0]), torch.empty((8, 3), dtype=torch.float32, device="cuda")
+    ws = binding.alloc_paged(d[0], d[1], d[2], d[5])
+    gaps = torch.empty(2 * ws.numel(), dtype=torch.uint8, device="cuda")[::2]
+    for bad in (gaps, torch.empty(1, dtype=torch.uint8, device="cuda").expand(ws.numel()), ws.cpu()):
+        with pytest.raises(ValueError):
+            binding.fab_paged_attention(*d, True, 0.125, bad, o, lse)
+        g = torch.zeros(1, 4, 2, 64, device="cuda")
+        w = torch.ones(64, device="cuda")
+        with pytest.raises(ValueError):
+            rows = g.transpose(1, 2).contiguous()
+            binding.fab_qk_norm_rope_backward(rows, rows, None, g, g, w, w, None, None, None, 1e-6, False, bad, g, g,
+                                              None, w, w)
+    binding.fab_paged_attention(*d, True, 0.125, ws, o, lse)
+    x.check(o, lse, True, 0.125)
