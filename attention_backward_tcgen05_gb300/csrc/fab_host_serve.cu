@@ -13,6 +13,9 @@ namespace fab {
 namespace {
 
 constexpr int64_t kMaxInt32 = 2147483647;
+// Tokens of a paged call: the attention kernels number those of its last unit in 32
+// bits up to the end of the unit's tiles, 255 past the last that is there.
+constexpr int64_t kMaxTokens = kMaxInt32 - 256;
 
 int64_t elem_size(int dtype) { return dtype == FAB_F32 ? 4 : 2; }
 
@@ -46,7 +49,7 @@ int check_rope_dims(const fab_rope_dims* d) {
 int check_paged_dims(const fab_paged_dims* d) {
   if (!d || d->B <= 0 || d->T < 0 || !heads_ok(d->H, d->Hkv, d->DK, d->DV)) return FAB_ERR_INVALID;
   if (d->page <= 0 || d->pages <= 0 || d->max_pages <= 0) return FAB_ERR_INVALID;
-  if (d->B >= kMaxInt32 || d->T > kMaxInt32 || d->page > kMaxInt32 || d->pages > kMaxInt32 || d->max_pages > kMaxInt32)
+  if (d->B >= kMaxInt32 || d->T > kMaxTokens || d->page > kMaxInt32 || d->pages > kMaxInt32 || d->max_pages > kMaxInt32)
     return FAB_ERR_INVALID;
   if (!fits(d->pages, d->page, d->Hkv, d->DK) || !fits(d->pages, d->page, d->Hkv, d->DV)) return FAB_ERR_INVALID;
   if (!fits(d->B, d->max_pages, 1, 1)) return FAB_ERR_INVALID;

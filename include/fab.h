@@ -276,7 +276,7 @@ FAB_EXPORT int fab_qk_norm_rope_backward(const float* dq, const float* dk, const
  * arguments; fab_last_device_error reports FAB_ERR_INVALID, and what was
  * computed for those tokens is meaningless. */
 typedef struct {
-  int64_t B, T;          /* sequences, rows of new tokens (T may be 0) */
+  int64_t B, T;          /* sequences, rows of new tokens (T may be 0; < 2^31 - 256) */
   int64_t H, Hkv;        /* query heads (< 2^31), key/value heads (H % Hkv == 0) */
   int64_t DK, DV;        /* query/key width, value width (<= 256) */
   int64_t page;          /* rows of a page */

@@ -85,6 +85,17 @@ def test_workspace_and_width_refusals():
     assert call_attention(wide) == binding.FAB_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("T", [(1 << 31) - 256, (1 << 31) - 1])
+def test_tokens_that_the_kernels_cannot_number_are_refused(T):
+    # a unit's tiles end up to 255 tokens behind its last one, and 32 bits have to hold their numbers
+    dims = paged_dims(T=T, H=1, Hkv=1, DK=8, DV=8, rot=8)
+    assert call_append(dims) == binding.FAB_ERR_INVALID
+    assert call_attention(dims) == binding.FAB_ERR_INVALID
+    assert binding.fab_paged_attention_workspace_bytes(dims, binding.FAB_BF16) == 0
+    dims.T = (1 << 31) - 257
+    assert binding.fab_paged_attention_workspace_bytes(dims, binding.FAB_BF16) > 0
+
+
 def test_no_tokens_is_nothing_to_do():
     assert call_append(paged_dims(T=0), q=None, k=None, v=None, qo=None) == binding.FAB_OK
     assert call_attention(paged_dims(T=0), q=None, o=None, lse=None) == binding.FAB_OK
