@@ -262,8 +262,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const CUtensorMap* map = keys ? &tmK : &tmV;
       int slot = 0, phase = 1, qslot = 0, qphase = 1, us = 0, up = 0;
       bool ok = true;
+      // (the warp goes on or gives up as one: its lanes meet at __syncwarp below)
+      auto wait = [&](int i, int parity) {
+        return ok = __all_sync(0xffffffffu, mbar_wait_asleep(bar(i), parity, abort_flag, err));
+      };
       for (;;) {
-        if (!(ok = mbar_wait_asleep(bar(B_DF + us), up, abort_flag, err))) break;
+        if (!wait(B_DF + us, up)) break;
         const UnitPart& u = units[us];
         if (!u.more) break;
         const int j0 = u.j0, j1 = u.j1, len = u.len, hk = u.hk;
@@ -283,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (keys) {
           if (lane == 0 && plan.lens[u.b] > plan.max_keys) atomicOr(err, kErrIndex);
           for (int s = 0; s < u.width; ++s) {
-            if (!(ok = mbar_wait_asleep(bar(B_QE + qslot), qphase, abort_flag, err))) break;
+            if (!wait(B_QE + qslot, qphase)) break;
             if (lane == 0) {
               mbar_arrive_expect_tx(bar(B_QF + qslot), (uint32_t)(64 * 2 * plan.gw * plan.nt * C::ATOMS));
               for (int a = 0; a < C::ATOMS; ++a)
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
         }
         for (int j = j0; j < j1; ++j) {
-          if (!(ok = mbar_wait_asleep(bar(empty + slot), phase, abort_flag, err))) break;
+          if (!wait(empty + slot, phase)) break;
           const int held = len - j * 128;  // keys of the tile and beyond
           const int boxes = held <= 0 ? 0 : held >= 128 ? 128 / p.box : (held + p.box - 1) / p.box;
           fence_proxy_async_smem();
@@ -316,7 +320,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++us == kUnits) us = 0, up ^= 1;
       }
       // after a failed wait, let the copies in flight land before shared memory goes
-      ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) {
         for (int s = 0; s < slots; ++s) mbar_drain(bar(full + s), s < slot ? phase ^ 1 : phase);
         if (keys)
