@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return sbase + C::OFF_BAR + 8u * (uint32_t)i; };
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC + 4);
+  int* copied = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);  // where the load warps' rings ended: keys and Q, values
   UnitPart* units = reinterpret_cast<UnitPart*>(smem + C::OFF_UNIT);
   float2* ml_s = reinterpret_cast<float2*>(smem + C::OFF_ML);
   PagedShared* sh = reinterpret_cast<PagedShared*>(smem + C::OFF_ML);
@@ -319,12 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(B_DE + us));
         if (++us == kUnits) us = 0, up ^= 1;
       }
-      // after a failed wait, let the copies in flight land before shared memory goes
-      if (!ok && lane == 0) {
-        for (int s = 0; s < slots; ++s) mbar_drain(bar(full + s), s < slot ? phase ^ 1 : phase);
-        if (keys)
-          for (int s = 0; s < C::NQ; ++s) mbar_drain(bar(B_QF + s), s < qslot ? qphase ^ 1 : qphase);
-      }
+      if (lane == 0) copied[keys ? 0 : 1] = slot | phase << 4 | qslot << 8 | qphase << 12;  // (see the end)
     } else {
       // ------------------------------------------------------------ products
       // One elected lane does it all: the compiler then knows that a single lane
@@ -781,6 +777,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 3) {
     tc_fence_after();
     tmem_dealloc(tm, 512);
+  }
+  // Where a wait ran out, copies may still be in flight that no warp has waited
+  // for: they land before shared memory goes.
+  if (*abort_flag != 0u && threadIdx.x == 0) {
+    auto drain = [&](int first, int slots, int slot, int phase) {
+      for (int s = 0; s < slots; ++s) mbar_drain(bar(first + s), s < slot ? phase ^ 1 : phase);
+    };
+    drain(B_KF, C::NK, copied[0] & 15, copied[0] >> 4 & 1);
+    drain(B_QF, C::NQ, copied[0] >> 8 & 15, copied[0] >> 12 & 1);
+    drain(B_VF, C::NV, copied[1] & 15, copied[1] >> 4 & 1);
   }
 }
 
