@@ -150,7 +150,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
   extern __shared__ uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // swizzled tiles need a 1024-byte-aligned base
-    if (threadIdx.x == 0) atomicOr(&g_err_paged_tc, kErrSmemAlign);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // (the call before may still be reading its notes)
+    if (threadIdx.x == 0) {
+      atomicOr(&g_err_paged_tc, kErrSmemAlign);
+      if (!p.plan.whole) p.parts.cuts[blockIdx.x] = PagedCut{0, 0, 0, 0, 0, 0, 0, 0};  // nothing to join
+    }
     return;
   }
   const uint32_t sbase = smem_u32(smem);
