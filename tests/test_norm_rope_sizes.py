@@ -1,6 +1,7 @@
 """Query/key norms with rotation and their gradient where the kernels step and
-loop: rows that are not there beside rows that are, heads by the million.
-Against the formulas in 64 bits, computed on the GPU.
+loop: rows that are not there beside rows that are, heads a CTA walks over,
+items behind one another, heads by the million.  Against the formulas in 64
+bits, computed on the GPU.
 
 Tolerances as in test_norm_rope.py; a weight's gradient adds `depth` values one
 after another at most, each addition within half a step of what it adds up.
@@ -148,3 +149,89 @@ def test_a_row_past_31_bits(gpu):
         dw, terms = dw + w, terms + t
     _, _, items = launch("bf16", 1, H, Hkv, D, 64, il)
     assert ((gwq.double() - dw).abs() <= (64 + depths(items)[0]) * U32 * terms).all()
+
+
+# ------------------------------------------------------------------ sizes at which the kernels loop
+
+# a training step's 4 x 2,048 tokens of 32 and 8 heads, and an odd neighbour
+LOOPS = [(dtype, B, N, H, Hkv, 128, 128, il, 0) for dtype in ("bf16", "f16", "f32")
+         for B, N, H, Hkv, il in ((4, 2048, 32, 8, False), (1, 8191, 33, 11, True))]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", LOOPS, ids=str)
+def test_steps_and_items(gpu, case):
+    dtype, B, N, H, Hkv, D, rot, il, _ = case
+    heads, step, items = launch(dtype, B * N, H, Hkv, D, rot, il)
+    assert heads > 2 * step and any(n > b for n, b, _ in items)
+    x, d, il, dt = inputs(*case)
+    check_forward(x, il, dt, 1e-6)
+    check_gradient(x, d, il, dt, 1e-6, depths(items))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_behind_one_another(gpu, dtype):
+    # rows at odd places, more of them than 768 (q) and 256 (k) blocks of eight warps
+    N, H, Hkv = 1024, 9, 3
+    assert N * H > 768 * 8 and N * Hkv > 256 * 8
+    x, d, il, dt = inputs(dtype, 1, N, H, Hkv, 64, 64, gap=3)
+    check_forward(x, il, dt, 1e-6)
+    # a warp's rows, warps, rows of partial sums, lanes
+    check_gradient(x, d, il, dt, 1e-6, [-(-N * h // (8 * b)) + 8 + -(-b // 32) + 5 for h, b in ((H, 768), (Hkv, 256))])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [("bf16", 1, 40, 4, 2, 256, 256, True, 0), ("f32", 3, 300, 6, 2, 96, 64, False, 0)], ids=str)
+def test_wide_pairs_and_f32(gpu, case):
+    x, d, il, dt = inputs(*case)
+    check_forward(x, il, dt, 1e-6)
+    check_gradient(x, d, il, dt, 1e-6, [case[1] * case[2] * h / 8 for h in case[3:5]])
+
+
+@pytest.mark.gpu
+def test_more_heads_than_a_grid_has_rows(gpu):
+    # the heads of a CTA are doubled until a grid's second dimension holds the blocks
+    H, Hkv, D = 2200000, 2, 8
+    assert -(-H // 32) > 65535
+    x, d, il, dt = inputs("bf16", 1, 3, H, Hkv, D, 0)
+    x.update(cos=None, sin=None, wq=None, wk=None, pos=None)
+    q, k, v = binding.qk_norm_rope(**x)
+    assert all(torch.equal(a, x[n].transpose(1, 2)) for n, a in (("q", q), ("k", k), ("v", v)))
+    gq, gk, gv, _, _ = binding.qk_norm_rope_backward(**d, q=None, k=None, dtype=dt)
+    assert all(torch.equal(a, d["d" + n].transpose(1, 2).to(dt)) for n, a in (("q", gq), ("k", gk), ("v", gv)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_append_at_size(gpu, dtype):
+    # prompts whose heads a CTA walks over: the same bits as from the tokens by themselves
+    H, Hkv, D, page, new, past = 32, 8, 128, 64, [2048, 1, 3001, 0, 2500, 900], [0, 70, 3, 10, 129, 64]
+    N = sum(new)
+    heads, step, _ = launch(dtype, N, H, Hkv, D, D, False)
+    assert heads > 2 * step
+    x, _, il, dt = inputs(dtype, 1, N, H, Hkv, D, D)
+    pos = torch.cat([torch.arange(p, p + n) for n, p in zip(new, past)])
+    x["pos"] = pos[None].int().cuda()
+    want = binding.qk_norm_rope(**x)
+    count = [-(-(n + p) // page) for n, p in zip(new, past)]
+    table = torch.zeros((len(new), max(count)), dtype=torch.int32)
+    order = torch.randperm(sum(count), generator=torch.Generator().manual_seed(4)).int()
+    for b, c in enumerate(order.split(count)):
+        table[b, : len(c)] = c
+    kc = torch.full((sum(count), Hkv, page, D), float("nan"), dtype=dt, device="cuda")
+    vc = kc.clone()
+    starts = torch.tensor([0] + new).cumsum(0).int().cuda()
+    lens = torch.tensor([n + p for n, p in zip(new, past)]).int().cuda()
+    q = binding.paged_append(x["q"][0], x["k"][0], x["v"][0], x["wq"], x["wk"], x["cos"], x["sin"], starts, lens,
+                             table.cuda(), kc, vc)
+    assert torch.equal(q, want[0][0].transpose(0, 1))
+    seq = torch.repeat_interleave(torch.arange(len(new)), torch.tensor(new))
+    where = table[seq, pos // page].long()
+    slot = pos % page
+    assert torch.equal(kc[where.cuda(), :, slot.cuda()], want[1][0].transpose(0, 1))
+    assert torch.equal(vc[where.cuda(), :, slot.cuda()], want[2][0].transpose(0, 1))
+    untouched = torch.ones(kc.shape[0], page, dtype=torch.bool)
+    untouched[where, slot] = False
+    for cache in (kc, vc):
+        assert cache.transpose(1, 2)[untouched.cuda()].isnan().all()
