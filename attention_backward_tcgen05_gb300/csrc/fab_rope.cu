@@ -431,16 +431,15 @@ __global__ void __launch_bounds__(kVecThreads, sizeof(T) == 4 ? 4 : 5) rope_vec_
   int64_t ystep = 0;
   if (p.starts == nullptr) {
     const int64_t b = t / p.N, n = t - b * p.N;
-    y0 = static_cast<T*>(kind == 0 ? p.q_out : kind == 1 ? p.k_out : p.v_out) + (b * heads * p.N + n) * D;
+    y0 = static_cast<T*>(kind == 0 ? p.q_out : kind == 1 ? p.k_out : p.v_out) + ((b * heads + j0) * p.N + n) * D;
     ystep = p.N * D;
   } else if (kind == 0) {
-    y0 = static_cast<T*>(p.q_out) + t * p.H * D;
+    y0 = static_cast<T*>(p.q_out) + (t * p.H + j0) * D;
     ystep = D;
   } else {
-    y0 = static_cast<T*>(kind == 1 ? p.k_out : p.v_out) + (at.page * p.Hkv * p.page + at.slot) * D;
+    y0 = static_cast<T*>(kind == 1 ? p.k_out : p.v_out) + ((at.page * p.Hkv + j0) * p.page + at.slot) * D;
     ystep = p.page * D;
   }
-  y0 += j0 * ystep;
   const bool store = row_ok && at.live && (p.starts == nullptr || kind == 0 || at.page >= 0);
   const float inv_d = 1.f / (float)D;
   for (int j = 0; j < nj; j += U) {
