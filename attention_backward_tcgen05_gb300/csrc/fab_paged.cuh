@@ -11,7 +11,11 @@
 // key tile of a unit of two tiles takes: measured at 1.2 us for that, 0.9 us
 // for one of a unit of one tile (whose streams wait for memory or for one
 // another rather than for the tensor core) and 3 us for the start and the end,
-// by a fit over the CTAs of a batch of mixed chunks at width 64.  A unit cut by
+// by a fit over the CTAs of a batch of mixed chunks at width 64.  The same figures
+// serve width 128 and the CUDA cores, where they were not fitted but tried:
+// starts and ends counted half, as they are, double: mixed chunks at width 128 98, 83 and 84
+// us, 200 short decoding sequences 83, 77 and 79, 16 in f32 68, 62 and 64, mixed f32
+// chunks 463, 437 and 400 (the one that another figure would serve).  A unit cut by
 // a border leaves unnormalised partial results (output, maximum, sum) in the
 // workspace, at most two to a CTA, which paged_combine_kernel joins.
 #pragma once
@@ -502,8 +506,10 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t sm
 // bf16, width 128: one sequence of 500 keys 12.6 and 11.5 us, of 1,000 15.6 and
 // 14.8, of 2,000 18.2 and 22.4; 36 sequences of up to 500 (288 units) 25.8 and 20.8,
 // 64 of up to 1,000 (512 units) 40.7 and 48.5; chunks of 50 to 400 tokens behind
-// up to 500 keys 25.0 and 16.6, behind up to 2,000 29.7 and 26.4.  f32: one sequence of
-// 200 keys 13.2 and 14.6, of 500 19.2 and 21.6.
+// up to 500 keys 25.0 and 16.6, behind up to 2,000 29.7 and 26.4.  f32, 4 tiles at most:
+// one sequence at width 64 of 128 keys 9.8 and 8.4, of 256 12.4 and 11.6, of 500 18.5 and 18.5;
+// at width 128 with 32 heads of 200 keys 13.8 and 14.0, of 256 13.8 and 13.2, of 500 16.4 and
+// 20.6; 4 sequences of 500 14.6 and 21.1; 16 of 200 18.2 and 14.4, of 500 24.8 and 21.2.
 inline int paged_grid(PagedPlan* plan, int sms, int few) {
   const int64_t units = (plan->T / (plan->nt * plan->tiles) + plan->B) * plan->heads;  // at most
   const int64_t tiles = (plan->max_keys + plan->kt - 1) / plan->kt;                    // of a unit, at most

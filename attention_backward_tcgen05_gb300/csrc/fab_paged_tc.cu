@@ -27,13 +27,16 @@
 // (log2): weights then stay below 2^8 and the output is rescaled rarely; the
 // sum and the output share the stale maximum, so the result is exact.  f16
 // weights are kept 2^7 larger, which moves their smallest step 2^7 down.
-// Weights are rounded to the input type for the second product; their sum is
-// not.
+// Weights are rounded to the input type for the second product, which takes
+// both operands in 16 bits; their sum is not.  Against 64 bits the result is then
+// off by 1.3 to 1.4 times what one rounding of an f32 result gives (64 decoding
+// sequences, bf16: 0.0022 of its size for 0.0017).  A third product, of what
+// the rounding left, would cost chunks half as many products again.
 //
 // Bounds and measured times (bf16, 32 heads on 8, width 128).  Decoding: memory;
 // 64 sequences of 64 to 4,095 keys 98 us, 5.7 TB/s; one of 131,000 keys 89 us,
 // 6.0 TB/s.  Chunks: the tensor core; two of 2,048 tokens behind 14,336 keys
-// 625 to 690 us as the power cap allows, 1.5 to 1.65 PFLOP/s (the pipe is 78%
+// 645 to 690 us as the power cap allows, 1.5 to 1.6 PFLOP/s (the pipe is 78%
 // active; a plain library product of bf16 sustains 1.69).  At width 64 the
 // exponentials: the 16,384 of a 128 x 128 tile take 1,024 cycles, its products
 // about 630; chunks of 2,048 tokens behind 6,000 keys 216 us, 1.1 PFLOP/s.

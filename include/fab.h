@@ -299,8 +299,10 @@ FAB_EXPORT int fab_paged_append(const void* q, const void* k, const void* v, con
                                 void* q_out, void* k_cache, void* v_cache, fab_stream stream);
 
 /* Device workspace bytes of fab_paged_attention on the current device; 0 for bad
- * dims, and for short calls that need none (of few sequences whose rows of the
- * table hold few keys; workspace may then be NULL). */
+ * dims (which fab_paged_attention itself refuses), and for short calls that need
+ * none (of few sequences whose rows of the table hold few keys; workspace may then
+ * be NULL).  Ask for each call's own sizes: one of fewer tokens can need a
+ * workspace where one of more needs none. */
 FAB_EXPORT size_t fab_paged_attention_workspace_bytes(const fab_paged_dims* dims, int dtype);
 
 /* Attention of the new tokens over their sequences' caches: token i of the n
@@ -311,6 +313,11 @@ FAB_EXPORT size_t fab_paged_attention_workspace_bytes(const fab_paged_dims* dims
  * lse = +inf.  Cache rows from lens[b] on are never read into a result, whatever
  * they hold; rows before it have to be finite: a later token's value takes part in
  * an earlier one's sum with weight 0, which a NaN or an infinity survives.
+ * bf16 and f16 calls with DK and DV multiples of 8 up to 128 and pages of a
+ * multiple of 8 rows run on the tensor cores, which take the softmax weights of
+ * the second product in `dtype`, rounded one by one, as in fab_forward_lse (their
+ * sum is not rounded); every other call keeps them in f32.  Scores, maxima, sums and
+ * unfinished outputs are f32 in both.  o and lse must not overlap the inputs.
  * workspace: device, fab_paged_attention_workspace_bytes() bytes, contents
  * overwritten; calls that may overlap on the GPU need one each. */
 FAB_EXPORT int fab_paged_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* starts,
