@@ -16,6 +16,9 @@ Tensor shapes (torch, C order; the reverse of ggml's ne order):
     paged: projection rows q (T, H, DK)  k (T, Hkv, DK)  v (T, Hkv, DV)
         k_cache (pages, Hkv, page, DK)  v_cache (pages, Hkv, page, DV)
         starts (B + 1,)  lens (B,)  table (B, max_pages), int32;  o (T, H, DV)  lse (H, T) float32
+    drafted trees: parents (T,)  seen (T, words)  last (B,), int32
+    calls for all layers at once: k_cache (layers, pages, Hkv, page, DK), any distance between layers
+        (or 4-D: one layer);  refs (pages,)  source, kept (B,)  spare (1,), int32
 """
 from __future__ import annotations
 
@@ -39,7 +42,9 @@ EXPORTS = ("fab_version", "fab_status_string", "fab_packed_offsets", "fab_packed
            "fab_backward_main", "fab_backward_query_pass", "fab_backward_key_pass", "fab_backward_noalloc",
            "fab_last_device_error", "fab_qk_norm_rope", "fab_qk_norm_rope_backward",
            "fab_qk_norm_rope_backward_workspace_bytes", "fab_paged_append", "fab_paged_attention",
-           "fab_paged_attention_workspace_bytes")
+           "fab_paged_attention_workspace_bytes", "fab_draft_tree", "fab_paged_append_tree",
+           "fab_paged_attention_tree", "fab_paged_accept", "fab_paged_reserve", "fab_paged_reserve_workspace_bytes")
+DRAFT_MAX_WORDS = 512  # FAB_DRAFT_MAX_WORDS
 NOALLOC_MAX_ROWS = 1048576  # FAB_NOALLOC_MAX_ROWS
 
 
@@ -58,6 +63,11 @@ class fab_rope_dims(ctypes.Structure):
 class fab_paged_dims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "H", "Hkv", "DK", "DV", "page", "pages", "max_pages", "rot",
                                               "P", "ldq", "ldk", "ldv")]
+
+
+class fab_cache_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "words", "Hkv", "DK", "DV", "page", "pages", "max_pages",
+                                              "layers", "ldk", "ldv")]
 
 
 class FabError(RuntimeError):
@@ -82,6 +92,7 @@ def lib():
                 vp, sz, i32, f32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_float
                 dp = ctypes.POINTER(fab_dims)
                 rp, pp = ctypes.POINTER(fab_rope_dims), ctypes.POINTER(fab_paged_dims)
+                cp, i64 = ctypes.POINTER(fab_cache_dims), ctypes.c_int64
                 szp = ctypes.POINTER(ctypes.c_size_t)
                 sig = {
                     "fab_version": ([], i32),
@@ -104,6 +115,12 @@ def lib():
                     "fab_paged_append": ([vp] * 7 + [f32, i32, vp, vp, vp, i32, pp, vp, vp, vp, vp], i32),
                     "fab_paged_attention_workspace_bytes": ([pp, i32], sz),
                     "fab_paged_attention": ([vp] * 6 + [i32, f32, i32, pp, vp, sz, vp, vp, vp], i32),
+                    "fab_draft_tree": ([vp, vp, i64, i64, i64, vp, vp], i32),
+                    "fab_paged_append_tree": ([vp] * 7 + [f32, i32] + [vp] * 4 + [i64, i32, pp, vp, vp, vp, vp], i32),
+                    "fab_paged_attention_tree": ([vp] * 7 + [i64, f32, i32, pp, vp, sz, vp, vp, vp], i32),
+                    "fab_paged_accept": ([vp] * 5 + [i32, cp, vp, vp, vp, vp], i32),
+                    "fab_paged_reserve_workspace_bytes": ([cp], sz),
+                    "fab_paged_reserve": ([vp] * 5 + [i32, cp, vp, vp, vp, sz, vp, vp], i32),
                 }
                 for name, (args, res) in sig.items():
                     f = getattr(L, name)
@@ -514,11 +531,21 @@ def _paged_dims(H, T, dt, k_cache, v_cache, starts, lens, table):
     return fab_paged_dims(B, T, H, Hkv, DK, DV, page, pages, max_pages)
 
 
+def _seen_words(seen, T):
+    """Words of a row of the layout of `seen` (None: 0), checked."""
+    if seen is None:
+        return 0
+    if len(seen[0]) != 2 or seen[0][1] < 1:
+        raise ValueError(f"seen must be 2-D (T,words), got {tuple(seen[0])}")
+    _whole(seen, "seen", torch.int32, (T, seen[0][1]))
+    return seen[0][1]
+
+
 @functools.lru_cache(maxsize=1024)
 def _append_plan(layouts):
-    """(dims, their reference, dtype code, device) of a fab_paged_append call on
-    q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cache."""
-    q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cache = layouts
+    """(dims, their reference, dtype code, device, words) of a fab_paged_append
+    call on q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cache, seen."""
+    q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cache, seen = layouts
     if len(q[0]) != 3 or len(k[0]) != 3 or len(v[0]) != 3:
         raise ValueError("q, k, v must be 3-D: (T,H,DK), (T,Hkv,DK), (T,Hkv,DV)")
     T, H, DK = q[0]
@@ -529,24 +556,39 @@ def _append_plan(layouts):
     dims.ldq = _ld(q, "q", dt, (T, H, dims.DK))
     dims.ldk = _ld(k, "k", dt, (T, dims.Hkv, DK))
     dims.ldv = _ld(v, "v", dt, (T, dims.Hkv, dims.DV))
-    return dims, ctypes.byref(dims), code, dev
+    return dims, ctypes.byref(dims), code, dev, _seen_words(seen, T)
 
 
-def _append_call(plan, q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, q_out, k_cache, v_cache,
+def _append_call(plan, q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, seen, q_out, k_cache, v_cache,
                  stream):
     dev = plan[3]
     _current(dev)
-    _check(lib().fab_paged_append(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(wq), _addr(wk), _addr(cos), _addr(sin), eps,
-        1 if interleaved else 0, starts.data_ptr(), lens.data_ptr(), table.data_ptr(), plan[2], plan[1],
-        q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _raw_stream(stream, dev)), "fab_paged_append")
+    if seen is None:
+        _check(lib().fab_paged_append(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(wq), _addr(wk), _addr(cos), _addr(sin), eps,
+            1 if interleaved else 0, starts.data_ptr(), lens.data_ptr(), table.data_ptr(), plan[2], plan[1],
+            q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _raw_stream(stream, dev)), "fab_paged_append")
+    else:
+        _check(lib().fab_paged_append_tree(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(wq), _addr(wk), _addr(cos), _addr(sin), eps,
+            1 if interleaved else 0, starts.data_ptr(), lens.data_ptr(), table.data_ptr(), seen.data_ptr(), plan[4],
+            plan[2], plan[1], q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _raw_stream(stream, dev)),
+            "fab_paged_append_tree")
 
 
 def fab_paged_append(q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, q_out, k_cache, v_cache,
                      stream=None):
-    plan = _append_plan(_layouts(q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cache))
+    plan = _append_plan(_layouts(q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cache, None))
     _outputs(plan[3], (q_out, "q_out", q.dtype, q.shape))
-    _append_call(plan, q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, q_out, k_cache, v_cache,
+    _append_call(plan, q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, None, q_out, k_cache, v_cache,
+                 stream)
+
+
+def fab_paged_append_tree(q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, seen, q_out, k_cache,
+                          v_cache, stream=None):
+    plan = _append_plan(_layouts(q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cache, seen))
+    _outputs(plan[3], (q_out, "q_out", q.dtype, q.shape))
+    _append_call(plan, q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, seen, q_out, k_cache, v_cache,
                  stream)
 
 
@@ -556,9 +598,9 @@ def fab_paged_attention_workspace_bytes(dims: fab_paged_dims, dtype: int) -> int
 
 @functools.lru_cache(maxsize=1024)
 def _paged_plan(layouts):
-    """(dims, their reference, dtype code, device, workspace bytes) of a
-    fab_paged_attention call on q, k_cache, v_cache, starts, lens, table."""
-    q, k_cache, v_cache, starts, lens, table = layouts
+    """(dims, their reference, dtype code, device, workspace bytes, words) of a
+    fab_paged_attention call on q, k_cache, v_cache, starts, lens, table, seen."""
+    q, k_cache, v_cache, starts, lens, table, seen = layouts
     if len(q[0]) != 3:
         raise ValueError("q must be 3-D: (T,H,DK)")
     T, H, DK = q[0]
@@ -566,26 +608,163 @@ def _paged_plan(layouts):
     code, dev = _code(dt), _one_device(layouts)
     dims = _paged_dims(H, T, dt, k_cache, v_cache, starts, lens, table)
     _whole(q, "q", dt, (T, H, dims.DK))
+    words = _seen_words(seen, T)
     _current(dev)  # (the workspace's size goes by the current device)
-    return dims, ctypes.byref(dims), code, dev, fab_paged_attention_workspace_bytes(dims, code)
+    return dims, ctypes.byref(dims), code, dev, fab_paged_attention_workspace_bytes(dims, code), words
 
 
-def _paged_call(plan, q, k_cache, v_cache, starts, lens, table, causal, scale, ws, wsb, o, lse, stream):
+def _paged_call(plan, q, k_cache, v_cache, starts, lens, table, seen, causal, scale, ws, wsb, o, lse, stream):
     dev = plan[3]
     _current(dev)
-    _check(lib().fab_paged_attention(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), starts.data_ptr(), lens.data_ptr(), table.data_ptr(),
-        1 if causal else 0, float(scale), plan[2], plan[1], _addr(ws), wsb, o.data_ptr(), _addr(lse),
-        _raw_stream(stream, dev)), "fab_paged_attention")
+    if seen is None:
+        _check(lib().fab_paged_attention(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), starts.data_ptr(), lens.data_ptr(), table.data_ptr(),
+            1 if causal else 0, float(scale), plan[2], plan[1], _addr(ws), wsb, o.data_ptr(), _addr(lse),
+            _raw_stream(stream, dev)), "fab_paged_attention")
+    else:
+        _check(lib().fab_paged_attention_tree(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), starts.data_ptr(), lens.data_ptr(), table.data_ptr(),
+            seen.data_ptr(), plan[5], float(scale), plan[2], plan[1], _addr(ws), wsb, o.data_ptr(), _addr(lse),
+            _raw_stream(stream, dev)), "fab_paged_attention_tree")
 
 
 def fab_paged_attention(q, k_cache, v_cache, starts, lens, table, causal, scale, workspace, o, lse, stream=None):
     """lse may be None, and workspace where its size is 0."""
-    plan = _paged_plan(_layouts(q, k_cache, v_cache, starts, lens, table))
+    plan = _paged_plan(_layouts(q, k_cache, v_cache, starts, lens, table, None))
     T, H = q.shape[:2]
     _outputs(plan[3], (o, "o", q.dtype, (T, H, plan[0].DV)), (lse, "lse", torch.float32, (H, T)))
-    _paged_call(plan, q, k_cache, v_cache, starts, lens, table, causal, scale, workspace, _bytes(workspace, plan[3]), o,
-                lse, stream)
+    _paged_call(plan, q, k_cache, v_cache, starts, lens, table, None, causal, scale, workspace,
+                _bytes(workspace, plan[3]), o, lse, stream)
+
+
+def fab_paged_attention_tree(q, k_cache, v_cache, starts, lens, table, seen, scale, workspace, o, lse, stream=None):
+    """lse may be None, and workspace where its size is 0."""
+    plan = _paged_plan(_layouts(q, k_cache, v_cache, starts, lens, table, seen))
+    T, H = q.shape[:2]
+    _outputs(plan[3], (o, "o", q.dtype, (T, H, plan[0].DV)), (lse, "lse", torch.float32, (H, T)))
+    _paged_call(plan, q, k_cache, v_cache, starts, lens, table, seen, True, scale, workspace,
+                _bytes(workspace, plan[3]), o, lse, stream)
+
+
+# ------------------------------------------------------------------ drafted trees, rows and pages
+
+
+@functools.lru_cache(maxsize=1024)
+def _tree_plan(layouts, words):
+    """(B, T, words, device) of a fab_draft_tree call on starts, parents."""
+    starts, parents = layouts
+    if len(starts[0]) != 1 or starts[0][0] < 2 or len(parents[0]) != 1:
+        raise ValueError("starts, parents must be 1-D: (B + 1,), (T,)")
+    if not 1 <= words <= DRAFT_MAX_WORDS:
+        raise ValueError(f"seen takes 1 to {DRAFT_MAX_WORDS} words a token, got {words}")
+    _whole(starts, "starts", torch.int32, starts[0])
+    _whole(parents, "parents", torch.int32, parents[0])
+    return starts[0][0] - 1, parents[0][0], words, _one_device(layouts)
+
+
+def _tree_call(plan, starts, parents, seen, stream):
+    dev = plan[3]
+    _current(dev)
+    _check(lib().fab_draft_tree(starts.data_ptr(), parents.data_ptr(), plan[0], plan[1], plan[2], seen.data_ptr(),
+                                _raw_stream(stream, dev)), "fab_draft_tree")
+
+
+def fab_draft_tree(starts, parents, seen, stream=None):
+    plan = _tree_plan(_layouts(starts, parents), seen.shape[1] if seen.dim() == 2 else 0)
+    _outputs(plan[3], (seen, "seen", torch.int32, (plan[1], plan[2])))
+    _tree_call(plan, starts, parents, seen, stream)
+
+
+def _layer_step(x, name, dtype, shape):
+    """Elements between the layers of a cache's layout, each of `shape`; checked."""
+    lead = len(x[0]) - 4
+    whole = (x[0][lead:], x[1][lead:], x[2], x[3])
+    _whole(whole, name, dtype, shape)
+    layers, inner = (x[0][0] if lead else 1), shape[0] * shape[1] * shape[2] * shape[3]
+    if layers < 2:
+        return inner
+    if x[1][0] < inner:
+        raise ValueError(f"{name}: its layers overlap, got strides {x[1]}")
+    return x[1][0]
+
+
+def _cache_dims(k_cache, v_cache, table):
+    """dims of a call on a cache of one layer (4-D) or more (5-D), their layouts checked."""
+    if len(k_cache[0]) not in (4, 5) or len(v_cache[0]) != len(k_cache[0]) or len(table[0]) != 2:
+        raise ValueError("k_cache, v_cache must be 4-D (pages,Hkv,page,width) or 5-D (layers,...), table 2-D (B,max_pages)")
+    dt, lead = k_cache[2], k_cache[0][:-4]
+    if v_cache[0][:-4] != lead:
+        raise ValueError(f"k_cache and v_cache have {tuple(lead)} and {tuple(v_cache[0][:-4])} layers")
+    pages, Hkv, page, DK = k_cache[0][-4:]
+    DV = v_cache[0][-1]
+    B, max_pages = table[0]
+    _whole(table, "table", torch.int32, (B, max_pages))
+    return fab_cache_dims(B, 0, 0, Hkv, DK, DV, page, pages, max_pages, lead[0] if lead else 1,
+                          _layer_step(k_cache, "k_cache", dt, (pages, Hkv, page, DK)),
+                          _layer_step(v_cache, "v_cache", dt, (pages, Hkv, page, DV)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _accept_plan(layouts):
+    """(dims, their reference, dtype code, device) of a fab_paged_accept call on
+    starts, lens, table, seen, last, k_cache, v_cache."""
+    starts, lens, table, seen, last, k_cache, v_cache = layouts
+    code, dev = _code(k_cache[2]), _one_device(layouts)
+    dims = _cache_dims(k_cache, v_cache, table)
+    for x, name, n in ((starts, "starts", dims.B + 1), (lens, "lens", dims.B), (last, "last", dims.B)):
+        _whole(x, name, torch.int32, (n,))
+    if len(seen[0]) != 2:
+        raise ValueError(f"seen must be 2-D (T,words), got {tuple(seen[0])}")
+    dims.T = seen[0][0]
+    dims.words = _seen_words(seen, dims.T)
+    return dims, ctypes.byref(dims), code, dev
+
+
+def _accept_call(plan, starts, lens, table, seen, last, k_cache, v_cache, lens_out, stream):
+    dev = plan[3]
+    _current(dev)
+    _check(lib().fab_paged_accept(starts.data_ptr(), lens.data_ptr(), table.data_ptr(), seen.data_ptr(),
+                                  last.data_ptr(), plan[2], plan[1], k_cache.data_ptr(), v_cache.data_ptr(),
+                                  lens_out.data_ptr(), _raw_stream(stream, dev)), "fab_paged_accept")
+
+
+def fab_paged_accept(starts, lens, table, seen, last, k_cache, v_cache, lens_out, stream=None):
+    plan = _accept_plan(_layouts(starts, lens, table, seen, last, k_cache, v_cache))
+    _outputs(plan[3], (lens_out, "lens_out", torch.int32, (plan[0].B,)))
+    _accept_call(plan, starts, lens, table, seen, last, k_cache, v_cache, lens_out, stream)
+
+
+def fab_paged_reserve_workspace_bytes(dims: fab_cache_dims) -> int:
+    return lib().fab_paged_reserve_workspace_bytes(ctypes.byref(dims))
+
+
+@functools.lru_cache(maxsize=1024)
+def _reserve_plan(layouts):
+    """(dims, their reference, dtype code, device, workspace bytes) of a
+    fab_paged_reserve call on table, refs, source, kept, lens, k_cache, v_cache."""
+    table, refs, source, kept, lens, k_cache, v_cache = layouts
+    code, dev = _code(k_cache[2]), _one_device(layouts)
+    dims = _cache_dims(k_cache, v_cache, table)
+    _whole(refs, "refs", torch.int32, (dims.pages,))
+    for x, name in ((source, "source"), (kept, "kept"), (lens, "lens")):
+        _whole(x, name, torch.int32, (dims.B,))
+    return dims, ctypes.byref(dims), code, dev, fab_paged_reserve_workspace_bytes(dims)
+
+
+def _reserve_call(plan, table, refs, source, kept, lens, k_cache, v_cache, ws, wsb, spare, stream):
+    dev = plan[3]
+    _current(dev)
+    _check(lib().fab_paged_reserve(table.data_ptr(), refs.data_ptr(), _addr(source), kept.data_ptr(), lens.data_ptr(),
+                                   plan[2], plan[1], k_cache.data_ptr(), v_cache.data_ptr(), _addr(ws), wsb,
+                                   spare.data_ptr(), _raw_stream(stream, dev)), "fab_paged_reserve")
+
+
+def fab_paged_reserve(table, refs, source, kept, lens, k_cache, v_cache, workspace, spare, stream=None):
+    """source may be None: every row continues itself."""
+    plan = _reserve_plan(_layouts(table, refs, source, kept, lens, k_cache, v_cache))
+    _outputs(plan[3], (spare, "spare", torch.int32, (1,)))
+    _reserve_call(plan, table, refs, source, kept, lens, k_cache, v_cache, workspace, _bytes(workspace, plan[3]), spare,
+                  stream)
 
 
 def _on(stream):
@@ -644,15 +823,16 @@ def qk_norm_rope_backward(dq, dk, dv, q, k, wq=None, wk=None, cos=None, sin=None
 
 
 def paged_append(q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cache, eps=1e-6, interleaved=False,
-                 stream=None):
+                 stream=None, seen=None):
     """Puts the new tokens' keys and values into the caches and returns their
     queries (T,H,DK), normalised and rotated as qk_norm_rope does; rows of
-    padding tokens are left as allocated."""
-    plan = _append_plan(_layouts(q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cache))
+    padding tokens are left as allocated.  With `seen` (draft_tree) the new tokens
+    are drafted trees, each rotated by its place on its path."""
+    plan = _append_plan(_layouts(q, k, v, wq, wk, cos, sin, starts, lens, table, k_cache, v_cache, seen))
     with _on(stream):
         qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        _append_call(plan, q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, qo, k_cache, v_cache,
-                     stream)
+        _append_call(plan, q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, seen, qo, k_cache,
+                     v_cache, stream)
     return qo
 
 
@@ -665,10 +845,13 @@ def alloc_paged(q, k_cache, v_cache, table):
     return torch.empty(wsb, dtype=torch.uint8, device=q.device)
 
 
-def paged_attention(q, k_cache, v_cache, starts, lens, table, causal=True, scale=None, stream=None):
+def paged_attention(q, k_cache, v_cache, starts, lens, table, causal=True, scale=None, stream=None, seen=None):
     """Returns (o (T,H,DV) in q's dtype, lse (H,T) float32); rows of padding
-    tokens are left as allocated."""
-    plan = _paged_plan(_layouts(q, k_cache, v_cache, starts, lens, table))
+    tokens are left as allocated.  With `seen` (draft_tree; causal) a new token
+    sees of the new ones up to itself only those whose bits are set."""
+    if seen is not None and not causal:
+        raise ValueError("drafted trees (seen) are causal")
+    plan = _paged_plan(_layouts(q, k_cache, v_cache, starts, lens, table, seen))
     T, H, DK = q.shape
     scale = DK ** -0.5 if scale is None else scale
     with _on(stream):
@@ -676,8 +859,45 @@ def paged_attention(q, k_cache, v_cache, starts, lens, table, causal=True, scale
         o = torch.empty((T, H, v_cache.shape[3]), dtype=q.dtype, device=dev)
         lse = torch.empty((H, T), dtype=torch.float32, device=dev)
         ws = torch.empty((wsb,), dtype=torch.uint8, device=dev) if wsb > 0 else None
-        _paged_call(plan, q, k_cache, v_cache, starts, lens, table, causal, scale, ws, wsb, o, lse, stream)
+        _paged_call(plan, q, k_cache, v_cache, starts, lens, table, seen, causal, scale, ws, wsb, o, lse, stream)
     return o, lse
+
+
+def draft_tree(starts, parents, most, stream=None):
+    """Who sees whom in drafted trees: seen (T, words) int32 for paged_append,
+    paged_attention and paged_accept, words enough for sequences of `most` new
+    tokens.  parents (T,) int32: the number in its sequence of each token's
+    predecessor, -1: what the cache held before the draft."""
+    plan = _tree_plan(_layouts(starts, parents), -(-int(most) // 32))
+    with _on(stream):
+        seen = torch.empty((plan[1], plan[2]), dtype=torch.int32, device=starts.device)
+        _tree_call(plan, starts, parents, seen, stream)
+    return seen
+
+
+def paged_accept(starts, lens, table, seen, last, k_cache, v_cache, stream=None):
+    """Keeps of each sequence's new tokens the path that ends at number last[b]
+    (-1: none): its rows move to the front of the new ones, in every layer.
+    Returns the lengths (B,) int32 with the path counted and the rest not."""
+    plan = _accept_plan(_layouts(starts, lens, table, seen, last, k_cache, v_cache))
+    with _on(stream):
+        out = torch.empty((plan[0].B,), dtype=torch.int32, device=lens.device)
+        _accept_call(plan, starts, lens, table, seen, last, k_cache, v_cache, out, stream)
+    return out
+
+
+def paged_reserve(table, refs, kept, lens, k_cache, v_cache, source=None, stream=None):
+    """Brings the table and its pages' reference counts in line: row b continues
+    row source[b] (None: itself; -1: nothing) with its first kept[b] tokens and gets
+    pages up to lens[b] tokens (0: freed); a shared page that it would go on writing
+    is copied for it, in every layer.  Returns the number of pages left free
+    ((1,) int32; below zero: how many were missing)."""
+    plan = _reserve_plan(_layouts(table, refs, source, kept, lens, k_cache, v_cache))
+    with _on(stream):
+        ws = torch.empty((plan[4],), dtype=torch.uint8, device=table.device)
+        spare = torch.empty((1,), dtype=torch.int32, device=table.device)
+        _reserve_call(plan, table, refs, source, kept, lens, k_cache, v_cache, ws, plan[4], spare, stream)
+    return spare
 
 
 def forward(q, k, v, mask=None, causal=False, scale=None, stream=None):

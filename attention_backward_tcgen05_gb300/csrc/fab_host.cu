@@ -387,7 +387,7 @@ FAB_API int fab_backward(const void* q, const void* k, const void* v, const void
 FAB_API int fab_last_device_error(fab_stream stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FAB_ERR_CUDA;
   const uint32_t e = take_error_tc() | take_error_dq() | take_error_fwd() | take_error_rope() | take_error_paged() |
-                     take_error_paged_tc();
+                     take_error_paged_tc() | take_error_pages();
   if (e & kErrSmemAlign) return FAB_ERR_CUDA;
   if (e & kErrTimeout) return FAB_ERR_TIMEOUT;
   return (e & kErrIndex) ? FAB_ERR_INVALID : FAB_OK;

@@ -108,6 +108,52 @@ PagedProblem paged_problem(const fab_paged_dims* d, int dtype) {
   return p;
 }
 
+// The trees of a call's T tokens.
+int check_seen(const int32_t* seen, int64_t words, int64_t T) {
+  if (words <= 0 || words > kMaxInt32 / 32) return FAB_ERR_INVALID;
+  if (T > 0 && (!aligned(seen, 16) || !fits(T, words, 1, 1))) return FAB_ERR_INVALID;
+  return FAB_OK;
+}
+
+// A cache of one layer or more and the table of its pages.
+int check_cache(const fab_cache_dims* d, int dtype, const void* k_cache, const void* v_cache) {
+  if (!d || !dtype_ok(dtype)) return FAB_ERR_INVALID;
+  if (d->B <= 0 || d->Hkv <= 0 || d->DK <= 0 || d->DV <= 0 || d->layers <= 0) return FAB_ERR_INVALID;
+  if (d->page <= 0 || d->pages <= 0 || d->max_pages <= 0) return FAB_ERR_INVALID;
+  if (d->page > kMaxInt32 || d->pages > kMaxInt32 || d->max_pages > kMaxInt32) return FAB_ERR_INVALID;
+  // (the kernels number a sequence's entries, and a layer's heads with their rows, in 32 bits)
+  if (d->B > (int64_t(1) << 30) / d->max_pages || d->layers > (int64_t(1) << 24) / d->Hkv) return FAB_ERR_INVALID;
+  if (!fits(d->pages, d->page, d->Hkv, d->DK) || !fits(d->pages, d->page, d->Hkv, d->DV)) return FAB_ERR_INVALID;
+  if (d->layers > 1) {
+    const int64_t rows = d->pages * d->page * d->Hkv;
+    if (d->ldk < rows * d->DK || d->ldv < rows * d->DV || d->ldk > kMaxElems / d->layers ||
+        d->ldv > kMaxElems / d->layers)
+      return FAB_ERR_INVALID;
+  }
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return FAB_ERR_INVALID;
+  return FAB_OK;
+}
+
+CacheProblem cache_problem(const fab_cache_dims* d, int dtype, void* k_cache, void* v_cache) {
+  CacheProblem p{};
+  p.B = d->B;
+  p.T = d->T;
+  p.words = d->words;
+  p.Hkv = d->Hkv;
+  p.DK = d->DK;
+  p.DV = d->DV;
+  p.page = d->page;
+  p.pages = d->pages;
+  p.max_pages = d->max_pages;
+  p.layers = d->layers;
+  p.ldk = d->layers > 1 ? d->ldk : 0;
+  p.ldv = d->layers > 1 ? d->ldv : 0;
+  p.dtype = dtype;
+  p.k = k_cache;
+  p.v = v_cache;
+  return p;
+}
+
 size_t paged_workspace_bytes(const PagedProblem& p) {
   return paged_tc_supported(p) ? paged_tc_workspace_bytes(p) : paged_simt_workspace_bytes(p);
 }
@@ -199,10 +245,13 @@ FAB_API int fab_qk_norm_rope_backward(const float* dq, const float* dk, const fl
   return from_cuda(launch_rope_backward(p, static_cast<cudaStream_t>(stream)));
 }
 
-FAB_API int fab_paged_append(const void* q, const void* k, const void* v, const void* wq, const void* wk,
-                             const float* cos, const float* sin, float eps, int interleaved, const int32_t* starts,
-                             const int32_t* lens, const int32_t* table, int dtype, const fab_paged_dims* dims,
-                             void* q_out, void* k_cache, void* v_cache, fab_stream stream) {
+namespace {
+
+// fab_paged_append, and with `seen` fab_paged_append_tree.
+int append(const void* q, const void* k, const void* v, const void* wq, const void* wk, const float* cos,
+           const float* sin, float eps, int interleaved, const int32_t* starts, const int32_t* lens,
+           const int32_t* table, const int32_t* seen, int64_t words, int dtype, const fab_paged_dims* dims, void* q_out,
+           void* k_cache, void* v_cache, fab_stream stream) {
   int rc = check_paged_dims(dims);
   if (rc != FAB_OK) return rc;
   if (!rot_ok(dims->rot, dims->DK, dims->P)) return FAB_ERR_INVALID;
@@ -246,21 +295,19 @@ FAB_API int fab_paged_append(const void* q, const void* k, const void* v, const 
   p.page = dims->page;
   p.pages = dims->pages;
   p.max_pages = dims->max_pages;
+  p.seen = reinterpret_cast<const uint32_t*>(seen);
+  p.words = words;
   p.q_out = q_out;
   p.k_out = k_cache;
   p.v_out = v_cache;
   return from_cuda(launch_rope(p, static_cast<cudaStream_t>(stream)));
 }
 
-FAB_API size_t fab_paged_attention_workspace_bytes(const fab_paged_dims* dims, int dtype) {
-  if (check_paged_dims(dims) != FAB_OK || !dtype_ok(dtype)) return 0;
-  return paged_workspace_bytes(paged_problem(dims, dtype));
-}
-
-FAB_API int fab_paged_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* starts,
-                                const int32_t* lens, const int32_t* table, int causal, float scale, int dtype,
-                                const fab_paged_dims* dims, void* workspace, size_t workspace_bytes, void* o,
-                                float* lse, fab_stream stream) {
+// fab_paged_attention, and with `seen` fab_paged_attention_tree.
+int attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* starts, const int32_t* lens,
+              const int32_t* table, const int32_t* seen, int64_t words, int causal, float scale, int dtype,
+              const fab_paged_dims* dims, void* workspace, size_t workspace_bytes, void* o, float* lse,
+              fab_stream stream) {
   const int rc = check_paged_dims(dims);
   if (rc != FAB_OK) return rc;
   if (!dtype_ok(dtype) || !isfinite(scale)) return FAB_ERR_INVALID;
@@ -280,6 +327,8 @@ FAB_API int fab_paged_attention(const void* q, const void* k_cache, const void* 
   p.starts = starts;
   p.lens = lens;
   p.table = table;
+  p.seen = reinterpret_cast<const uint32_t*>(seen);
+  p.words = words;
   p.o = o;
   p.lse = lse;
   p.workspace = workspace;
@@ -288,4 +337,108 @@ FAB_API int fab_paged_attention(const void* q, const void* k_cache, const void* 
     return from_cuda(launch_paged_tc(p, static_cast<cudaStream_t>(stream)));
   }
   return from_cuda(launch_paged_simt(p, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+FAB_API int fab_paged_append(const void* q, const void* k, const void* v, const void* wq, const void* wk,
+                             const float* cos, const float* sin, float eps, int interleaved, const int32_t* starts,
+                             const int32_t* lens, const int32_t* table, int dtype, const fab_paged_dims* dims,
+                             void* q_out, void* k_cache, void* v_cache, fab_stream stream) {
+  return append(q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, nullptr, 0, dtype, dims, q_out,
+                k_cache, v_cache, stream);
+}
+
+FAB_API int fab_paged_append_tree(const void* q, const void* k, const void* v, const void* wq, const void* wk,
+                                  const float* cos, const float* sin, float eps, int interleaved,
+                                  const int32_t* starts, const int32_t* lens, const int32_t* table,
+                                  const int32_t* seen, int64_t words, int dtype, const fab_paged_dims* dims,
+                                  void* q_out, void* k_cache, void* v_cache, fab_stream stream) {
+  const int rc = check_seen(seen, words, dims ? dims->T : 0);
+  if (rc != FAB_OK) return rc;
+  return append(q, k, v, wq, wk, cos, sin, eps, interleaved, starts, lens, table, seen, words, dtype, dims, q_out,
+                k_cache, v_cache, stream);
+}
+
+FAB_API size_t fab_paged_attention_workspace_bytes(const fab_paged_dims* dims, int dtype) {
+  if (check_paged_dims(dims) != FAB_OK || !dtype_ok(dtype)) return 0;
+  return paged_workspace_bytes(paged_problem(dims, dtype));
+}
+
+FAB_API int fab_paged_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* starts,
+                                const int32_t* lens, const int32_t* table, int causal, float scale, int dtype,
+                                const fab_paged_dims* dims, void* workspace, size_t workspace_bytes, void* o,
+                                float* lse, fab_stream stream) {
+  return attention(q, k_cache, v_cache, starts, lens, table, nullptr, 0, causal, scale, dtype, dims, workspace,
+                   workspace_bytes, o, lse, stream);
+}
+
+FAB_API int fab_paged_attention_tree(const void* q, const void* k_cache, const void* v_cache, const int32_t* starts,
+                                     const int32_t* lens, const int32_t* table, const int32_t* seen, int64_t words,
+                                     float scale, int dtype, const fab_paged_dims* dims, void* workspace,
+                                     size_t workspace_bytes, void* o, float* lse, fab_stream stream) {
+  const int rc = check_seen(seen, words, dims ? dims->T : 0);
+  if (rc != FAB_OK) return rc;
+  return attention(q, k_cache, v_cache, starts, lens, table, seen, words, 1, scale, dtype, dims, workspace,
+                   workspace_bytes, o, lse, stream);
+}
+
+FAB_API int fab_draft_tree(const int32_t* starts, const int32_t* parents, int64_t B, int64_t T, int64_t words,
+                           int32_t* seen, fab_stream stream) {
+  if (B <= 0 || B >= kMaxInt32 || T < 0 || T > kMaxTokens || !aligned(starts, 4)) return FAB_ERR_INVALID;
+  const int rc = check_seen(seen, words, T);
+  if (rc != FAB_OK) return rc;
+  if (T > 0 && !aligned(parents, 4)) return FAB_ERR_INVALID;
+  if (words > FAB_DRAFT_MAX_WORDS) return FAB_ERR_UNSUPPORTED;
+  if (T == 0) return FAB_OK;
+  return from_cuda(launch_draft_tree(starts, parents, B, T, words, reinterpret_cast<uint32_t*>(seen),
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+FAB_API int fab_paged_accept(const int32_t* starts, const int32_t* lens, const int32_t* table, const int32_t* seen,
+                             const int32_t* last, int dtype, const fab_cache_dims* dims, void* k_cache, void* v_cache,
+                             int32_t* lens_out, fab_stream stream) {
+  int rc = check_cache(dims, dtype, k_cache, v_cache);
+  if (rc != FAB_OK) return rc;
+  if (dims->T < 0 || dims->T > kMaxTokens) return FAB_ERR_INVALID;
+  rc = check_seen(seen, dims->words, dims->T);
+  if (rc != FAB_OK) return rc;
+  if (!aligned(starts, 4) || !aligned(lens, 4) || !aligned(table, 4) || !aligned(last, 4) || !aligned(lens_out, 4))
+    return FAB_ERR_INVALID;
+  if (!widths_ok(dims->DK, dims->DV)) return FAB_ERR_UNSUPPORTED;
+  CacheProblem p = cache_problem(dims, dtype, k_cache, v_cache);
+  p.starts = starts;
+  p.lens = lens;
+  p.table = const_cast<int32_t*>(table);
+  p.seen = reinterpret_cast<const uint32_t*>(seen);
+  p.last = last;
+  p.lens_out = lens_out;
+  return from_cuda(launch_paged_accept(p, static_cast<cudaStream_t>(stream)));
+}
+
+FAB_API size_t fab_paged_reserve_workspace_bytes(const fab_cache_dims* dims) {
+  static const int32_t any __attribute__((aligned(16))) = 0;  // (an aligned address: no cache is read)
+  if (check_cache(dims, FAB_F32, &any, &any) != FAB_OK) return 0;
+  return paged_reserve_workspace_bytes(cache_problem(dims, FAB_F32, nullptr, nullptr));
+}
+
+FAB_API int fab_paged_reserve(int32_t* table, int32_t* refs, const int32_t* source, const int32_t* kept,
+                              const int32_t* lens, int dtype, const fab_cache_dims* dims, void* k_cache, void* v_cache,
+                              void* workspace, size_t workspace_bytes, int32_t* spare, fab_stream stream) {
+  const int rc = check_cache(dims, dtype, k_cache, v_cache);
+  if (rc != FAB_OK) return rc;
+  if (!aligned(table, 4) || !aligned(refs, 16) || (source && !aligned(source, 4)) || !aligned(kept, 4) ||
+      !aligned(lens, 4) || !aligned(spare, 4))
+    return FAB_ERR_INVALID;
+  if (!widths_ok(dims->DK, dims->DV)) return FAB_ERR_UNSUPPORTED;
+  if (!aligned(workspace, 16) || workspace_bytes < fab_paged_reserve_workspace_bytes(dims)) return FAB_ERR_WORKSPACE;
+  CacheProblem p = cache_problem(dims, dtype, k_cache, v_cache);
+  p.table = table;
+  p.refs = refs;
+  p.source = source;
+  p.kept = kept;
+  p.lens = lens;
+  p.spare = spare;
+  p.workspace = workspace;
+  return from_cuda(launch_paged_reserve(p, static_cast<cudaStream_t>(stream)));
 }

@@ -86,6 +86,10 @@ struct RopeProblem {
   // v_out are the caches
   const int32_t *starts, *lens, *table;
   int64_t seqs, page, pages, max_pages;
+  // appending drafted tokens (or null): row t of `words` words says which new
+  // tokens of its sequence token t sees; it is rotated by its place on its path
+  const uint32_t* seen;
+  int64_t words;
   // backward
   const float *dq, *dk, *dv;
   void *gq, *gk, *gv;
@@ -105,6 +109,8 @@ struct PagedProblem {
   int dtype;
   const void *q, *k, *v;
   const int32_t *starts, *lens, *table;
+  const uint32_t* seen;  // drafted trees (then causal): [words,T], else null
+  int64_t words;
   void* o;
   float* lse;  // or null
   void* workspace;
@@ -117,6 +123,26 @@ cudaError_t launch_paged_tc(const PagedProblem& p, cudaStream_t s);
 // fab_paged_simt.cu: CUDA cores, every dtype, DK, DV <= 256, any page.
 size_t paged_simt_workspace_bytes(const PagedProblem& p);
 cudaError_t launch_paged_simt(const PagedProblem& p, cudaStream_t s);
+
+// fab_pages.cu: who sees whom in drafted trees, keeping an accepted path, and
+// the pages of a cache.
+struct CacheProblem {
+  int64_t B, T, words, Hkv, DK, DV, page, pages, max_pages, layers, ldk, ldv;
+  int dtype;
+  const int32_t *starts, *lens;
+  const uint32_t* seen;
+  const int32_t* last;                // accept
+  int32_t* lens_out;                  // accept
+  int32_t *table, *refs, *spare;      // (accept reads the table only)
+  const int32_t *kept, *source;       // reserve; source may be null
+  void *k, *v;
+  void* workspace;
+};
+cudaError_t launch_draft_tree(const int32_t* starts, const int32_t* parents, int64_t B, int64_t T, int64_t words,
+                              uint32_t* seen, cudaStream_t s);
+cudaError_t launch_paged_accept(const CacheProblem& p, cudaStream_t s);
+size_t paged_reserve_workspace_bytes(const CacheProblem& p);
+cudaError_t launch_paged_reserve(const CacheProblem& p, cudaStream_t s);
 
 // fab_host.cu: the checks the entry points share.
 bool dtype_ok(int dtype);
@@ -138,5 +164,6 @@ uint32_t take_error_fwd();
 uint32_t take_error_rope();
 uint32_t take_error_paged();
 uint32_t take_error_paged_tc();
+uint32_t take_error_pages();
 
 }  // namespace fab

@@ -24,6 +24,7 @@
 
 #include "fab_device.cuh"
 #include "fab_internal.h"
+#include "fab_launch.cuh"
 
 namespace fab {
 
@@ -479,24 +480,6 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
       if (lse != nullptr && c0 == 0) lse[h * p.T + t] = l == 0.f ? INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
   }
-}
-
-// Launches a kernel that may start while the one before it in the stream still
-// runs, and waits for that one itself (griddepcontrol.wait) before it touches
-// memory: its launch and its first instructions cost no time of their own.
-template <typename... P, typename... A>
-cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
 // Sets plan.whole and returns the grid.  Short calls are not cut: a CTA then walks

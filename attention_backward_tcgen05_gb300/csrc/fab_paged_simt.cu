@@ -6,6 +6,8 @@
 //   token i of the n new ones of sequence b, head h:
 //   s_m = scale q . k_m over m <= lens[b] - n + i (causal) or m < lens[b],
 //   o = sum softmax(s)_m v_m,  lse = log sum exp(s_m)
+// Drafted trees (TREE): causal, and of the new keys m = lens[b] - n + j only
+// those whose bit j is set in the token's row of `seen`.
 //
 // The work is shared out as on the tensor cores (fab_paged.cuh), with tiles of
 // R rows and key tiles of 64.  Each of a CTA's eight warps owns 8 keys of every
@@ -59,6 +61,8 @@ struct SimtParams {
   int stages;          // of a warp's ring
   int bulk;            // rows come in whole aligned 16-byte pieces
   float c1;            // scale log2 e
+  const uint32_t* seen;
+  int words;
   const void *q, *k, *v;
   void* o;
   float* lse;
@@ -88,7 +92,7 @@ FAB_DEV float halve(bool set, float first, float second, int bit) {
   return keep + __shfl_xor_sync(0xffffffffu, give, bit);
 }
 
-template <typename T, int R, int CPL>
+template <typename T, int R, int CPL, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_constant__ SimtParams p) {
   static_assert((R == 4 || R == 8 || R == 16) && CPL % 4 == 0, "");
   constexpr int RPL = R / 4;  // rows a lane scores
@@ -150,7 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
         v = to_f32(static_cast<const T*>(p.q)[((int64_t)(w.q.s0 + token0 + i) * p.H + (int64_t)hk * plan.G + g) * p.DK + d]);
       q_s[x] = v;
     }
-    if (threadIdx.x == 0 && plan.lens[w.at.b] > plan.max_keys) atomicOr(&g_err_paged, kErrIndex);
+    if (threadIdx.x == 0 && (plan.lens[w.at.b] > plan.max_keys || (TREE && w.q.n > (int64_t)p.words * 32)))
+      atomicOr(&g_err_paged, kErrIndex);
     __syncthreads();
     int last[RPL];  // last key that each of this lane's rows sees
 #pragma unroll
@@ -234,6 +239,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
         break;
       }
       __syncwarp();
+      // whether this lane's rows see its key, where it is a new token's: fetched ahead of the sums
+      [[maybe_unused]] uint32_t see[RPL];
+      if constexpr (TREE) {
+        const int at = j * 64 + warp * kKeys + key - w.q.last0;  // the key's number among the new ones
+#pragma unroll
+        for (int e = 0; e < RPL; ++e) {
+          const int token = token0 + (rg * RPL + e) / plan.gw;
+          see[e] = at < 0 ? 1u
+                   : token < w.q.n && at >> 5 < p.words
+                       ? __ldg(p.seen + (int64_t)(w.q.s0 + token) * p.words + (at >> 5)) >> (at & 31) & 1u
+                       : 0u;
+        }
+      }
       const uint8_t* kb = ring + out * stage_bytes + kg * 4 * p.ks;
       const uint8_t* vb = ring + out * stage_bytes + kKeys * p.ks;
       float part[4][4];  // [row][key] over this lane's columns
@@ -280,7 +298,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
       float f[RPL];
 #pragma unroll
       for (int e = 0; e < RPL; ++e) {
-        s[e] = mk <= last[e] ? s[e] * p.c1 : -INFINITY;
+        bool sees = mk <= last[e];
+        if constexpr (TREE) sees = sees && see[e] != 0u;
+        s[e] = sees ? s[e] * p.c1 : -INFINITY;
         float top = s[e];
 #pragma unroll
         for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -422,7 +442,7 @@ PagedPlan plan_of(const PagedProblem& pr) {
   return p;
 }
 
-template <typename T, int R, int CPL>
+template <typename T, int R, int CPL, bool TREE>
 cudaError_t launch_r(const PagedProblem& pr, int sms, cudaStream_t s) {
   SimtParams p;
   p.plan = plan_of(pr);
@@ -441,6 +461,8 @@ cudaError_t launch_r(const PagedProblem& pr, int sms, cudaStream_t s) {
   p.vs = (dp_of(pr) * e + 15) / 16 * 16;
   p.bulk = p.DK * e % 16 == 0 && p.DV * e % 16 == 0;
   p.c1 = pr.scale * kLog2e;
+  p.seen = pr.seen;
+  p.words = (int)pr.words;
   p.q = pr.q;
   p.k = pr.k;
   p.v = pr.v;
@@ -453,20 +475,25 @@ cudaError_t launch_r(const PagedProblem& pr, int sms, cudaStream_t s) {
   const int smem = fixed + (p.stages * stage > end ? p.stages * stage : end);
   const int grid = paged_grid(&p.plan, sms, kFewTiles);
   // (the limit is the kernel's, for all threads of the process: every call sets the same, whatever it needs itself)
-  cudaError_t err =
-      cudaFuncSetAttribute(paged_simt_kernel<T, R, CPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+  const auto kernel = paged_simt_kernel<T, R, CPL, TREE>;
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (err != cudaSuccess) return err;
-  err = launch_early(paged_simt_kernel<T, R, CPL>, dim3((unsigned)grid), kThreads, (size_t)smem, s, p);
+  err = launch_early(kernel, dim3((unsigned)grid), kThreads, (size_t)smem, s, p);
   if (err != cudaSuccess) return err;
   return launch_combine<T>(p.plan, p.parts, grid, p.DV, p.H, static_cast<T*>(pr.o), pr.lse, s);
 }
 
+template <typename T, bool TREE>
+cudaError_t launch_m(const PagedProblem& pr, int sms, cudaStream_t s) {
+  const int R = rows_of(pr);
+  if (pr.DV > 128) return R == 4 ? launch_r<T, 4, 8, TREE>(pr, sms, s) : launch_r<T, 8, 8, TREE>(pr, sms, s);
+  if (R == 16) return launch_r<T, 16, 4, TREE>(pr, sms, s);
+  return R == 4 ? launch_r<T, 4, 4, TREE>(pr, sms, s) : launch_r<T, 8, 4, TREE>(pr, sms, s);
+}
+
 template <typename T>
 cudaError_t launch_t(const PagedProblem& pr, int sms, cudaStream_t s) {
-  const int R = rows_of(pr);
-  if (pr.DV > 128) return R == 4 ? launch_r<T, 4, 8>(pr, sms, s) : launch_r<T, 8, 8>(pr, sms, s);
-  if (R == 16) return launch_r<T, 16, 4>(pr, sms, s);
-  return R == 4 ? launch_r<T, 4, 4>(pr, sms, s) : launch_r<T, 8, 4>(pr, sms, s);
+  return pr.seen != nullptr ? launch_m<T, true>(pr, sms, s) : launch_m<T, false>(pr, sms, s);
 }
 
 }  // namespace

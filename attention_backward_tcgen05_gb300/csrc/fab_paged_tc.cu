@@ -5,6 +5,8 @@
 //   token i of the n new ones of sequence b, head h:
 //   s_m = scale q . k_m over m <= lens[b] - n + i (causal) or m < lens[b],
 //   o = sum softmax(s)_m v_m,  lse = log sum exp(s_m)
+// Drafted trees (TREE): causal, and of the new keys m = lens[b] - n + j only
+// those whose bit j is set in the token's row of `seen`.
 //
 // Tiles.  A row of a tile is a (token, query head) pair of one key/value head:
 // 128 / group tokens times the group's heads, so a page of keys is read once
@@ -138,6 +140,8 @@ struct TcParams {
   int page, box;  // rows of a page, of a TMA box
   int H, DV;
   float scale;
+  const uint32_t* seen;
+  int words;
   void* o;
   float* lse;
 };
@@ -145,7 +149,7 @@ struct TcParams {
 FAB_DEV void reg_dealloc() { asm volatile("setmaxnreg.dec.sync.aligned.u32 96;"); }
 FAB_DEV void reg_alloc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 200;"); }
 
-template <int DP, bool F16>
+template <int DP, bool F16, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TcParams p) {
@@ -293,7 +297,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         int row, page = lookup(j0, row);
         if (keys) {
-          if (lane == 0 && plan.lens[u.b] > plan.max_keys) atomicOr(err, kErrIndex);
+          if (lane == 0 && (plan.lens[u.b] > plan.max_keys || (TREE && u.n > (int64_t)p.words * 32)))
+            atomicOr(err, kErrIndex);
           for (int s = 0; s < u.width; ++s) {
             if (!wait(B_QE + qslot, qphase)) break;
             if (lane == 0) {
@@ -603,6 +608,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t buf = C::NB == 3 ? step % 3u : (uint32_t)s;
           const uint32_t tS = tm + lane_off + C::TM_S + buf * 128;
           if (C::NB == 3) sphase = (step / 3u) & 1u;
+          // the words that say which of the tile's keys the row sees, fetched while its
+          // products run: all of the past, of the new tokens those whose bits are set
+          [[maybe_unused]] uint32_t wd[5];
+          [[maybe_unused]] const int off = t * 128 + u.j0 * 128 - u.last0;  // the tile's first key, from the first new one
+          [[maybe_unused]] const bool masked = TREE && off + 127 >= 0;
+          if constexpr (TREE) {
+            if (masked) {
+              const uint32_t* row = p.seen + (int64_t)(u.s0 + token) * p.words;
+#pragma unroll
+              for (int c = 0; c < 5; ++c) {
+                const int w = (off >> 5) + c;
+                wd[c] = w < 0 ? 0xffffffffu : row_ok && w < p.words ? __ldg(row + w) : 0u;
+              }
+            }
+          }
           if (!ok || !(ok = __all_sync(0xffffffffu, mbar_wait_asleep(bar(B_S + buf), sphase, abort_flag, err)))) break;
           sphase ^= 1;
           if (active) {
@@ -614,7 +634,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld_wait(x[c]);
             auto sv = [&](int e) -> uint32_t& { return x[e >> 5][e & 31]; };
-            if (__any_sync(0xffffffffu, row_ok && k0 + 127 > last)) {
+            if (TREE) {
+              if (masked || __any_sync(0xffffffffu, row_ok && k0 + 127 > last)) {
+                const int lim = last - k0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  const int top = lim - c * 32;  // last key of these 32 up to the token itself
+                  uint32_t see = top < 0 ? 0u : top >= 31 ? 0xffffffffu : (2u << top) - 1u;
+                  if (masked) see &= __funnelshift_r(wd[c], wd[c + 1], (uint32_t)off & 31u);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (!(see >> e & 1u)) x[c][e] = 0xff800000u;  // -inf
+                }
+              }
+            } else if (__any_sync(0xffffffffu, row_ok && k0 + 127 > last)) {
               const int lim = last - k0;
 #pragma unroll
               for (int e = 0; e < 128; ++e)
@@ -831,7 +864,7 @@ PagedPlan plan_of(const PagedProblem& pr) {
   return p;
 }
 
-template <int DP, bool F16>
+template <int DP, bool F16, bool TREE>
 cudaError_t launch_d(const PagedProblem& pr, int sms, cudaStream_t s) {
   using C = PCfg<DP>;
   using T = typename std::conditional<F16, __half, __nv_bfloat16>::type;
@@ -846,6 +879,8 @@ cudaError_t launch_d(const PagedProblem& pr, int sms, cudaStream_t s) {
   p.H = (int)pr.H;
   p.DV = (int)pr.DV;
   p.scale = pr.scale;
+  p.seen = pr.seen;
+  p.words = (int)pr.words;
   p.o = pr.o;
   p.lse = pr.lse;
   CUtensorMap mq, mk, mv;
@@ -863,10 +898,10 @@ cudaError_t launch_d(const PagedProblem& pr, int sms, cudaStream_t s) {
     if (!make_map(v ? &mv : &mk, F16, 4, v ? pr.v : pr.k, dims, str, box)) return cudaErrorInvalidValue;
   }
   const int grid = paged_grid(&p.plan, sms, kFewTiles);
-  cudaError_t err =
-      cudaFuncSetAttribute(paged_tc_kernel<DP, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  const auto kernel = paged_tc_kernel<DP, F16, TREE>;
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (err != cudaSuccess) return err;
-  err = launch_early(paged_tc_kernel<DP, F16>, dim3((unsigned)grid), kThreads, C::SMEM, s, mq, mk, mv, p);
+  err = launch_early(kernel, dim3((unsigned)grid), kThreads, C::SMEM, s, mq, mk, mv, p);
   if (err != cudaSuccess) return err;
   return launch_combine<T>(p.plan, p.parts, grid, (int)pr.DV, (int)pr.H, static_cast<T*>(pr.o), pr.lse, s);
 }
@@ -891,9 +926,13 @@ size_t paged_tc_workspace_bytes(const PagedProblem& p) {
 cudaError_t launch_paged_tc(const PagedProblem& p, cudaStream_t s) {
   const int sms = paged_sms();
   if (sms == 0) return cudaErrorInvalidValue;
-  if (padded_width(p) == 128)
-    return p.dtype == FAB_F16 ? launch_d<128, true>(p, sms, s) : launch_d<128, false>(p, sms, s);
-  return p.dtype == FAB_F16 ? launch_d<64, true>(p, sms, s) : launch_d<64, false>(p, sms, s);
+  const bool wide = padded_width(p) == 128;
+  if (p.seen != nullptr) {
+    if (wide) return p.dtype == FAB_F16 ? launch_d<128, true, true>(p, sms, s) : launch_d<128, false, true>(p, sms, s);
+    return p.dtype == FAB_F16 ? launch_d<64, true, true>(p, sms, s) : launch_d<64, false, true>(p, sms, s);
+  }
+  if (wide) return p.dtype == FAB_F16 ? launch_d<128, true, false>(p, sms, s) : launch_d<128, false, false>(p, sms, s);
+  return p.dtype == FAB_F16 ? launch_d<64, true, false>(p, sms, s) : launch_d<64, false, false>(p, sms, s);
 }
 
 uint32_t take_error_paged_tc() {

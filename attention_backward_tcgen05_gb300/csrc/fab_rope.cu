@@ -75,6 +75,17 @@ __device__ Place place_of(const RopeProblem& p, int64_t t) {
         bad = true;
       }
     }
+    if (p.seen != nullptr) {
+      // a drafted token lies in the row of its number and stands as far behind
+      // the past as it sees earlier ones
+      const int i = (int)(t - s0);
+      const uint32_t* row = p.seen + t * p.words;
+      int deep = 0;
+      for (int w = 0; w <= i >> 5 && w < p.words; ++w)
+        deep += __popc(w < i >> 5 ? row[w] : row[w] & ((1u << (i & 31)) - 1u));
+      bad |= i >= 32 * p.words;
+      x.pos += deep - i;
+    }
   } else {
     x.pos = p.pos != nullptr ? p.pos[t] : t % p.N;
   }

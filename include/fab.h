@@ -325,11 +325,118 @@ FAB_EXPORT int fab_paged_attention(const void* q, const void* k_cache, const voi
                                    const fab_paged_dims* dims, void* workspace, size_t workspace_bytes, void* o,
                                    float* lse, fab_stream stream);
 
+/* ---- Drafted trees ----
+ *
+ * A draft is a tree of tokens that go on from what a sequence's cache holds: the
+ * new tokens of fab_paged_append and fab_paged_attention, of which each sees its
+ * ancestors and not the other branches.  Who sees whom is a row of `words`
+ * 32-bit words for each of the T tokens: bit j % 32 of word j / 32 of token i's
+ * row is set where token i sees new token j of its sequence; only bits j <= i
+ * count.  words is at least the largest sequence's new tokens / 32, rounded up (a
+ * sequence of more is reported as FAB_ERR_INVALID, its results are meaningless).
+ * One step is fab_paged_reserve, fab_draft_tree, then for each layer
+ * fab_paged_append_tree and fab_paged_attention_tree, then fab_paged_accept. */
+
+/* Words of a row that fab_draft_tree takes at most (16,384 new tokens). */
+#define FAB_DRAFT_MAX_WORDS 512
+
+/* seen [words,T] (device int32, 16-byte aligned): each token's own bit and its
+ * ancestors'.  parents [T] (device int32): token i of a sequence follows its token
+ * parents[i] < i, or, -1, what the cache held before; anything else is reported
+ * as FAB_ERR_INVALID and taken as -1.  starts as above; rows of tokens from
+ * starts[B] on are left as they were.  Words past FAB_DRAFT_MAX_WORDS are
+ * FAB_ERR_UNSUPPORTED. */
+FAB_EXPORT int fab_draft_tree(const int32_t* starts, const int32_t* parents, int64_t B, int64_t T, int64_t words,
+                              int32_t* seen, fab_stream stream);
+
+/* fab_paged_append of a draft: token i is written where fab_paged_append writes
+ * it, and rotated by the position lens[b] - n + (new tokens before it that it
+ * sees): its place on its path. */
+FAB_EXPORT int fab_paged_append_tree(const void* q, const void* k, const void* v, const void* wq, const void* wk,
+                                     const float* cos, const float* sin, float eps, int interleaved,
+                                     const int32_t* starts, const int32_t* lens, const int32_t* table,
+                                     const int32_t* seen, int64_t words, int dtype, const fab_paged_dims* dims,
+                                     void* q_out, void* k_cache, void* v_cache, fab_stream stream);
+
+/* fab_paged_attention of a draft, causal: token i sees the keys before the
+ * sequence's new tokens, and of those the j <= i whose bits are set.  A token
+ * without a key gets o = 0 and lse = +inf.  Rows before lens[b] have to be finite,
+ * those of branches that a token does not see too.  Types, widths, roundings and the
+ * workspace (fab_paged_attention_workspace_bytes) are fab_paged_attention's. */
+FAB_EXPORT int fab_paged_attention_tree(const void* q, const void* k_cache, const void* v_cache, const int32_t* starts,
+                                        const int32_t* lens, const int32_t* table, const int32_t* seen, int64_t words,
+                                        float scale, int dtype, const fab_paged_dims* dims, void* workspace,
+                                        size_t workspace_bytes, void* o, float* lse, fab_stream stream);
+
+/* ---- Rows and pages of a cache, in all layers at once ---- */
+
+/* A cache of `layers` layers that share one table: layer l's keys are the cache
+ * [DK, page, Hkv, pages] from element l*ldk on, its values from l*ldv on (ldk, ldv
+ * at least a layer's elements; not read for one layer).  B * max_pages is at
+ * most 2^30, layers * Hkv at most 2^24. */
+typedef struct {
+  int64_t B;             /* sequences (rows of the table) */
+  int64_t T, words;      /* new tokens, words of a row of `seen` (fab_paged_accept only) */
+  int64_t Hkv, DK, DV;   /* key/value heads, key width, value width (<= 256) */
+  int64_t page;          /* rows of a page */
+  int64_t pages;         /* pages of the cache */
+  int64_t max_pages;     /* entries of a sequence's row of the table */
+  int64_t layers;
+  int64_t ldk, ldv;
+} fab_cache_dims;
+
+/* Keeps one path of each draft: last[b] is the number (among the new tokens of
+ * sequence b) of the last token accepted, -1 for none.  The tokens that it sees up to
+ * itself become the sequence's next ones: their rows move, in order, to the places
+ * from lens[b] - n on, in every layer, and lens_out[b] = lens[b] - n + how many they
+ * are (lens[b] for a sequence without new tokens, whose last[b] is not read).  What the rows behind
+ * them hold afterwards is not defined; no other row is written.  starts,
+ * lens (counting the draft), table, seen, last: device int32 as the calls before
+ * had them; lens_out: device int32 [B], not overlapping them.  No two sequences may
+ * share a page that holds new tokens.  A last[b] outside -1 .. n-1, or lens, starts
+ * and pages out of range, are reported as FAB_ERR_INVALID, and touch nothing outside
+ * the arguments. */
+FAB_EXPORT int fab_paged_accept(const int32_t* starts, const int32_t* lens, const int32_t* table, const int32_t* seen,
+                                const int32_t* last, int dtype, const fab_cache_dims* dims, void* k_cache,
+                                void* v_cache, int32_t* lens_out, fab_stream stream);
+
+/* Device workspace bytes of fab_paged_reserve; 0 for bad dims. */
+FAB_EXPORT size_t fab_paged_reserve_workspace_bytes(const fab_cache_dims* dims);
+
+/* Hands out the pages of a cache.  table [max_pages,B]: entries that hold no page
+ * are -1.  refs [pages] (16-byte aligned): how many entries of the table name each
+ * page, 0: it is free.  Both are read and brought up to date.  Row b afterwards
+ * has room for lens[b] tokens and holds the first kept[b] (lens[b] where that is
+ * less) of the row source[b] as it was before the call (source NULL: of itself;
+ * source[b] = -1: of none):
+ *   - the entries of those tokens' pages are carried over, and shared where
+ *     several rows continue one (a fork);
+ *   - where lens[b] > kept[b] and the last of those pages is partly filled, it will be
+ *     written, and may then belong to no other row: the lowest such row keeps it if
+ *     all rows that hold it would write it, every other gets a fresh page with
+ *     its kept[b] % page rows copied, in every layer;
+ *   - further entries up to lens[b] are fresh pages, those behind are -1, and pages
+ *     that no entry names any more are free (lens[b] = 0 frees a row).
+ * Fresh pages are the free ones, lowest first, in order of row and entry, those
+ * that this call frees among them.  spare [1] gets the number of pages left
+ * free, below zero the number that were missing: the last entries in that order
+ * are then -1, and what a copy among them should have held is lost.
+ * source, kept, lens: device int32 [B].  kept[b] past what the row source[b] holds,
+ * or any of them out of range, and references that do not fit the table, are reported
+ * as FAB_ERR_INVALID (the rows concerned are meaningless; nothing outside the
+ * arguments is touched).  fab_cache_dims' T and words are not read.  workspace: device,
+ * fab_paged_reserve_workspace_bytes() bytes, contents overwritten; calls that may
+ * overlap on the GPU need one each. */
+FAB_EXPORT int fab_paged_reserve(int32_t* table, int32_t* refs, const int32_t* source, const int32_t* kept,
+                                 const int32_t* lens, int dtype, const fab_cache_dims* dims, void* k_cache,
+                                 void* v_cache, void* workspace, size_t workspace_bytes, int32_t* spare,
+                                 fab_stream stream);
+
 /* Synchronises `stream`, then returns and clears the device-side error word
  * of the current device: FAB_OK, FAB_ERR_TIMEOUT (a bounded wait inside a
  * kernel ran out; that kernel's outputs are invalid), FAB_ERR_INVALID (a
- * position, page number or start that a kernel read from device memory was out
- * of range) or FAB_ERR_CUDA. */
+ * position, page number, start or other index that a kernel read from device
+ * memory was out of range) or FAB_ERR_CUDA. */
 FAB_EXPORT int fab_last_device_error(fab_stream stream);
 
 #ifdef __cplusplus
