@@ -199,6 +199,17 @@ FAB_DEV void tma_store_4d(const CUtensorMap* map, uint32_t src, int c0, int c1, 
                : "memory");
 }
 
+// Stores `bytes` (a multiple of 16, both sides 16-byte aligned) of shared memory,
+// in this thread's bulk group.
+FAB_DEV void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(__cvta_generic_to_global(dst)),
+               "r"(src), "r"(bytes)
+               : "memory");
+}
+
+// Waits until this thread's bulk groups are done.
+FAB_DEV void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 FAB_DEV void bulk_commit_group() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
 // Waits until every bulk store this thread committed has finished reading
@@ -494,6 +505,12 @@ FAB_DEV uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
+}
+
+// Barrier for all threads of the cluster; what they wrote before it, to global
+// memory too, is seen behind it.
+FAB_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Sets kErrIndex in *err unless starts[0 .. B] ascends from 0 to at most T;

@@ -3,6 +3,8 @@
 // holds which page (forked, grown, cut, freed, copied before it is written).
 #include <limits.h>
 
+#include <type_traits>
+
 #include "fab.h"
 #include "fab_device.cuh"
 #include "fab_internal.h"
@@ -103,136 +105,307 @@ __global__ void __launch_bounds__(kTreeThreads) draft_tree_kernel(const int32_t*
 //
 // Row j of a path lies at or behind row j of its destination, paths ascend, and
 // no two paths share a row: rows are moved in order, a batch read whole before it
-// is written, by one warp for each (layer, head, keys or values), and nothing is
-// overwritten before it has been read.
+// is written, by one warp for each item (keys or values, layer, head) of a
+// sequence, and nothing is overwritten before it has been read.
+//
+// How many rows move is known on the device only, and differs: the items of all
+// sequences form one line, each as long as its rows, and every warp takes an equal
+// piece of it (the items that begin there).  Each CTA lays the line out for itself.
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoves = 64;  // rows of a path listed at once
+constexpr int kMoveWarps = kMoveThreads / 32;
+constexpr int kMoveCtas = 2;  // CTAs that an SM holds
+constexpr int kMoves = 64;    // rows of a path listed at once
+constexpr int kMoveBuffer = 8192;  // bytes of rows that a warp has on their way
 
+// How rows of a cache are moved: in pieces of 16 bytes where every row of every
+// layer starts at 16 bytes, else of an element.  Index 0: keys, 1: values.
+struct Pieces {
+  int row[2];        // pieces of a row
+  int64_t layer[2];  // from one layer to the next
+  int bytes;
+};
+Pieces pieces_of(const CacheProblem& p) {
+  const int64_t e = p.dtype == FAB_F32 ? 4 : 2;
+  const bool whole = p.DK * e % 16 == 0 && p.DV * e % 16 == 0 && p.ldk * e % 16 == 0 && p.ldv * e % 16 == 0;
+  Pieces x;
+  x.bytes = whole ? 16 : (int)e;
+  x.row[0] = (int)(p.DK * e / x.bytes);
+  x.row[1] = (int)(p.DV * e / x.bytes);
+  x.layer[0] = p.ldk * e / x.bytes;
+  x.layer[1] = p.ldv * e / x.bytes;
+  return x;
+}
+
+// What a sequence keeps.
+struct PathPlan {
+  int64_t past;        // rows before the new tokens
+  const uint32_t* row; // who the path's last token sees, itself included
+  int words;           // words of it up to that token's (0: nothing is kept)
+  uint32_t last_mask;  // of the last one
+  bool bad;
+};
+FAB_DEV PathPlan path_plan(const CacheProblem& p, int64_t b) {
+  const int64_t s0 = p.starts[b], n = (int64_t)p.starts[b + 1] - s0, len = p.lens[b], told = p.last[b];
+  const int64_t last = n > 0 ? told : -1;
+  PathPlan x;
+  x.past = len - n;
+  x.bad = s0 < 0 || n < 0 || s0 + n > p.T || x.past < 0 || len > p.max_pages * p.page || last < -1 || last >= n ||
+          last >= 32 * p.words;
+  x.words = x.bad || last < 0 ? 0 : (int)(last >> 5) + 1;
+  x.row = p.seen + (x.words > 0 ? s0 + last : 0) * p.words;
+  x.last_mask = (last & 31) == 31 ? 0xffffffffu : (2u << (last & 31)) - 1u;
+  return x;
+}
+FAB_DEV uint32_t path_word(const PathPlan& x, int w) {
+  const uint32_t bits = __ldg(x.row + w);
+  return w == x.words - 1 ? bits & x.last_mask : bits;
+}
+
+// a / b for a >= 0, b > 0 (a 64-bit division is some hundred instructions)
+FAB_DEV int64_t ratio(int64_t a, int64_t b) {
+  return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// Copies `rows` rows of a cache from src to dst (a lane's own; null: none), one
+// warp.  Rows of whole aligned 16-byte pieces go through shared memory by bulk
+// copies, a lane a row: 256 B cost a lane two instructions, where copies through
+// registers have the whole warp work on two rows (64 drafts in 32 layers, 52 MB: 15.6
+// us, through registers 17.0, both with the rows shared out evenly; a CTA a sequence and
+// an equal share of the items, through registers, 21.7).
+struct BulkMover {
+  uint32_t buf, bar;  // kMoveBuffer bytes, a barrier
+  uint32_t phase;
+  volatile uint32_t* abort_flag;
+  FAB_DEV int most(uint32_t row_bytes) const {
+    const int n = kMoveBuffer / (int)row_bytes;
+    return n < 32 ? n : 32;
+  }
+  FAB_DEV bool operator()(const uint8_t* src, uint8_t* dst, uint32_t row_bytes) {
+    const uint32_t mine = buf + lane_id() * row_bytes;
+    bulk_wait_read_all();  // (the rows before have left the buffer)
+    const uint32_t there = (uint32_t)__popc(__ballot_sync(0xffffffffu, src != nullptr));
+    if (lane_id() == 0) mbar_arrive_expect_tx(bar, there * row_bytes);
+    __syncwarp();
+    if (src != nullptr) bulk_load(mine, src, row_bytes, bar);
+    if (!__all_sync(0xffffffffu, mbar_wait_asleep(bar, phase, abort_flag, &g_err_pages))) {
+      mbar_drain(bar, phase);  // (what is on its way lands before shared memory goes)
+      return false;
+    }
+    phase ^= 1u;
+    if (src != nullptr) bulk_store(dst, mine, row_bytes);
+    bulk_commit_group();
+    return true;
+  }
+  FAB_DEV void finish() { bulk_wait_all(); }
+};
 template <typename V>
-__global__ void __launch_bounds__(kMoveThreads) paged_accept_kernel(const CacheProblem p, int kv, int vv) {
-  __shared__ int64_t from_s[kMoves], to_s[kMoves];  // rows, as if of head 0
-  __shared__ int count_s, next_s;
+struct PieceMover {
+  FAB_DEV int most(uint32_t) const { return 32; }
+  FAB_DEV bool operator()(const uint8_t* src, uint8_t* dst, uint32_t row_bytes) {
+    const int n = (int)(row_bytes / sizeof(V)), lane = (int)lane_id();
+    // four rows at a time, each at most 256 pieces
+    for (int r0 = 0; r0 < 32; r0 += 4) {
+      V v[4][8];
+      uint64_t to[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const V* from = reinterpret_cast<const V*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(src), r0 + r));
+        to[r] = from != nullptr ? __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), r0 + r) : 0;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (from != nullptr && u * 32 + lane < n) v[r][u] = from[u * 32 + lane];
+      }
+      __syncwarp();
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (to[r] != 0 && u * 32 + lane < n) reinterpret_cast<V*>(to[r])[u * 32 + lane] = v[r][u];
+      __syncwarp();
+    }
+    return true;
+  }
+  FAB_DEV void finish() {}
+};
+
+// V: uint4 (bulk copies) or an element.
+template <typename V>
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) paged_accept_kernel(const CacheProblem p, const Pieces pc) {
+  constexpr bool kBulk = sizeof(V) == 16;
+  extern __shared__ __align__(128) uint8_t buf_s[];
+  __shared__ int64_t from_s[kMoveWarps][kMoves], to_s[kMoveWarps][kMoves];  // rows, as if of head 0
+  __shared__ int64_t ends_s[kMoveThreads];  // rows that move, of the sequences up to this one
+  __shared__ int64_t sums_s[kMoveWarps];
+  __shared__ uint64_t bars[kMoveWarps];
+  __shared__ uint32_t abort_s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) abort_s = 0u;
+  typename std::conditional<kBulk, BulkMover, PieceMover<V>>::type mover;
+  if constexpr (kBulk) {
+    if (lane == 0) mbar_init(smem_u32(&bars[warp]), 1);
+    fence_mbar_init();
+    mover = BulkMover{smem_u32(buf_s) + warp * kMoveBuffer, smem_u32(&bars[warp]), 0u, &abort_s};
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    check_starts(p.starts, p.B, p.T, (int)threadIdx.x, kMoveThreads, &g_err_pages);
-  const int64_t b = blockIdx.x;
-  const int64_t s0 = p.starts[b], n = (int64_t)p.starts[b + 1] - s0, len = p.lens[b], last = n > 0 ? p.last[b] : -1;
-  const int64_t past = len - n;
-  const bool bad = s0 < 0 || n < 0 || s0 + n > p.T || past < 0 || len > p.max_pages * p.page || last < -1 ||
-                   last >= n || last >= 32 * p.words;
-  if (bad) {
-    if (threadIdx.x == 0) {
-      atomicOr(&g_err_pages, kErrIndex);
-      if (blockIdx.y == 0) p.lens_out[b] = (int32_t)len;
+  if (blockIdx.x == 0) check_starts(p.starts, p.B, p.T, (int)threadIdx.x, kMoveThreads, &g_err_pages);
+  const int64_t items = p.layers * p.Hkv;  // of keys, and as many of values
+
+  // ends_s of the sequences from b0 on; returns how many rows of theirs move
+  auto lay_out = [&](int64_t b0, bool tell) -> int64_t {
+    const int64_t b = b0 + threadIdx.x;
+    int64_t moves = 0;
+    if (b < p.B) {
+      const PathPlan x = path_plan(p, b);
+      int64_t count = 0, stay = 0;  // rows of the path, those of them that are in place
+      for (int w = 0; w < x.words; ++w) {
+        const uint32_t bits = path_word(x, w);
+        if (stay == w * 32) stay += bits == 0xffffffffu ? 32 : __ffs((int)~bits) - 1;
+        count += __popc(bits);
+      }
+      moves = count - stay;
+      if (tell) {
+        if (x.bad) atomicOr(&g_err_pages, kErrIndex);
+        p.lens_out[b] = x.bad ? p.lens[b] : (int32_t)(x.past + count);
+      }
     }
-    return;
-  }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t* row = p.seen + (s0 + (last < 0 ? 0 : last)) * p.words;
-  const int words = (int)(last >> 5) + 1;  // (none for -1)
-  // items: (layer, head) of keys and of values, the warps' shares alternate between the two
-  const int64_t items = p.layers * p.Hkv;
-  const int64_t i0 = items * blockIdx.y / gridDim.y, i1 = items * (blockIdx.y + 1) / gridDim.y;
-  const bool values = warp & 1;
-  const int64_t sub = warp >> 1, subs = kMoveThreads / 64;
-  const int64_t w0 = i0 + (i1 - i0) * sub / subs, w1 = i0 + (i1 - i0) * (sub + 1) / subs;
-  const uint32_t nv = values ? vv : kv;  // vectors of a row
-  V* const base = static_cast<V*>(values ? p.v : p.k);
-  const int64_t ld = (values ? p.ldv : p.ldk) / (int64_t)((values ? p.DV : p.DK) / nv);  // vectors between layers
-  // a batch is whole rows, as many as U vectors a lane hold; this lane's of them
-  constexpr int U = 8;
-  const uint32_t rows = 32 * U / nv;
-  uint32_t ru[U], cu[U];
+    int64_t incl = moves;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    ru[u] = (uint32_t)(u * 32 + lane) / nv;
-    cu[u] = (uint32_t)(u * 32 + lane) - ru[u] * nv;
-  }
-  int64_t taken = 0;  // rows of the path before the list
-  for (int word = 0; word < words;) {
-    // warp 0 lists the next rows that move, 32 candidates at a time
-    if (warp == 0) {
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    __syncthreads();
+    if (lane == 31) sums_s[warp] = incl;
+    __syncthreads();
+    int64_t base = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kMoveWarps; ++w) {
+      if (w < warp) base += sums_s[w];
+      all += sums_s[w];
+    }
+    ends_s[threadIdx.x] = base + incl;
+    __syncthreads();
+    return all;
+  };
+  int64_t total = 0;
+  for (int64_t b0 = 0; b0 < p.B; b0 += kMoveThreads) total += lay_out(b0, blockIdx.x == 0);
+
+  // this warp's piece of the line
+  const int64_t line = total * 2 * items, all_warps = (int64_t)gridDim.x * kMoveWarps;
+  const int64_t me = (int64_t)blockIdx.x * kMoveWarps + warp;
+  const int64_t q = ratio(line, all_warps), r = line - q * all_warps;
+  const int64_t p0 = q * me + ratio(r * me, all_warps), p1 = q * (me + 1) + ratio(r * (me + 1), all_warps);
+
+  // sequence b's items (keys', then values') whose place on the line (from a on, `moves` each) is in the piece
+  auto work = [&](int64_t b, int64_t a, int64_t moves) -> bool {
+    const int64_t x0 = p0 <= a ? 0 : ratio(p0 - a + moves - 1, moves), x1 = p1 <= a ? 0 : ratio(p1 - a + moves - 1, moves);
+    const int64_t i0 = x0, i1 = x1 < 2 * items ? x1 : 2 * items;
+    if (i0 >= i1) return true;
+    const PathPlan x = path_plan(p, b);
+    const int32_t* table = p.table + b * p.max_pages;
+    int64_t taken = 0;  // rows of the path before the list
+    for (int word = 0; word < x.words;) {
       int count = 0;
-      for (; word < words && count <= kMoves - 32; ++word) {
-        uint32_t bits = __ldg(row + word);
-        if (word == words - 1 && (last & 31) != 31) bits &= (2u << (last & 31)) - 1u;
-        const int64_t to = past + taken + __popc(bits & ((1u << lane) - 1u)), from = past + word * 32 + lane;
-        const bool moves = (bits >> lane & 1u) && to != from;
-        const uint32_t moving = __ballot_sync(0xffffffffu, moves);
-        if (moves) {
-          const int32_t a = p.table[b * p.max_pages + from / p.page], z = p.table[b * p.max_pages + to / p.page];
+      for (; word < x.words && count <= kMoves - 32; ++word) {
+        const uint32_t bits = path_word(x, word);
+        const int64_t to = x.past + taken + __popc(bits & ((1u << lane) - 1u)), from = x.past + word * 32 + lane;
+        const bool moves_now = (bits >> lane & 1u) && to != from;
+        const uint32_t moving = __ballot_sync(0xffffffffu, moves_now);
+        if (moves_now) {
+          const uint32_t page = (uint32_t)p.page, pa = (uint32_t)from / page, pz = (uint32_t)to / page;
+          const int32_t ta = table[pa], tz = table[pz];
           const int at = count + __popc(moving & ((1u << lane) - 1u));
-          const bool ok = a >= 0 && a < p.pages && z >= 0 && z < p.pages;
+          const bool ok = ta >= 0 && ta < p.pages && tz >= 0 && tz < p.pages;
           if (!ok) atomicOr(&g_err_pages, kErrIndex);  // (the row stays where it is)
-          from_s[at] = ok ? ((int64_t)a * p.Hkv) * p.page + from % p.page : -1;
-          to_s[at] = ok ? ((int64_t)z * p.Hkv) * p.page + to % p.page : -1;
+          from_s[warp][at] = ok ? (int64_t)ta * p.Hkv * p.page + ((uint32_t)from - pa * page) : -1;
+          to_s[warp][at] = ok ? (int64_t)tz * p.Hkv * p.page + ((uint32_t)to - pz * page) : -1;
         }
         count += __popc(moving);
         taken += __popc(bits);
       }
-      if (lane == 0) {
-        count_s = count;
-        next_s = word;
-      }
-    }
-    __syncthreads();
-    const uint32_t m = (uint32_t)count_s;
-    word = next_s;
-    if (m > 0) {
-      const uint32_t total = (uint32_t)(w1 - w0) * m;
-      for (uint32_t r0 = 0; r0 < total; r0 += rows) {
-        V v[U];
-        int64_t dst[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const uint32_t r = r0 + ru[u];
-          dst[u] = -1;
-          if (ru[u] < rows && r < total) {
-            const uint32_t item = (uint32_t)w0 + r / m, mv = r % m;
+      __syncwarp();
+      for (int kind = 0; kind < 2; ++kind) {
+        const int64_t k0 = i0 - kind * items > 0 ? i0 - kind * items : 0, k = i1 - kind * items, k1 = k < items ? k : items;
+        if (k0 >= k1 || count == 0) continue;
+        const uint32_t rb = (uint32_t)pc.row[kind] * sizeof(V), rows = (uint32_t)(k1 - k0) * count;
+        uint8_t* const base = static_cast<uint8_t*>(kind ? p.v : p.k);
+        const uint32_t step = (uint32_t)mover.most(rb);
+        // a lane a row, in order of (item, move)
+        for (uint32_t r0 = 0; r0 < rows; r0 += step) {
+          const uint32_t y = r0 + lane;
+          const uint8_t* src = nullptr;
+          uint8_t* dst = nullptr;
+          if (lane < (int)step && y < rows) {
+            const uint32_t it = y / (uint32_t)count, mv = y - it * count, item = (uint32_t)k0 + it;
             const uint32_t layer = item / (uint32_t)p.Hkv, head = item - layer * (uint32_t)p.Hkv;
-            const int64_t from = from_s[mv], at = layer * ld + (int64_t)head * p.page * nv + cu[u];
+            uint8_t* const at = base + (layer * pc.layer[kind] * (int64_t)sizeof(V) + (int64_t)head * p.page * rb);
+            const int64_t from = from_s[warp][mv];
             if (from >= 0) {
-              v[u] = base[at + from * nv];
-              dst[u] = at + to_s[mv] * nv;
+              src = at + from * rb;
+              dst = at + to_s[warp][mv] * rb;
             }
           }
+          if (!mover(src, dst, rb)) return false;
         }
-        __syncwarp();
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (dst[u] >= 0) base[dst[u]] = v[u];
-        __syncwarp();
+      }
+      __syncwarp();
+    }
+    return true;
+  };
+  int64_t before = 0;  // rows of the sequences before ends_s
+  bool ok = true;
+  for (int64_t b0 = 0; b0 < p.B; b0 += kMoveThreads) {
+    const int64_t here = p.B > kMoveThreads ? lay_out(b0, false) : total;
+    if (ok && p0 < p1 && p0 < (before + here) * 2 * items && p1 > before * 2 * items) {
+      // the first sequence that reaches into the piece, and on from there
+      int lo = 0, hi = kMoveThreads - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if ((before + ends_s[mid]) * 2 * items > p0) hi = mid; else lo = mid + 1;
+      }
+      for (int i = lo; ok && i < kMoveThreads && b0 + i < p.B; ++i) {
+        const int64_t first = i > 0 ? ends_s[i - 1] : 0, moves = ends_s[i] - first;
+        if ((before + first) * 2 * items >= p1) break;
+        if (moves > 0) ok = work(b0 + i, (before + first) * 2 * items, moves);
       }
     }
-    __syncthreads();
+    before += here;
   }
-  if (blockIdx.y == 0 && threadIdx.x == 0) p.lens_out[b] = (int32_t)(past + taken);
+  mover.finish();
 }
 
 // ------------------------------------------------------------------ pages
 //
-// Three kernels.  `release` drops and adds references as rows lose and gain
-// entries, `plan` (which alone sees all rows) settles who keeps a page that
-// several rows would go on writing, and hands out the free pages in order of
-// (row, entry), `fill` writes the table and copies what has to be copied.
+// Two kernels.  `plan`, one cluster of CTAs, drops and adds references as rows
+// lose and gain entries, settles who keeps a page that several rows would go on
+// writing, finds the free pages and hands them out in order of (row, entry): steps
+// that each need all of the one before, with the cluster's barrier between them.
+// Each CTA has a share of the rows and a share of the pages.  `copy` copies what has
+// to be copied.
 
-struct ReserveRow {
-  int first;   // the first entry that gets a fresh page
-  int rank;    // its place among all fresh ones
-};
 struct ReserveCopy {
   int from, rows;  // page, rows of it
   int rank;        // the fresh page's place
   int pad;
 };
+struct ReserveRow {
+  int first;  // the first entry that gets a fresh page
+  int rank;   // its place among all fresh ones
+  int copy;   // 1: that page is a copy
+  int kept;   // the page that it goes on writing and keeps, or -1
+};
+static_assert(sizeof(ReserveRow) == 16, "read as one piece");
+constexpr int kPlanCtas = 8;  // the largest cluster that every GPU runs
+constexpr int kPlanThreads = 1024;
 struct ReserveSpace {
   int32_t* carried;     // [B][max_pages], of rows that continue another one
   int32_t* free_pages;  // the free ones, lowest first
   ReserveRow* rows;     // [B]
   ReserveCopy* copies;  // [B]
-  int32_t* counts;      // free pages, copies
+  int64_t* totals;      // [kPlanCtas][3] fresh pages, copies, free pages of a CTA's share
+  int64_t* counts;      // free pages, copies
 };
 ReserveSpace reserve_space(const CacheProblem& p, size_t* bytes) {
   size_t at = 0;
@@ -244,7 +417,8 @@ ReserveSpace reserve_space(const CacheProblem& p, size_t* bytes) {
   ReserveSpace x;
   x.copies = reinterpret_cast<ReserveCopy*>(take((size_t)p.B * sizeof(ReserveCopy)));
   x.rows = reinterpret_cast<ReserveRow*>(take((size_t)p.B * sizeof(ReserveRow)));
-  x.counts = reinterpret_cast<int32_t*>(take(2 * sizeof(int32_t)));
+  x.totals = reinterpret_cast<int64_t*>(take(3 * kPlanCtas * sizeof(int64_t)));
+  x.counts = reinterpret_cast<int64_t*>(take(2 * sizeof(int64_t)));
   x.free_pages = reinterpret_cast<int32_t*>(take((size_t)p.pages * sizeof(int32_t)));
   x.carried = reinterpret_cast<int32_t*>(take((size_t)(p.B * p.max_pages) * sizeof(int32_t)));
   if (bytes) *bytes = at;
@@ -253,20 +427,19 @@ ReserveSpace reserve_space(const CacheProblem& p, size_t* bytes) {
 
 // What a row's numbers say.
 struct RowPlan {
-  int64_t source;   // the row it continues, -1: none
+  int source;       // the row it continues, -1: none
   int first, end;   // entries carried over, entries it will have
   int part;         // rows of its last carried page that it goes on behind, 0: it does not
-  bool bad;
 };
-FAB_DEV RowPlan row_plan(const CacheProblem& p, int64_t b) {
-  RowPlan r;
+FAB_DEV RowPlan row_plan(const CacheProblem& p, int64_t b, bool* bad) {
   const int64_t room = p.max_pages * p.page;
   int64_t src = p.source != nullptr ? p.source[b] : b, len = p.lens[b], kept = p.kept[b];
-  r.bad = src < -1 || src >= p.B || len < 0 || len > room || kept < 0 || kept > room;
+  *bad |= src < -1 || src >= p.B || len < 0 || len > room || kept < 0 || kept > room;
   if (src >= p.B || src < 0) src = -1;
   len = len < 0 ? 0 : len > room ? room : len;
   kept = src < 0 || kept < 0 ? 0 : kept > len ? len : kept;
-  r.source = src;
+  RowPlan r;
+  r.source = (int)src;
   r.first = (int)((kept + p.page - 1) / p.page);
   r.end = (int)((len + p.page - 1) / p.page);
   r.part = len > kept ? (int)(kept % p.page) : 0;
@@ -274,190 +447,277 @@ FAB_DEV RowPlan row_plan(const CacheProblem& p, int64_t b) {
 }
 FAB_DEV bool page_ok(const CacheProblem& p, int32_t page) { return page >= 0 && page < p.pages; }
 
-constexpr int kReserveThreads = 256;
-constexpr int kReserveSlots = 4 * kReserveThreads;  // entries of a row that a CTA looks at
-
-__global__ void __launch_bounds__(kReserveThreads) reserve_release_kernel(const CacheProblem p, const ReserveSpace ws,
-                                                                          int chunks) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t b = blockIdx.x / (unsigned)chunks;
-  const int64_t s0 = (int64_t)(blockIdx.x % (unsigned)chunks) * kReserveSlots;
-  const RowPlan r = row_plan(p, b);
-  bool bad = r.bad;
-  const int32_t* own = p.table + b * p.max_pages;
-  const int32_t* from = p.table + r.source * p.max_pages;
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int64_t s = s0 + u * kReserveThreads + (int)threadIdx.x;
-    if (s >= p.max_pages) break;
-    // (the page that the row goes on writing is dropped here, and settled by `plan`)
-    const bool stays = s < r.first && !(r.part > 0 && s == r.first - 1);
-    const int32_t had = own[s];
-    if (had >= p.pages) bad = true;
-    if (r.source == b) {
-      if (!stays && page_ok(p, had)) atomicSub(p.refs + had, 1);
-      if (s < r.first && !page_ok(p, had)) bad = true;
-    } else {
-      if (page_ok(p, had)) atomicSub(p.refs + had, 1);
-      if (s < r.first) {
-        const int32_t page = from[s];
-        ws.carried[b * p.max_pages + s] = page_ok(p, page) ? page : -1;
-        if (!page_ok(p, page))
-          bad = true;
-        else if (stays)
-          atomicAdd(p.refs + page, 1);
-      }
-    }
-  }
-  if (bad) atomicOr(&g_err_pages, kErrIndex);
-}
-
-constexpr int kPlanThreads = 1024;
-
 // Sum over the block of one value a thread, and what the threads before this one
 // add up to.
-FAB_DEV int64_t block_scan(int64_t v, int64_t* before, int64_t* sums) {
+FAB_DEV int block_scan(int v, int* before, int* sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t incl = v;
+  int incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+    const int up = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += up;
   }
   __syncthreads();
   if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  int64_t base = 0, all = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w < warp) base += sums[w];
-    all += sums[w];
+  int of_warps = sums[lane];  // (32 warps: each sums them up by itself)
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, of_warps, o);
+    if (lane >= o) of_warps += up;
   }
-  *before = base + incl - v;
-  return all;
+  const int base = __shfl_sync(0xffffffffu, of_warps, warp > 0 ? warp - 1 : 0);
+  *before = (warp > 0 ? base : 0) + incl - v;
+  return __shfl_sync(0xffffffffu, of_warps, 31);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const CacheProblem p, const ReserveSpace ws) {
-  __shared__ int64_t sums[kPlanThreads / 32];
+constexpr int kPlanRows = 1024;        // rows of a CTA's share held in shared memory at once
+constexpr int kPlanSlots = 128;        // entries that a warp looks at
+constexpr int kPlanPages = 16 * kPlanThreads;  // pages that a CTA looks at at once
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
+    reserve_plan_kernel(const CacheProblem p, const ReserveSpace ws) {
+  static_assert(kPlanThreads == 1024, "block_scan is for 32 warps");
+  __shared__ RowPlan rows_s[kPlanRows];
+  __shared__ int sums[32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // the page that row b goes on writing, or -1
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = (int)blockIdx.x;
+  const int64_t b0 = p.B * cta / kPlanCtas, b1 = p.B * (cta + 1) / kPlanCtas;
+  const int segs = (int)((p.max_pages + kPlanSlots - 1) / kPlanSlots);  // of a row, a warp each
+  bool bad = false;
+  int held = -1;  // rows_s holds this part of the share
+  // calls f(count of rows in rows_s, the first of them) for each part of the share
+  auto each_part = [&](auto f) {
+    int part = 0;
+    for (int64_t r0 = b0; r0 < b1; r0 += kPlanRows, ++part) {
+      const int n = (int)(b1 - r0 < kPlanRows ? b1 - r0 : kPlanRows);
+      if (held != part) {
+        __syncthreads();
+        if ((int)threadIdx.x < n) rows_s[threadIdx.x] = row_plan(p, r0 + threadIdx.x, &bad);
+        __syncthreads();
+        held = part;
+      }
+      f(n, r0);
+    }
+  };
+  // the page that a row goes on writing, or -1
   auto wanted = [&](const RowPlan& r) -> int32_t {
     if (r.part == 0) return -1;
     const int32_t page = p.table[r.source * p.max_pages + r.first - 1];
     return page_ok(p, page) ? page : -1;
   };
-  // Of the rows that would go on writing a page which no other row holds (its
-  // references have all been dropped) the first keeps it.
-  for (int64_t b = threadIdx.x; b < p.B; b += kPlanThreads) {
-    const int32_t page = wanted(row_plan(p, b));
-    if (page >= 0 && __ldcg(p.refs + page) <= 0) atomicMin(p.refs + page, INT_MIN + (int)b);
-  }
-  __syncthreads();
-  int64_t need = 0, copies = 0;  // of the rows before
-  for (int64_t b0 = 0; b0 < p.B; b0 += kPlanThreads) {
-    const int64_t b = b0 + threadIdx.x;
-    RowPlan r{-1, 0, 0, 0, false};
-    int32_t page = -1;
-    bool keeps = false;
-    if (b < p.B) {
-      r = row_plan(p, b);
-      page = wanted(r);
-      keeps = page >= 0 && __ldcg(p.refs + page) == INT_MIN + (int)b;
-    }
-    // (a row whose page is not there gets a fresh one, and nothing is copied)
-    const int first = r.first - (r.part > 0 && !keeps ? 1 : 0);
-    const bool copy = page >= 0 && !keeps;
-    int64_t before, at;
-    const int64_t all = block_scan(r.end - first, &before, sums);
-    const int64_t many = block_scan(copy ? 1 : 0, &at, sums);
-    if (b < p.B) ws.rows[b] = ReserveRow{first, (int)(need + before)};
-    if (copy) ws.copies[copies + at] = ReserveCopy{page, r.part, (int)(need + before), 0};
-    need += all;
-    copies += many;
-  }
-  __syncthreads();
-  for (int64_t b = threadIdx.x; b < p.B; b += kPlanThreads) {
-    const int32_t page = wanted(row_plan(p, b));
-    if (page >= 0 && __ldcg(p.refs + page) == INT_MIN + (int)b) __stcg(p.refs + page, 1);
-  }
-  __syncthreads();
-  // the free pages, in order
-  int64_t free = 0;
-  bool bad = false;
-  for (int64_t x0 = 0; x0 < p.pages; x0 += 4 * kPlanThreads) {
-    const int64_t x = x0 + threadIdx.x * 4;
-    uint32_t is = 0;
+  // 1. Entries that go and come.  (A page that a row goes on writing is dropped.)
+  each_part([&](int n, int64_t r0) {
+    for (int x = warp; x < n * segs; x += kPlanThreads / 32) {
+      const int i = x / segs;
+      const int64_t b = r0 + i;
+      const RowPlan r = rows_s[i];
+      const int32_t* own = p.table + b * p.max_pages;
+      const int32_t* from = p.table + (int64_t)(r.source < 0 ? 0 : r.source) * p.max_pages;
+      const int64_t s0 = (int64_t)(x - i * segs) * kPlanSlots + lane;
+      int32_t had[4], get[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int32_t held = x + u < p.pages ? __ldcg(p.refs + x + u) : 1;
-      if (held == 0) is |= 1u << u;
-      bad |= held < 0;  // (more entries named it than its references say)
-    }
-    int64_t before;
-    const int64_t all = block_scan(__popc(is), &before, sums);
-    int64_t at = free + before;
+      for (int u = 0; u < 4; ++u) {
+        const int64_t s = s0 + u * 32;
+        had[u] = s < p.max_pages ? own[s] : -1;
+        get[u] = r.source != b && s < r.first ? from[s] : -1;
+      }
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (is >> u & 1u) ws.free_pages[at++] = (int32_t)(x + u);
-    free += all;
-  }
-  if (bad) atomicOr(&g_err_pages, kErrIndex);
-  if (threadIdx.x == 0) {
-    ws.counts[0] = (int32_t)free;
-    ws.counts[1] = (int32_t)copies;
-    const int64_t left = free - need;
-    *p.spare = (int32_t)(left < INT_MIN ? INT_MIN : left);
-  }
-}
-
-// Blocks below `table_blocks` write the table, the others copy.
-template <typename V>
-__global__ void __launch_bounds__(kReserveThreads) reserve_fill_kernel(const CacheProblem p, const ReserveSpace ws,
-                                                                       int chunks, int64_t table_blocks, int kv, int vv) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int32_t free = ws.counts[0];
-  if (blockIdx.x < table_blocks) {
-    const int64_t b = blockIdx.x / (unsigned)chunks;
-    const int64_t s0 = (int64_t)(blockIdx.x % (unsigned)chunks) * kReserveSlots;
-    const RowPlan r = row_plan(p, b);
-    const ReserveRow x = ws.rows[b];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t s = s0 + u * kReserveThreads + (int)threadIdx.x;
-      if (s >= p.max_pages) break;
-      int32_t* entry = p.table + b * p.max_pages + s;
-      if (s < x.first) {
-        if (r.source != b) *entry = ws.carried[b * p.max_pages + s];
-      } else if (s < r.end) {
-        const int64_t rank = (int64_t)x.rank + (s - x.first);
-        const int32_t page = rank < free ? ws.free_pages[rank] : -1;
-        *entry = page;
-        if (page >= 0) p.refs[page] = 1;
-      } else {
-        *entry = -1;
+      for (int u = 0; u < 4; ++u) {
+        const int64_t s = s0 + u * 32;
+        const bool carried = s < r.first, stays = carried && !(r.part > 0 && s == r.first - 1);
+        if (had[u] >= p.pages) bad = true;
+        if (r.source == b) {
+          if (!stays && page_ok(p, had[u])) atomicSub(p.refs + had[u], 1);
+          if (carried && had[u] < 0) bad = true;
+        } else {
+          if (page_ok(p, had[u])) atomicSub(p.refs + had[u], 1);
+          if (carried) {
+            const bool ok = page_ok(p, get[u]);
+            ws.carried[b * p.max_pages + s] = ok ? get[u] : -1;
+            if (!ok)
+              bad = true;
+            else if (stays)
+              atomicAdd(p.refs + get[u], 1);
+          }
+        }
       }
     }
-    return;
+  });
+  cluster_sync();
+  // 2. Of the rows that would go on writing a page which no other row holds (its
+  // references have all been dropped) the first keeps it: the lowest mark stays.
+  each_part([&](int n, int64_t r0) {
+    if ((int)threadIdx.x < n) {
+      const int32_t page = wanted(rows_s[threadIdx.x]);
+      if (page >= 0 && __ldcg(p.refs + page) <= 0) atomicMin(p.refs + page, INT_MIN + (int)(r0 + threadIdx.x));
+    }
+  });
+  cluster_sync();
+  // 3. The share's fresh pages and copies, and how many pages of the other share are free.
+  int64_t need = 0, copies = 0, free = 0;
+  auto keeps = [&](int32_t page, int64_t b) { return page >= 0 && __ldcg(p.refs + page) == INT_MIN + (int)b; };
+  each_part([&](int n, int64_t r0) {
+    int fresh = 0, copy = 0;
+    if ((int)threadIdx.x < n) {
+      const RowPlan r = rows_s[threadIdx.x];
+      const int32_t page = wanted(r);
+      const bool own = keeps(page, r0 + threadIdx.x);
+      // (a row whose page is not there gets a fresh one, and nothing is copied)
+      fresh = r.end - r.first + (r.part > 0 && !own ? 1 : 0);
+      copy = page >= 0 && !own ? 1 : 0;
+    }
+    int before;
+    need += block_scan(fresh, &before, sums);
+    copies += __syncthreads_count(copy);
+  });
+  const int64_t g0 = (p.pages + 3) / 4 * cta / kPlanCtas * 4;
+  const int64_t g = (p.pages + 3) / 4 * (cta + 1) / kPlanCtas * 4, g1 = g < p.pages ? g : p.pages;
+  // Of the 128 pages from x on: bit u of this lane's says that page x + 4 lane + u is free.
+  auto look = [&](int64_t x) -> uint32_t {
+    x += lane * 4;
+    int4 v = make_int4(1, 1, 1, 1);
+    if (x + 4 <= g1) {
+      v = __ldcg(reinterpret_cast<const int4*>(p.refs + x));
+    } else {
+      if (x < g1) v.x = __ldcg(p.refs + x);
+      if (x + 1 < g1) v.y = __ldcg(p.refs + x + 1);
+      if (x + 2 < g1) v.z = __ldcg(p.refs + x + 2);
+    }
+    auto odd = [](int32_t c) { return c < 0 && c > INT_MIN / 2; };  // (more entries named it than its references say)
+    if (odd(v.x) || odd(v.y) || odd(v.z) || odd(v.w)) bad = true;
+    return (v.x == 0 ? 1u : 0u) | (v.y == 0 ? 2u : 0u) | (v.z == 0 ? 4u : 0u) | (v.w == 0 ? 8u : 0u);
+  };
+  uint32_t mine = 0;  // the last part's bits of this thread
+  for (int64_t x0 = g0; x0 < g1; x0 += kPlanPages) {
+    mine = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mine |= look(x0 + warp * 512 + k * 128) << (4 * k);
+    int before;
+    free += block_scan(__popc(mine), &before, sums);
   }
-  // units: (copy, layer, keys or values, head), a warp each
+  if (threadIdx.x == 0) {
+    ws.totals[3 * cta] = need;
+    ws.totals[3 * cta + 1] = copies;
+    ws.totals[3 * cta + 2] = free;
+  }
+  cluster_sync();
+  // 4. Ranks of the rows, the list of the free pages.
+  int64_t need0 = 0, copies0 = 0, free0 = 0, all_need = 0, all_copies = 0, all_free = 0;
+  for (int c = 0; c < kPlanCtas; ++c) {
+    const int64_t x = __ldcg(ws.totals + 3 * c), y = __ldcg(ws.totals + 3 * c + 1), z = __ldcg(ws.totals + 3 * c + 2);
+    if (c < cta) need0 += x, copies0 += y, free0 += z;
+    all_need += x, all_copies += y, all_free += z;
+  }
+  each_part([&](int n, int64_t r0) {
+    int fresh = 0;
+    RowPlan r{-1, 0, 0, 0};
+    int32_t page = -1;
+    bool own = false;
+    if ((int)threadIdx.x < n) {
+      r = rows_s[threadIdx.x];
+      page = wanted(r);
+      own = keeps(page, r0 + threadIdx.x);
+      fresh = r.end - r.first + (r.part > 0 && !own ? 1 : 0);
+    }
+    const bool copy = page >= 0 && !own;
+    int before, at;
+    const int all = block_scan(fresh, &before, sums), many = block_scan(copy ? 1 : 0, &at, sums);
+    if ((int)threadIdx.x < n)
+      ws.rows[r0 + threadIdx.x] = ReserveRow{r.end - fresh, (int)(need0 + before), copy ? 1 : 0, own ? page : -1};
+    if (copy) ws.copies[copies0 + at] = ReserveCopy{page, r.part, (int)(need0 + before), 0};
+    need0 += all;
+    copies0 += many;
+  });
+  const bool again = g1 - g0 > kPlanPages;  // (the bits of more than one part are looked at again)
+  for (int64_t x0 = g0; x0 < g1 && free0 < all_need; x0 += kPlanPages) {
+    if (again) {
+      mine = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mine |= look(x0 + warp * 512 + k * 128) << (4 * k);
+    }
+    // in order of page: the warp's four pieces of 128, in each the lanes in turn
+    int before;
+    const int of_part = block_scan(__popc(mine), &before, sums);
+    int64_t at = free0 + __shfl_sync(0xffffffffu, before, 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t bits = mine >> (4 * k) & 15u;
+      int ahead = 0, of_piece = 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t m = __ballot_sync(0xffffffffu, bits >> u & 1u);
+        ahead += __popc(m & ((1u << lane) - 1u));
+        of_piece += __popc(m);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (bits >> u & 1u) {
+          if (at + ahead < all_need) ws.free_pages[at + ahead] = (int32_t)(x0 + warp * 512 + k * 128 + lane * 4 + u);
+          ++ahead;
+        }
+      at += of_piece;
+    }
+    free0 += of_part;
+  }
+  if (cta == 0 && threadIdx.x == 0) {
+    ws.counts[0] = all_free;
+    ws.counts[1] = all_copies;
+    const int64_t left = all_free - all_need;
+    *p.spare = (int32_t)(left < INT_MIN ? INT_MIN : left);
+  }
+  cluster_sync();
+  // 5. The table, and the references of what was handed out and kept.
+  each_part([&](int n, int64_t r0) {
+    for (int x = warp; x < n * segs; x += kPlanThreads / 32) {
+      const int i = x / segs;
+      const int64_t b = r0 + i;
+      const RowPlan r = rows_s[i];
+      const int4 y = __ldcg(reinterpret_cast<const int4*>(ws.rows + b));
+      const int64_t s0 = (int64_t)(x - i * segs) * kPlanSlots + lane;
+      if (s0 == 0 && y.w >= 0) p.refs[y.w] = 1;
+      int32_t* row = p.table + b * p.max_pages;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t s = s0 + u * 32;
+        if (s >= p.max_pages) break;
+        if (s < y.x) {
+          if (r.source != b) row[s] = __ldcg(ws.carried + b * p.max_pages + s);
+        } else if (s < r.end) {
+          const int64_t rank = (int64_t)y.y + (s - y.x);
+          const int32_t page = rank < all_free ? __ldcg(ws.free_pages + rank) : -1;
+          row[s] = page;
+          if (page >= 0) p.refs[page] = 1;
+        } else {
+          row[s] = -1;
+        }
+      }
+    }
+  });
+  if (bad) atomicOr(&g_err_pages, kErrIndex);
+}
+
+constexpr int kCopyThreads = 256;
+
+// Units: (copy, layer, keys or values, head), a warp each.
+template <typename V>
+__global__ void __launch_bounds__(kCopyThreads) reserve_copy_kernel(const CacheProblem p, const ReserveSpace ws,
+                                                                    const Pieces pc) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t free = ws.counts[0];
   const int lane = threadIdx.x & 31;
   const int64_t per = p.layers * 2 * p.Hkv, units = ws.counts[1] * per;
-  const int64_t warps = (int64_t)(gridDim.x - table_blocks) * (kReserveThreads / 32);
-  for (int64_t x = (int64_t)(blockIdx.x - table_blocks) * (kReserveThreads / 32) + (threadIdx.x >> 5); x < units;
-       x += warps) {
-    const int64_t c = x / per;
-    int64_t y = x - c * per;
-    const int64_t layer = y / (2 * p.Hkv);
-    y -= layer * 2 * p.Hkv;
-    const bool values = y >= p.Hkv;
-    const int64_t head = values ? y - p.Hkv : y;
+  const int64_t warps = (int64_t)gridDim.x * (kCopyThreads / 32);
+  for (int64_t x = (int64_t)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); x < units; x += warps) {
+    const int64_t c = ratio(x, per);
+    const int y = (int)(x - c * per), hkv = (int)p.Hkv, layer = y / (2 * hkv), z = y - layer * 2 * hkv;
+    const int kind = z >= hkv ? 1 : 0, head = z - kind * hkv;
     const ReserveCopy copy = ws.copies[c];
     if (copy.rank >= free) continue;
-    const int nv = values ? vv : kv;
-    const int64_t ld = (values ? p.ldv : p.ldk) / (int64_t)((values ? p.DV : p.DK) / nv);
-    V* const base = static_cast<V*>(values ? p.v : p.k) + layer * ld;
+    const int nv = pc.row[kind];
+    V* const base = static_cast<V*>(kind ? p.v : p.k) + layer * pc.layer[kind];
     const V* src = base + ((int64_t)copy.from * p.Hkv + head) * p.page * nv;
     V* dst = base + ((int64_t)ws.free_pages[copy.rank] * p.Hkv + head) * p.page * nv;
     const int64_t count = (int64_t)copy.rows * nv;
@@ -472,13 +732,6 @@ __global__ void __launch_bounds__(kReserveThreads) reserve_fill_kernel(const Cac
         if (i0 + u * 32 < count) dst[i0 + u * 32] = v[u];
     }
   }
-}
-
-// Bytes of the pieces in which rows of a cache are moved: 16 where every row
-// of every layer starts at 16 bytes, else an element.
-int piece_bytes(const CacheProblem& p, int64_t e) {
-  const bool whole = p.DK * e % 16 == 0 && p.DV * e % 16 == 0 && p.ldk * e % 16 == 0 && p.ldv * e % 16 == 0;
-  return whole ? 16 : (int)e;
 }
 
 }  // namespace
@@ -497,17 +750,20 @@ cudaError_t launch_draft_tree(const int32_t* starts, const int32_t* parents, int
 }
 
 cudaError_t launch_paged_accept(const CacheProblem& p, cudaStream_t s) {
-  const int64_t items = p.layers * p.Hkv;
-  // CTAs of a sequence: about eight an SM in all, four items at least to a CTA
-  int64_t per = (1216 + p.B - 1) / p.B;
-  if (per > (items + 3) / 4) per = (items + 3) / 4;
-  if (per > 65535) per = 65535;
-  const dim3 grid((unsigned)p.B, (unsigned)per);
-  const int64_t e = p.dtype == FAB_F32 ? 4 : 2;
-  const int piece = piece_bytes(p, e), kv = (int)(p.DK * e / piece), vv = (int)(p.DV * e / piece);
-  if (piece == 16) return launch_early(paged_accept_kernel<uint4>, grid, kMoveThreads, 0, s, p, kv, vv);
-  if (piece == 4) return launch_early(paged_accept_kernel<uint32_t>, grid, kMoveThreads, 0, s, p, kv, vv);
-  return launch_early(paged_accept_kernel<uint16_t>, grid, kMoveThreads, 0, s, p, kv, vv);
+  // as many CTAs as run at once, at most one for every eight items
+  const int64_t items = p.B * 2 * p.layers * p.Hkv, most = kMoveCtas * 152;
+  const int64_t ctas = (items + kMoveWarps - 1) / kMoveWarps;
+  const dim3 grid((unsigned)(ctas < most ? ctas : most));
+  const Pieces pc = pieces_of(p);
+  if (pc.bytes == 16) {
+    constexpr int smem = kMoveWarps * kMoveBuffer;
+    const cudaError_t err =
+        cudaFuncSetAttribute(paged_accept_kernel<uint4>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    return launch_early(paged_accept_kernel<uint4>, grid, kMoveThreads, smem, s, p, pc);
+  }
+  if (pc.bytes == 4) return launch_early(paged_accept_kernel<uint32_t>, grid, kMoveThreads, 0, s, p, pc);
+  return launch_early(paged_accept_kernel<uint16_t>, grid, kMoveThreads, 0, s, p, pc);
 }
 
 size_t paged_reserve_workspace_bytes(const CacheProblem& p) {
@@ -518,22 +774,15 @@ size_t paged_reserve_workspace_bytes(const CacheProblem& p) {
 
 cudaError_t launch_paged_reserve(const CacheProblem& p, cudaStream_t s) {
   const ReserveSpace ws = reserve_space(p, nullptr);
-  const int chunks = (int)((p.max_pages + kReserveSlots - 1) / kReserveSlots);
-  const int64_t table_blocks = p.B * chunks;
-  cudaError_t err = launch_early(reserve_release_kernel, dim3((unsigned)table_blocks), kReserveThreads, 0, s, p, ws, chunks);
+  const cudaError_t err = launch_early(reserve_plan_kernel, dim3(kPlanCtas), kPlanThreads, 0, s, p, ws);
   if (err != cudaSuccess) return err;
-  err = launch_early(reserve_plan_kernel, dim3(1), kPlanThreads, 0, s, p, ws);
-  if (err != cudaSuccess) return err;
-  const int64_t e = p.dtype == FAB_F32 ? 4 : 2;
-  const int piece = piece_bytes(p, e), kv = (int)(p.DK * e / piece), vv = (int)(p.DV * e / piece);
+  const Pieces pc = pieces_of(p);
   const int64_t warps = p.B * p.layers * 2 * p.Hkv;  // units of copying, at most
-  const int64_t blocks = (warps + kReserveThreads / 32 - 1) / (kReserveThreads / 32);
-  const dim3 grid((unsigned)(table_blocks + (blocks < 1216 ? blocks : 1216)));
-  if (piece == 16)
-    return launch_early(reserve_fill_kernel<uint4>, grid, kReserveThreads, 0, s, p, ws, chunks, table_blocks, kv, vv);
-  if (piece == 4)
-    return launch_early(reserve_fill_kernel<uint32_t>, grid, kReserveThreads, 0, s, p, ws, chunks, table_blocks, kv, vv);
-  return launch_early(reserve_fill_kernel<uint16_t>, grid, kReserveThreads, 0, s, p, ws, chunks, table_blocks, kv, vv);
+  const int64_t blocks = (warps + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
+  const dim3 grid((unsigned)(blocks < 1216 ? blocks : 1216));
+  if (pc.bytes == 16) return launch_early(reserve_copy_kernel<uint4>, grid, kCopyThreads, 0, s, p, ws, pc);
+  if (pc.bytes == 4) return launch_early(reserve_copy_kernel<uint32_t>, grid, kCopyThreads, 0, s, p, ws, pc);
+  return launch_early(reserve_copy_kernel<uint16_t>, grid, kCopyThreads, 0, s, p, ws, pc);
 }
 
 uint32_t take_error_pages() {
