@@ -513,6 +513,16 @@ FAB_DEV void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The address, for the whole cluster, of another CTA's counterpart of a shared-memory address.
+FAB_DEV uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+  uint32_t out;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(out) : "r"(addr), "r"(rank));
+  return out;
+}
+FAB_DEV void st_cluster(uint32_t addr, int64_t v) {
+  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
 // Sets kErrIndex in *err unless starts[0 .. B] ascends from 0 to at most T;
 // `count` threads share the work, this one is `rank`.
 FAB_DEV void check_starts(const int32_t* starts, int64_t B, int64_t T, int rank, int count, uint32_t* err) {

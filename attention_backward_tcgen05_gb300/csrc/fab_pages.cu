@@ -2,6 +2,7 @@
 // in a drafted tree, keeping the accepted path's rows, and which sequence
 // holds which page (forked, grown, cut, freed, copied before it is written).
 #include <limits.h>
+#include <stddef.h>
 
 #include <type_traits>
 
@@ -399,12 +400,15 @@ struct ReserveRow {
 static_assert(sizeof(ReserveRow) == 16, "read as one piece");
 constexpr int kPlanCtas = 8;  // the largest cluster that every GPU runs
 constexpr int kPlanThreads = 1024;
+// What the shares of a CTA come to.
+struct PlanTotals {
+  int64_t need, copies, free;  // fresh pages and copies of its rows, free ones of its pages
+};
 struct ReserveSpace {
   int32_t* carried;     // [B][max_pages], of rows that continue another one
   int32_t* free_pages;  // the free ones, lowest first
   ReserveRow* rows;     // [B]
   ReserveCopy* copies;  // [B]
-  int64_t* totals;      // [kPlanCtas][3] fresh pages, copies, free pages of a CTA's share
   int64_t* counts;      // free pages, copies
 };
 ReserveSpace reserve_space(const CacheProblem& p, size_t* bytes) {
@@ -417,7 +421,6 @@ ReserveSpace reserve_space(const CacheProblem& p, size_t* bytes) {
   ReserveSpace x;
   x.copies = reinterpret_cast<ReserveCopy*>(take((size_t)p.B * sizeof(ReserveCopy)));
   x.rows = reinterpret_cast<ReserveRow*>(take((size_t)p.B * sizeof(ReserveRow)));
-  x.totals = reinterpret_cast<int64_t*>(take(3 * kPlanCtas * sizeof(int64_t)));
   x.counts = reinterpret_cast<int64_t*>(take(2 * sizeof(int64_t)));
   x.free_pages = reinterpret_cast<int32_t*>(take((size_t)p.pages * sizeof(int32_t)));
   x.carried = reinterpret_cast<int32_t*>(take((size_t)(p.B * p.max_pages) * sizeof(int32_t)));
@@ -440,9 +443,10 @@ FAB_DEV RowPlan row_plan(const CacheProblem& p, int64_t b, bool* bad) {
   kept = src < 0 || kept < 0 ? 0 : kept > len ? len : kept;
   RowPlan r;
   r.source = (int)src;
-  r.first = (int)((kept + p.page - 1) / p.page);
-  r.end = (int)((len + p.page - 1) / p.page);
-  r.part = len > kept ? (int)(kept % p.page) : 0;
+  const uint32_t page = (uint32_t)p.page, k = (uint32_t)kept, n = (uint32_t)len;  // (below 2^31, all three)
+  r.first = (int)((k + page - 1) / page);
+  r.end = (int)((n + page - 1) / page);
+  r.part = len > kept ? (int)(k % page) : 0;
   return r;
 }
 FAB_DEV bool page_ok(const CacheProblem& p, int32_t page) { return page >= 0 && page < p.pages; }
@@ -471,6 +475,15 @@ FAB_DEV int block_scan(int v, int* before, int* sums) {
   return __shfl_sync(0xffffffffu, of_warps, 31);
 }
 
+// The sum alone.
+FAB_DEV int block_sum(int v, int* sums) {
+  v = __reduce_add_sync(0xffffffffu, v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return __reduce_add_sync(0xffffffffu, sums[threadIdx.x & 31]);
+}
+
 constexpr int kPlanRows = 1024;        // rows of a CTA's share held in shared memory at once
 constexpr int kPlanSlots = 128;        // entries that a warp looks at
 constexpr int kPlanPages = 16 * kPlanThreads;  // pages that a CTA looks at at once
@@ -479,6 +492,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     reserve_plan_kernel(const CacheProblem p, const ReserveSpace ws) {
   static_assert(kPlanThreads == 1024, "block_scan is for 32 warps");
   __shared__ RowPlan rows_s[kPlanRows];
+  __shared__ PlanTotals totals_s[kPlanCtas];
   __shared__ int sums[32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -501,26 +515,32 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
       f(n, r0);
     }
   };
-  // the page that a row goes on writing, or -1
+  // What a thread knows of its row (of a share of more rows than threads: of the last part).
+  int32_t page = -1;   // the page that the row goes on writing, -1: none
+  bool own = false;    // and keeps
+  // the same for a row of another part
   auto wanted = [&](const RowPlan& r) -> int32_t {
     if (r.part == 0) return -1;
-    const int32_t page = p.table[r.source * p.max_pages + r.first - 1];
-    return page_ok(p, page) ? page : -1;
+    const int32_t x = p.table[(int64_t)r.source * p.max_pages + r.first - 1];
+    return page_ok(p, x) ? x : -1;
   };
+  auto keeps = [&](int32_t x, int64_t b) { return x >= 0 && __ldcg(p.refs + x) == INT_MIN + (int)b; };
+  const bool parts = b1 - b0 > kPlanRows;
   // 1. Entries that go and come.  (A page that a row goes on writing is dropped.)
   each_part([&](int n, int64_t r0) {
+    if ((int)threadIdx.x < n) page = wanted(rows_s[threadIdx.x]);
     for (int x = warp; x < n * segs; x += kPlanThreads / 32) {
       const int i = x / segs;
       const int64_t b = r0 + i;
       const RowPlan r = rows_s[i];
-      const int32_t* own = p.table + b * p.max_pages;
+      const int32_t* row = p.table + b * p.max_pages;
       const int32_t* from = p.table + (int64_t)(r.source < 0 ? 0 : r.source) * p.max_pages;
       const int64_t s0 = (int64_t)(x - i * segs) * kPlanSlots + lane;
       int32_t had[4], get[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int64_t s = s0 + u * 32;
-        had[u] = s < p.max_pages ? own[s] : -1;
+        had[u] = s < p.max_pages ? row[s] : -1;
         get[u] = r.source != b && s < r.first ? from[s] : -1;
       }
 #pragma unroll
@@ -549,79 +569,86 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   // 2. Of the rows that would go on writing a page which no other row holds (its
   // references have all been dropped) the first keeps it: the lowest mark stays.
   each_part([&](int n, int64_t r0) {
-    if ((int)threadIdx.x < n) {
-      const int32_t page = wanted(rows_s[threadIdx.x]);
-      if (page >= 0 && __ldcg(p.refs + page) <= 0) atomicMin(p.refs + page, INT_MIN + (int)(r0 + threadIdx.x));
-    }
+    if ((int)threadIdx.x >= n) return;
+    if (parts) page = wanted(rows_s[threadIdx.x]);
+    if (page >= 0 && __ldcg(p.refs + page) <= 0) atomicMin(p.refs + page, INT_MIN + (int)(r0 + threadIdx.x));
   });
   cluster_sync();
-  // 3. The share's fresh pages and copies, and how many pages of the other share are free.
-  int64_t need = 0, copies = 0, free = 0;
-  auto keeps = [&](int32_t page, int64_t b) { return page >= 0 && __ldcg(p.refs + page) == INT_MIN + (int)b; };
-  each_part([&](int n, int64_t r0) {
-    int fresh = 0, copy = 0;
-    if ((int)threadIdx.x < n) {
-      const RowPlan r = rows_s[threadIdx.x];
-      const int32_t page = wanted(r);
-      const bool own = keeps(page, r0 + threadIdx.x);
-      // (a row whose page is not there gets a fresh one, and nothing is copied)
-      fresh = r.end - r.first + (r.part > 0 && !own ? 1 : 0);
-      copy = page >= 0 && !own ? 1 : 0;
-    }
-    int before;
-    need += block_scan(fresh, &before, sums);
-    copies += __syncthreads_count(copy);
-  });
+  // 3. How many pages of the CTA's share are free, the fresh pages and copies of its rows.
   const int64_t g0 = (p.pages + 3) / 4 * cta / kPlanCtas * 4;
   const int64_t g = (p.pages + 3) / 4 * (cta + 1) / kPlanCtas * 4, g1 = g < p.pages ? g : p.pages;
-  // Of the 128 pages from x on: bit u of this lane's says that page x + 4 lane + u is free.
+  // Of the 512 pages from x on that a warp looks at, 128 at a time: bit 4 k + u of
+  // this lane's says that page x + 128 k + 4 lane + u is free.
   auto look = [&](int64_t x) -> uint32_t {
-    x += lane * 4;
-    int4 v = make_int4(1, 1, 1, 1);
-    if (x + 4 <= g1) {
-      v = __ldcg(reinterpret_cast<const int4*>(p.refs + x));
-    } else {
-      if (x < g1) v.x = __ldcg(p.refs + x);
-      if (x + 1 < g1) v.y = __ldcg(p.refs + x + 1);
-      if (x + 2 < g1) v.z = __ldcg(p.refs + x + 2);
+    int4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t at = x + k * 128 + lane * 4;
+      v[k] = make_int4(1, 1, 1, 1);
+      if (at + 4 <= g1) {
+        v[k] = __ldcg(reinterpret_cast<const int4*>(p.refs + at));
+      } else {
+        if (at < g1) v[k].x = __ldcg(p.refs + at);
+        if (at + 1 < g1) v[k].y = __ldcg(p.refs + at + 1);
+        if (at + 2 < g1) v[k].z = __ldcg(p.refs + at + 2);
+      }
     }
     auto odd = [](int32_t c) { return c < 0 && c > INT_MIN / 2; };  // (more entries named it than its references say)
-    if (odd(v.x) || odd(v.y) || odd(v.z) || odd(v.w)) bad = true;
-    return (v.x == 0 ? 1u : 0u) | (v.y == 0 ? 2u : 0u) | (v.z == 0 ? 4u : 0u) | (v.w == 0 ? 8u : 0u);
-  };
-  uint32_t mine = 0;  // the last part's bits of this thread
-  for (int64_t x0 = g0; x0 < g1; x0 += kPlanPages) {
-    mine = 0;
+    uint32_t bits = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) mine |= look(x0 + warp * 512 + k * 128) << (4 * k);
-    int before;
-    free += block_scan(__popc(mine), &before, sums);
+    for (int k = 0; k < 4; ++k) {
+      if (odd(v[k].x) || odd(v[k].y) || odd(v[k].z) || odd(v[k].w)) bad = true;
+      bits |= ((v[k].x == 0 ? 1u : 0u) | (v[k].y == 0 ? 2u : 0u) | (v[k].z == 0 ? 4u : 0u) | (v[k].w == 0 ? 8u : 0u))
+              << (4 * k);
+    }
+    return bits;
+  };
+  // a row's fresh entries; a row whose page is not there gets a fresh one, and nothing is copied
+  auto fresh_of = [&](const RowPlan& r) { return r.end - r.first + (r.part > 0 && !own ? 1 : 0); };
+  int64_t need = 0, copies = 0, free = 0;
+  uint32_t mine = look(g0 + warp * 512);  // the last part's bits of this thread
+  each_part([&](int n, int64_t r0) {
+    int fresh = 0;
+    if ((int)threadIdx.x < n) {
+      if (parts) page = wanted(rows_s[threadIdx.x]);
+      own = keeps(page, r0 + threadIdx.x);
+      fresh = fresh_of(rows_s[threadIdx.x]);
+    }
+    need += block_sum(fresh, sums);
+    copies += __syncthreads_count(page >= 0 && !own);
+  });
+  free = block_sum(__popc(mine), sums);
+  for (int64_t x0 = g0 + kPlanPages; x0 < g1; x0 += kPlanPages) {
+    mine = look(x0 + warp * 512);
+    free += block_sum(__popc(mine), sums);
   }
-  if (threadIdx.x == 0) {
-    ws.totals[3 * cta] = need;
-    ws.totals[3 * cta + 1] = copies;
-    ws.totals[3 * cta + 2] = free;
+  if (threadIdx.x < kPlanCtas) {  // to every CTA of the cluster
+    const uint32_t to = cluster_addr(smem_u32(totals_s + cta), threadIdx.x);
+    st_cluster(to + offsetof(PlanTotals, need), need);
+    st_cluster(to + offsetof(PlanTotals, copies), copies);
+    st_cluster(to + offsetof(PlanTotals, free), free);
   }
   cluster_sync();
   // 4. Ranks of the rows, the list of the free pages.
   int64_t need0 = 0, copies0 = 0, free0 = 0, all_need = 0, all_copies = 0, all_free = 0;
+#pragma unroll
   for (int c = 0; c < kPlanCtas; ++c) {
-    const int64_t x = __ldcg(ws.totals + 3 * c), y = __ldcg(ws.totals + 3 * c + 1), z = __ldcg(ws.totals + 3 * c + 2);
-    if (c < cta) need0 += x, copies0 += y, free0 += z;
-    all_need += x, all_copies += y, all_free += z;
+    const PlanTotals t = totals_s[c];
+    if (c < cta) need0 += t.need, copies0 += t.copies, free0 += t.free;
+    all_need += t.need, all_copies += t.copies, all_free += t.free;
   }
   each_part([&](int n, int64_t r0) {
     int fresh = 0;
     RowPlan r{-1, 0, 0, 0};
-    int32_t page = -1;
-    bool own = false;
     if ((int)threadIdx.x < n) {
       r = rows_s[threadIdx.x];
-      page = wanted(r);
-      own = keeps(page, r0 + threadIdx.x);
-      fresh = r.end - r.first + (r.part > 0 && !own ? 1 : 0);
+      if (parts) {
+        page = wanted(r);
+        own = keeps(page, r0 + threadIdx.x);
+      }
+      fresh = fresh_of(r);
     }
-    const bool copy = page >= 0 && !own;
+    const bool copy = (int)threadIdx.x < n && page >= 0 && !own;
     int before, at;
     const int all = block_scan(fresh, &before, sums), many = block_scan(copy ? 1 : 0, &at, sums);
     if ((int)threadIdx.x < n)
@@ -632,11 +659,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   });
   const bool again = g1 - g0 > kPlanPages;  // (the bits of more than one part are looked at again)
   for (int64_t x0 = g0; x0 < g1 && free0 < all_need; x0 += kPlanPages) {
-    if (again) {
-      mine = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) mine |= look(x0 + warp * 512 + k * 128) << (4 * k);
-    }
+    if (again) mine = look(x0 + warp * 512);
     // in order of page: the warp's four pieces of 128, in each the lanes in turn
     int before;
     const int of_part = block_scan(__popc(mine), &before, sums);
@@ -686,9 +709,9 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
           if (r.source != b) row[s] = __ldcg(ws.carried + b * p.max_pages + s);
         } else if (s < r.end) {
           const int64_t rank = (int64_t)y.y + (s - y.x);
-          const int32_t page = rank < all_free ? __ldcg(ws.free_pages + rank) : -1;
-          row[s] = page;
-          if (page >= 0) p.refs[page] = 1;
+          const int32_t given = rank < all_free ? __ldcg(ws.free_pages + rank) : -1;
+          row[s] = given;
+          if (given >= 0) p.refs[given] = 1;
         } else {
           row[s] = -1;
         }
