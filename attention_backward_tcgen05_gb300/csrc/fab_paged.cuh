@@ -316,19 +316,26 @@ struct PagedCut {
 };
 
 // Partial results: outputs, and (maximum in log2 units, sum) pairs by row.  The
-// outputs of a unit of two row tiles lie by 4 columns, then by row, as the writers'
-// lanes are rows (mixed chunks 53.7 -> 51.5 us); those of one, which may have few
-// rows, row by row (one sequence of 131,000 keys 89.5 us, the other way 99.5).
+// outputs of a unit of more than 32 rows lie by 4 columns, then by row, as the writers'
+// lanes are rows (units of two row tiles, mixed chunks: 53.7 -> 51.5 us; of one, @@);
+// those of fewer rows row by row (one sequence of 131,000 keys 89.5 us, the other
+// way 99.5).  On the CUDA cores, whose tiles have 16 rows at most, always so.
 struct PagedParts {
   float* out;
   float2* ml;
   PagedCut* cuts;
   int rows, dp;  // rows of a slot, columns (a multiple of 4)
 };
-FAB_DEV float4* paged_part(const PagedParts& x, int64_t slot, int width, int row, int c4) {
+FAB_DEV float4* paged_part(const PagedParts& x, int64_t slot, bool by_columns, int row, int c4) {
   const int n4 = x.dp / 4;
-  return reinterpret_cast<float4*>(x.out) + slot * (n4 * x.rows) + (width == 2 ? c4 * x.rows + row : row * n4 + c4);
+  return reinterpret_cast<float4*>(x.out) + slot * (n4 * x.rows) + (by_columns ? c4 * x.rows + row : row * n4 + c4);
 }
+// Rows of a unit that belong to a token: `left` tokens of its sequence from its first on.
+FAB_DEV int paged_live(int left, int gw, int rows) {
+  const int64_t live = (int64_t)left * gw;
+  return live < rows ? (int)live : rows;
+}
+FAB_DEV bool paged_by_columns(int live) { return live > 32; }
 inline size_t paged_parts_bytes(int rows, int dp) {
   return (size_t)(2 * kPagedMaxGrid) * rows * (dp + 2) * sizeof(float) + kPagedMaxGrid * sizeof(PagedCut);
 }
@@ -365,13 +372,16 @@ FAB_DEV void paged_store(__half* p, float x) { *p = __float2half_rn(x); }
 constexpr int kCombineThreads = 256;
 
 // Joins the cut unit whose first part CTA blockIdx.x holds, if there is one:
-// out = sum 2^(m_i - M) out_i / sum 2^(m_i - M) l_i over its parts.  Of a unit of two
-// row tiles (16-bit types, DV a multiple of 8) a thread takes 8 columns of a row and its neighbours the next rows,
-// as the parts lie; of one, LPR lanes share a row, four columns at a time.
-// blockIdx.y of gridDim.y shares the work.  Launched while the attention kernel
-// still runs; waits for it first.
-template <typename T, int LPR>
-__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedPlan p, const PagedParts parts,
+// out = sum 2^(m_i - M) out_i / sum 2^(m_i - M) l_i over its parts.  Where the parts lie by
+// columns (16-bit types on the tensor cores, DV a multiple of 8) a thread takes 8 columns of a row and its neighbours the
+// next rows; where they lie by rows, LPR lanes share a row, four columns at a time.
+// blockIdx.y of gridDim.y shares the work.  U parts are fetched at once: eight where
+// a unit has several, two, which leaves registers for six blocks an SM, where most
+// have two (four in both: one sequence of 131,000 keys and 64 new tokens 107.4 -> 105.4 us
+// with eight, 32 drafts of 8 to 64 tokens 63.7 -> 62.7 and 64 decoding sequences 98.6 -> 97.7 with two).
+// Launched while the attention kernel still runs; waits for it first.
+template <typename T, int LPR, int U>
+__global__ void __launch_bounds__(kCombineThreads, U == 2 ? 6 : 2) paged_combine_kernel(const PagedPlan p, const PagedParts parts,
                                                                         int DV, int H, T* o, float* lse) {
   constexpr int RPB = kCombineThreads / LPR;  // rows a block takes at once
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -381,9 +391,8 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
   const int sub = (int)threadIdx.x % LPR;
   const int tile_rows = p.nt * p.gw;
   const int hk = cut.head / p.gblocks, gb = cut.head - hk * p.gblocks;
-  if (sizeof(T) == 2 && cut.rows > tile_rows) {  // (f32's units have one row tile)
-    const int64_t left = (int64_t)(cut.n - cut.token0) * p.gw;
-    const int live = left < cut.rows ? (int)left : cut.rows;  // rows that belong to a token
+  const int live = paged_live(cut.n - cut.token0, p.gw, cut.rows);
+  if (sizeof(T) == 2 && paged_by_columns(live)) {  // (f32's units have 16 rows at most)
     const int nc8 = DV / 8, items = (live + 31) / 32 * 32 * nc8;
     for (int x = (int)blockIdx.y * kCombineThreads + (int)threadIdx.x; x < items; x += (int)gridDim.y * kCombineThreads) {
       const int rblk = x / (32 * nc8), c8 = x / 32 - rblk * nc8, at = rblk * 32 + x % 32;
@@ -395,7 +404,6 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
       float m = -INFINITY, l = 0.f, acc[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-      constexpr int U = 4;  // parts whose loads are in flight
       for (int k0 = c; k0 <= cut.last; k0 += U) {
         float2 ml[U];
         float4 v[U][2];
@@ -407,8 +415,8 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
           if (k <= cut.last && (k == c || !cut.gaps || parts.cuts[k].head_part)) {
             const int64_t slot = k == c ? 2 * k + 1 : 2 * k;
             ml[u] = parts.ml[slot * parts.rows + row];
-            v[u][0] = *paged_part(parts, slot, 2, row, c8 * 2);
-            v[u][1] = *paged_part(parts, slot, 2, row, c8 * 2 + 1);
+            v[u][0] = *paged_part(parts, slot, true, row, c8 * 2);
+            v[u][1] = *paged_part(parts, slot, true, row, c8 * 2 + 1);
           }
         }
 #pragma unroll
@@ -444,7 +452,6 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
     for (int c0 = sub * 4; c0 < parts.dp; c0 += LPR * 4) {
       float m = -INFINITY, l = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      constexpr int U = 4;  // parts whose loads are in flight
       for (int k0 = c; k0 <= cut.last; k0 += U) {
         float2 ml[U];
         float4 v[U];
@@ -482,6 +489,9 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
   }
 }
 
+// Units of a call at most.
+inline int64_t paged_most_units(const PagedPlan& p) { return (p.T / (p.nt * p.tiles) + p.B) * p.heads; }
+
 // Sets plan.whole and returns the grid.  Short calls are not cut: a CTA then walks
 // `few` key tiles more, but nothing is left to join and a launch is saved.
 // Decoding: units of up to `few` key tiles, two to a CTA at most; chunks, whose
@@ -494,7 +504,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
 // at width 128 with 32 heads of 200 keys 13.8 and 14.0, of 256 13.8 and 13.2, of 500 16.4 and
 // 20.6; 4 sequences of 500 14.6 and 21.1; 16 of 200 18.2 and 14.4, of 500 24.8 and 21.2.
 inline int paged_grid(PagedPlan* plan, int sms, int few) {
-  const int64_t units = (plan->T / (plan->nt * plan->tiles) + plan->B) * plan->heads;  // at most
+  const int64_t units = paged_most_units(*plan);
   const int64_t tiles = (plan->max_keys + plan->kt - 1) / plan->kt;                    // of a unit, at most
   const int most = sms < kPagedMaxGrid ? sms : kPagedMaxGrid;
   const bool chunks = plan->tiles == 2 && plan->T > plan->B * plan->nt;
@@ -529,9 +539,10 @@ cudaError_t launch_combine(const PagedPlan& plan, const PagedParts& parts, int g
   const int rows = plan.nt * plan.gw;
   const int per = kCombineThreads / (parts.dp <= 64 ? 16 : 32);  // rows of a block at once
   const dim3 g((unsigned)(grid - 1), (unsigned)((rows + per - 1) / per));
-  if (parts.dp <= 64)
-    return launch_early(paged_combine_kernel<T, 16>, g, kCombineThreads, 0, s, plan, parts, DV, H, o, lse);
-  return launch_early(paged_combine_kernel<T, 32>, g, kCombineThreads, 0, s, plan, parts, DV, H, o, lse);
+  const bool few = paged_most_units(plan) > grid;  // (units of more parts than two are few)
+  const auto kernel = parts.dp <= 64 ? (few ? paged_combine_kernel<T, 16, 2> : paged_combine_kernel<T, 16, 8>)
+                                     : (few ? paged_combine_kernel<T, 32, 2> : paged_combine_kernel<T, 32, 8>);
+  return launch_early(kernel, g, kCombineThreads, 0, s, plan, parts, DV, H, o, lse);
 }
 
 }  // namespace fab

@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_simt_kernel(const __grid_co
         if (col == 0 && p.lse != nullptr) p.lse[h * plan.T + t] = sum == 0.f ? INFINITY : (ref + log2f(sum)) * kLn2;
       } else {
         const int64_t slot = w.slot((int)blockIdx.x);
-        reinterpret_cast<float*>(paged_part(p.parts, slot, 1, r, col / 4))[col % 4] = val;
+        reinterpret_cast<float*>(paged_part(p.parts, slot, false, r, col / 4))[col % 4] = val;
         if (col == 0) p.parts.ml[slot * p.parts.rows + r] = make_float2(ref, sum);
       }
     }

@@ -761,8 +761,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float a0 = l == 0.f ? 0.f : f0 * inv, a1 = f1 * inv;
           T* o = static_cast<T*>(p.o) + (tok * p.H + head) * p.DV;
           const int prow = (wide ? s * 128 : 0) + r;
-          float4* part = paged_part(p.parts, u.slot, u.width, prow, 0);
-          const int next4 = wide ? 256 : 1;  // from 4 columns to the next
+          const bool columns = paged_by_columns(paged_live(u.n - u.token0, plan.gw, u.width * plan.nt * plan.gw));
+          float4* part = paged_part(p.parts, u.slot, columns, prow, 0);
+          const int next4 = columns ? 256 : 1;  // from 4 columns to the next
 #pragma unroll 1
           for (int c0 = 0; c0 < DP; c0 += 32) {
             uint32_t x[32];
