@@ -731,6 +731,8 @@ def _accept_call(plan, starts, lens, table, seen, last, k_cache, v_cache, lens_o
 def fab_paged_accept(starts, lens, table, seen, last, k_cache, v_cache, lens_out, stream=None):
     plan = _accept_plan(_layouts(starts, lens, table, seen, last, k_cache, v_cache))
     _outputs(plan[3], (lens_out, "lens_out", torch.int32, (plan[0].B,)))
+    if abs(lens_out.data_ptr() - lens.data_ptr()) < 4 * plan[0].B:
+        raise ValueError("lens_out overlaps lens, which is read until the call is over")
     _accept_call(plan, starts, lens, table, seen, last, k_cache, v_cache, lens_out, stream)
 
 

@@ -317,7 +317,7 @@ struct PagedCut {
 
 // Partial results: outputs, and (maximum in log2 units, sum) pairs by row.  The
 // outputs of a unit of more than 32 rows lie by 4 columns, then by row, as the writers'
-// lanes are rows (units of two row tiles, mixed chunks: 53.7 -> 51.5 us; of one, @@);
+// lanes are rows (units of two row tiles, mixed chunks: 53.7 -> 51.5 us; of one 51.2 -> 50.4);
 // those of fewer rows row by row (one sequence of 131,000 keys 89.5 us, the other
 // way 99.5).  On the CUDA cores, whose tiles have 16 rows at most, always so.
 struct PagedParts {
@@ -377,8 +377,8 @@ constexpr int kCombineThreads = 256;
 // next rows; where they lie by rows, LPR lanes share a row, four columns at a time.
 // blockIdx.y of gridDim.y shares the work.  U parts are fetched at once: eight where
 // a unit has several, two, which leaves registers for six blocks an SM, where most
-// have two (four in both: one sequence of 131,000 keys and 64 new tokens 107.4 -> 105.4 us
-// with eight, 32 drafts of 8 to 64 tokens 63.7 -> 62.7 and 64 decoding sequences 98.6 -> 97.7 with two).
+// have two (four in both: one sequence of 131,000 keys and 64 new tokens 107.4 -> 106.6 us
+// with eight, 32 drafts of 8 to 64 tokens 63.7 -> 62.4 and mixed chunks 52.1 -> 51.3 with two).
 // Launched while the attention kernel still runs; waits for it first.
 template <typename T, int LPR, int U>
 __global__ void __launch_bounds__(kCombineThreads, U == 2 ? 6 : 2) paged_combine_kernel(const PagedPlan p, const PagedParts parts,

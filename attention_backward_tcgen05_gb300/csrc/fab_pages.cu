@@ -765,9 +765,11 @@ cudaError_t launch_draft_tree(const int32_t* starts, const int32_t* parents, int
   int64_t per = (304 + B - 1) / B;
   if (per > words) per = words;
   const size_t smem = (size_t)words * 32 * sizeof(int2);
-  cudaError_t err = cudaFuncSetAttribute(draft_tree_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         FAB_DRAFT_MAX_WORDS * 32 * (int)sizeof(int2));
-  if (err != cudaSuccess) return err;
+  if (smem > 48 * 1024) {  // (what a kernel has without asking)
+    const cudaError_t err = cudaFuncSetAttribute(draft_tree_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 FAB_DRAFT_MAX_WORDS * 32 * (int)sizeof(int2));
+    if (err != cudaSuccess) return err;
+  }
   return launch_early(draft_tree_kernel, dim3((unsigned)B, (unsigned)per), kTreeThreads, smem, s, starts, parents, B, T,
                       (int)words, seen);
 }

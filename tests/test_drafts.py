@@ -521,6 +521,30 @@ def test_accept_of_one_layer_and_far_offsets(gpu):
 
 
 @pytest.mark.gpu
+def test_layers_far_apart(gpu):
+    # layers 2^31 elements from each other, keys and values between one another's
+    x = Batch([30, 64], [50, 150], 2, 2, 64, 64, 16, "bf16", seed=13)
+    dense, seen = drafted(x, 14)
+    n, far = x.k.numel(), 1 << 31
+    flat = torch.empty(far + 2 * n, dtype=torch.bfloat16, device="cuda")
+    k, v = (flat[at:].as_strided((2, *x.k.shape), (far, *x.k.stride())) for at in (0, n))
+    k.normal_()
+    v.normal_()
+    want, wk, wv = accepted(x, k.cpu(), v.cpu(), dense, [29, 60])
+    got = binding.paged_accept(x.starts.cuda(), x.lens.cuda(), x.table.cuda(), seen,
+                               torch.tensor([29, 60], dtype=torch.int32).cuda(), k, v)
+    assert torch.equal(got.cpu(), want) and torch.equal(k.cpu(), wk) and torch.equal(v.cpu(), wv)
+    table = torch.tensor([[0, 1], [-1, -1]], dtype=torch.int32, device="cuda")
+    refs = torch.zeros(x.pages, dtype=torch.int32, device="cuda")
+    refs[:2] = 1
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32).cuda()  # noqa: E731
+    binding.paged_reserve(table, refs, i32(20, 20), i32(21, 21), k, v, i32(0, 0))
+    assert table.tolist() == [[0, 1], [0, 2]]
+    for c in (k, v):
+        assert torch.equal(c[:, 2, :, :4], c[:, 1, :, :4])
+
+
+@pytest.mark.gpu
 def test_accept_reports_what_is_out_of_range(gpu):
     x = Batch([8, 33], [40, 60], 2, 2, 64, 64, 16, "bf16", seed=7)
     dense, seen = drafted(x, 8, "recent")
@@ -561,3 +585,5 @@ def test_accept_refuses_what_does_not_match(gpu):
                 (starts, lens, table, seen, last, k.transpose(1, 2), v), (starts, lens, table, seen, last, k, v.cpu())):
         with pytest.raises(ValueError):
             binding.paged_accept(*bad)
+    with pytest.raises(ValueError):
+        binding.fab_paged_accept(starts, lens, table, seen, last, k, v, lens)
