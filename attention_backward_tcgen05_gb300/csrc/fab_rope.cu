@@ -17,6 +17,7 @@
 #include "fab.h"
 #include "fab_device.cuh"
 #include "fab_internal.h"
+#include "fab_launch.cuh"
 
 namespace fab {
 namespace {
@@ -147,6 +148,8 @@ __device__ __forceinline__ int partner(int i, int half, int interleaved, int& f,
 // A warp per row of any width, alignment and stride.
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32) rope_rows_kernel(const RopeProblem p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (launched early)
   if (p.starts != nullptr && blockIdx.x == 0)
     check_starts(p.starts, p.seqs, p.N, (int)threadIdx.x, (int)blockDim.x, &g_err_rope);
   const int lane = threadIdx.x & 31;
@@ -424,6 +427,7 @@ __global__ void __launch_bounds__(kVecThreads, sizeof(T) == 4 ? 4 : 5) rope_vec_
                                                                                      int bq, int bk) {
   constexpr int U = sizeof(T) == 4 ? 1 : 2;  // rows a step
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (launched early)
   if (p.starts != nullptr && blockIdx.x == 0 && blockIdx.y == 0)
     check_starts(p.starts, p.seqs, p.N, (int)threadIdx.x, (int)blockDim.x, &g_err_rope);
   const int sub = threadIdx.x & (L - 1);
@@ -743,11 +747,8 @@ cudaError_t rope_vec(const RopeProblem& p, cudaStream_t s) {
   const int64_t bq = (p.H + hb - 1) / hb, bk = (p.Hkv + hb - 1) / hb;
   if (gx > 2147483647ll) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)gx, (unsigned)blocks(hb));
-  if (p.interleaved)
-    rope_vec_kernel<T, L, true><<<grid, kVecThreads, 0, s>>>(p, (int)hb, (int)bq, (int)bk);
-  else
-    rope_vec_kernel<T, L, false><<<grid, kVecThreads, 0, s>>>(p, (int)hb, (int)bq, (int)bk);
-  return cudaPeekAtLastError();
+  const auto kernel = p.interleaved ? rope_vec_kernel<T, L, true> : rope_vec_kernel<T, L, false>;
+  return launch_early(kernel, grid, kVecThreads, 0, s, p, (int)hb, (int)bq, (int)bk);
 }
 
 template <typename T, int L>
@@ -784,8 +785,7 @@ cudaError_t rope_t(const RopeProblem& p, cudaStream_t s) {
   const int64_t rows = p.B * p.N * (p.H + p.Hkv + (p.v != nullptr ? p.Hkv : 0));
   const int64_t grid = (rows + kWarps - 1) / kWarps;
   if (grid > 2147483647ll) return cudaErrorInvalidValue;
-  rope_rows_kernel<T><<<(unsigned)grid, kWarps * 32, 0, s>>>(p);
-  return cudaPeekAtLastError();
+  return launch_early(rope_rows_kernel<T>, dim3((unsigned)grid), kWarps * 32, 0, s, p);
 }
 
 template <typename T>
