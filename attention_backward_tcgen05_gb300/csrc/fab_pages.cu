@@ -615,7 +615,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
       fresh = fresh_of(rows_s[threadIdx.x]);
     }
     need += block_sum(fresh, sums);
-    copies += __syncthreads_count(page >= 0 && !own);
+    copies += __syncthreads_count((int)threadIdx.x < n && page >= 0 && !own);  // (of this part's rows alone)
   });
   free = block_sum(__popc(mine), sums);
   for (int64_t x0 = g0 + kPlanPages; x0 < g1; x0 += kPlanPages) {

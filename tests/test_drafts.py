@@ -401,6 +401,12 @@ APPEND = {
     "bf16_pairs_part": ([30, 3], [33, 77], 4, 2, 80, 64, 24, "bf16", 32, True, True),
     "f32_no_rot": ([3, 11], [13, 11], 4, 2, 64, 64, 16, "f32", 0, False, True),
     "f32_odd": ([3, 41], [13, 41], 4, 2, 7, 5, 3, "f32", 6, False, True),
+    "bf16_many_sequences": ([(7 * i) % 3 if i % 50 else 0 for i in range(1500)],
+                            [(7 * i) % 3 + i % 9 + 1 for i in range(1500)], 2, 1, 16, 16, 8, "bf16", 16, False, True),
+    "f32_many_sequences_odd": ([(5 * i) % 4 for i in range(1100)], [(5 * i) % 4 + i % 9 for i in range(1100)], 2, 1, 7, 5,
+                               8, "f32", 4, False, True),
+    "f16_forty_sequences": ([(7 * i) % 5 for i in range(40)], [(7 * i) % 5 + i for i in range(40)], 4, 2, 64, 64, 16,
+                            "f16", 64, False, True),
     "bf16_wide_tree": ([300, 1, 100], [900, 4, 600], 8, 2, 128, 128, 32, "bf16", 128, False, True),
 }
 
@@ -498,6 +504,48 @@ def test_accept(gpu, name, which):
     want, wk, wv = accepted(x, k.cpu(), v.cpu(), dense, last)
     got = binding.paged_accept(x.starts.cuda(), x.lens.cuda(), x.table.cuda(), seen,
                                torch.tensor(last, dtype=torch.int32).cuda(), k, v)
+    assert torch.equal(got.cpu(), want) and torch.equal(k.cpu(), wk) and torch.equal(v.cpu(), wv)
+
+
+@pytest.mark.gpu
+def test_accept_takes_bits_as_they_are(gpu):
+    # rows of `seen` that no tree gives: what is kept is what the last token sees, up to itself
+    x = Batch([40, 70, 5], [45, 133, 5], 2, 2, 64, 64, 16, "bf16", seed=7)
+    dense = torch.rand((x.T, 70), generator=x.g) < 0.5
+    dense[39], dense[114] = True, False
+    last = [39, 69, 4]
+    k, v = layered(x, 2, 0)
+    want, wk, wv = accepted(x, k.cpu(), v.cpu(), dense, last)
+    got = binding.paged_accept(x.starts.cuda(), x.lens.cuda(), x.table.cuda(), packed(dense, 3).cuda(),
+                               torch.tensor(last, dtype=torch.int32).cuda(), k, v)
+    assert want.tolist()[::2] == [45, 0]
+    assert torch.equal(got.cpu(), want) and torch.equal(k.cpu(), wk) and torch.equal(v.cpu(), wv)
+
+
+@pytest.mark.gpu
+def test_accept_without_new_tokens(gpu):
+    x = Batch([0, 0], [20, 0], 2, 2, 64, 64, 16, "bf16", seed=7)
+    k, v = layered(x, 2, 0)
+    was = k.clone(), v.clone()
+    got = binding.paged_accept(x.starts.cuda(), x.lens.cuda(), x.table.cuda(),
+                               torch.empty((0, 1), dtype=torch.int32).cuda(),
+                               torch.tensor([5, -9], dtype=torch.int32).cuda(), k, v)  # (last is not read)
+    assert got.tolist() == [20, 0] and torch.equal(k, was[0]) and torch.equal(v, was[1])
+
+
+@pytest.mark.gpu
+def test_accept_of_many_sequences(gpu):
+    # more than the threads of a block, most of them with nothing to move
+    new = [(7 * i) % 5 if i % 3 else 0 for i in range(700)]
+    held = [n + (3 * i) % 20 for i, n in enumerate(new)]
+    x = Batch(new, held, 1, 1, 8, 16, 8, "f16", seed=7)
+    dense, seen = drafted(x, 8, "recent")
+    r = random.Random(9)
+    last = [r.randint(-1, n - 1) for n in new]
+    k, v = layered(x, 1, 0)
+    want, wk, wv = accepted(x, k.cpu(), v.cpu(), dense, last)
+    got = binding.paged_accept(x.starts.cuda(), x.lens.cuda(), x.table.cuda(), seen,
+                               torch.tensor(last, dtype=torch.int32).cuda(), k[0], v[0])
     assert torch.equal(got.cpu(), want) and torch.equal(k.cpu(), wk) and torch.equal(v.cpu(), wv)
 
 

@@ -125,6 +125,10 @@ POOLS = {
     "bf16_wide_page": (5, 3, 20, 128, 2, 128, 128, "bf16", 1, 0),
     "f32_page_of_one": (5, 40, 300, 1, 1, 4, 4, "f32", 1, 0),
     "bf16_many_rows": (1500, 3, 4600, 16, 1, 8, 8, "bf16", 1, 0),
+    "bf16_one_row": (1, 1, 2, 16, 1, 8, 8, "bf16", 1, 0),
+    "bf16_three_rows": (3, 2, 5, 16, 1, 8, 8, "bf16", 2, 0),
+    "bf16_large_pool": (4, 9, 150001, 4, 1, 8, 8, "bf16", 1, 0),
+    "bf16_rows_of_several_shares": (9000, 2, 18001, 2, 1, 8, 8, "bf16", 1, 0),
     "bf16_long_rows": (3, 2600, 9001, 4, 1, 8, 8, "bf16", 1, 0),
 }
 
@@ -137,7 +141,7 @@ def test_drawn_steps(gpu, name):
     r = random.Random(sum(map(ord, name)))
     most = W * page
     held = [0] * B  # tokens that each row has room for
-    for i in range(14 if B < 100 else 6):
+    for i in range(14 if B < 100 else 6 if B < 5000 else 4):
         source = None
         if i % 3 == 1:  # forks, ends, and rows that go on
             source = [r.choice([b, b, r.randrange(B), r.randrange(B), -1]) for b in range(B)]
