@@ -371,7 +371,8 @@ FAB_DEV void paged_store(__half* p, float x) { *p = __float2half_rn(x); }
 
 constexpr int kCombineThreads = 256;
 
-// Joins the cut unit whose first part CTA blockIdx.x holds, if there is one:
+// Joins the cut unit whose first part CTA blockIdx.x holds, if there is one (where
+// units are few, `listed`: the blockIdx.x-th cut unit):
 // out = sum 2^(m_i - M) out_i / sum 2^(m_i - M) l_i over its parts.  Where the parts lie by
 // columns (16-bit types on the tensor cores, DV a multiple of 8) a thread takes 8 columns of a row and its neighbours the
 // next rows; where they lie by rows, LPR lanes share a row, four columns at a time.
@@ -382,10 +383,34 @@ constexpr int kCombineThreads = 256;
 // Launched while the attention kernel still runs; waits for it first.
 template <typename T, int LPR, int U>
 __global__ void __launch_bounds__(kCombineThreads, U == 2 ? 6 : 2) paged_combine_kernel(const PagedPlan p, const PagedParts parts,
-                                                                        int DV, int H, T* o, float* lse) {
+                                                                        int ctas, int listed, int DV, int H, T* o, float* lse) {
   constexpr int RPB = kCombineThreads / LPR;  // rows a block takes at once
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = (int)blockIdx.x;
+  int c = (int)blockIdx.x;
+  if (U == 8 && listed) {  // (as many blocks as there can be units: most CTAs hold no unit's first part)
+    __shared__ int found_s, counts_s[kCombineThreads / 32];
+    const int lane = (int)threadIdx.x & 31, warp = (int)threadIdx.x >> 5;
+    if (threadIdx.x == 0) found_s = -1;
+    int before = 0;
+    for (int c0 = 0; c0 < ctas; c0 += kCombineThreads) {
+      const int at = c0 + (int)threadIdx.x;
+      const bool is = at < ctas && parts.cuts[at].last != 0;
+      const uint32_t of_warp = __ballot_sync(0xffffffffu, is);
+      __syncthreads();
+      if (lane == 0) counts_s[warp] = __popc(of_warp);
+      __syncthreads();
+      int rank = before + __popc(of_warp & ((1u << lane) - 1u));
+#pragma unroll
+      for (int w = 0; w < kCombineThreads / 32; ++w) {
+        if (w < warp) rank += counts_s[w];
+        before += counts_s[w];
+      }
+      if (is && rank == (int)blockIdx.x) found_s = at;
+    }
+    __syncthreads();
+    c = found_s;
+    if (c < 0) return;
+  }
   const PagedCut cut = parts.cuts[c];
   if (cut.last == 0) return;
   const int sub = (int)threadIdx.x % LPR;
@@ -538,11 +563,18 @@ cudaError_t launch_combine(const PagedPlan& plan, const PagedParts& parts, int g
   // (as many blocks as a unit of one row tile has use for, which one of two has too)
   const int rows = plan.nt * plan.gw;
   const int per = kCombineThreads / (parts.dp <= 64 ? 16 : 32);  // rows of a block at once
-  const dim3 g((unsigned)(grid - 1), (unsigned)((rows + per - 1) / per));
-  const bool few = paged_most_units(plan) > grid;  // (units of more parts than two are few)
+  const int64_t units = paged_most_units(plan);
+  const bool few = units > grid;  // (units of more parts than two are few)
+  // A block costs a place on an SM for 2 us even where its CTA holds no unit's first part.
+  // Where units are far fewer than CTAs, blocks are launched for as many as there can be, and look
+  // for theirs: one sequence of 131,000 keys and 64 new tokens 104.2 -> 102.2 us, of 500
+  // keys and 7 new ones in f32 20.1 -> 18.4; not worth its look for one new token (86.9 ->
+  // 87.8), nor for half as many units as CTAs (f32 chunks 21.3 -> 21.9).
+  const int listed = !few && units * 4 <= grid && plan.T > plan.B ? 1 : 0;
+  const dim3 g((unsigned)(listed ? units : grid - 1), (unsigned)((rows + per - 1) / per));
   const auto kernel = parts.dp <= 64 ? (few ? paged_combine_kernel<T, 16, 2> : paged_combine_kernel<T, 16, 8>)
                                      : (few ? paged_combine_kernel<T, 32, 2> : paged_combine_kernel<T, 32, 8>);
-  return launch_early(kernel, g, kCombineThreads, 0, s, plan, parts, DV, H, o, lse);
+  return launch_early(kernel, g, kCombineThreads, 0, s, plan, parts, grid - 1, listed, DV, H, o, lse);
 }
 
 }  // namespace fab
