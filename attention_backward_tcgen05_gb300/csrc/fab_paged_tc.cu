@@ -615,7 +615,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t tS = tm + lane_off + C::TM_S + buf * 128;
           if (C::NB == 3) sphase = (step / 3u) & 1u;
           // the words that say which of the tile's keys the row sees, fetched while its
-          // products run: all of the past, of the new tokens those whose bits are set
+          // products run: all of the past, of the new tokens those whose bits are set (32 drafts
+          // behind long pasts as fast as causal chunks, 64.3 and 64.4 us; trees of 100 to 500
+          // tokens at width 64, most of whose tiles are masked, 38.6 for 36.9)
           [[maybe_unused]] uint32_t wd[5];
           [[maybe_unused]] const int off = t * 128 + u.j0 * 128 - u.last0;  // the tile's first key, from the first new one
           [[maybe_unused]] const bool masked = TREE && off + 127 >= 0;

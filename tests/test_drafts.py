@@ -449,6 +449,34 @@ def test_append(gpu, name):
         assert torch.equal(same.nan_to_num(9), was.transpose(1, 2)[~touched].nan_to_num(9))
 
 
+@pytest.mark.gpu
+def test_sight_past_32_bits(gpu):
+    # 2^31 words and more of `seen`: chains of 512 tokens, which are the plain calls
+    B, n, page, D = 8200, 512, 64, 8
+    assert B * n * n > 1 << 31
+    starts = torch.arange(B + 1, dtype=torch.int32, device="cuda") * n
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    table = torch.arange(B * n // page, dtype=torch.int32, device="cuda").view(B, -1)
+    parents = torch.arange(B * n, dtype=torch.int32, device="cuda") % n - 1
+    seen = binding.draft_tree(starts, parents, n * 32)
+    assert seen.shape == (B * n, n)
+    bits = (1 << (torch.arange(n, device="cuda") % 32 + 1)) - 1  # of the word that a token's own bit is in
+    own = torch.arange(n, device="cuda") // 32
+    last = seen[-n:].long() & 0xffffffff
+    assert torch.equal(last[torch.arange(n), own], bits) and (last.sum(1) == bits + own * 0xffffffff).all()
+    cos, sin = (t.cuda() for t in tables(n, D))
+    for dtype in ("bf16", "f32"):
+        q, k, v = (torch.randn(B * n, 1, D, device="cuda").to(DT[dtype]) for _ in range(3))
+        out = []
+        for sight_of in (None, seen):
+            kc = torch.zeros(B * n // page, 1, page, D, dtype=DT[dtype], device="cuda")
+            vc = torch.zeros_like(kc)
+            x = binding.paged_append(q, k, v, None, None, cos, sin, starts, lens, table, kc, vc, seen=sight_of)
+            out.append((x, kc, vc, *binding.paged_attention(x, kc, vc, starts, lens, table, seen=sight_of)))
+        for a, b in zip(*out):
+            assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------ the accepted path
 
 
