@@ -36,12 +36,13 @@
 // the rounding left, would cost chunks half as many products again.
 //
 // Bounds and measured times (bf16, 32 heads on 8, width 128).  Decoding: memory;
-// 64 sequences of 64 to 4,095 keys 98 us, 5.7 TB/s; one of 131,000 keys 89 us,
-// 6.0 TB/s.  Chunks: the tensor core; two of 2,048 tokens behind 14,336 keys
+// 64 sequences of 64 to 4,095 keys 96 us, 5.9 TB/s; one of 131,000 keys 87 us,
+// 6.2 TB/s; 32 drafts of 8 to 64 tokens behind as many keys 57 us.  Chunks: the tensor core; two of 2,048 tokens behind 14,336 keys
 // 645 to 690 us as the power cap allows, 1.5 to 1.6 PFLOP/s (the pipe is 78%
-// active; a plain library product of bf16 sustains 1.69).  At width 64 the
-// exponentials: the 16,384 of a 128 x 128 tile take 1,024 cycles, its products
-// about 630; chunks of 2,048 tokens behind 6,000 keys 216 us, 1.1 PFLOP/s.
+// active; a plain library product of bf16 sustains 1.69).  At width 64 the softmax's
+// steps, of two warps a scheduler: chunks of 2,048 tokens behind 6,000 keys 212 us, 1.1
+// PFLOP/s, with issue slots 52%, the exponentials' pipe 49% and the tensor core 48%
+// active (an eighth of the exponentials as polynomials on the FMA pipe: 234 us).
 // Short calls: the chain of start, plan, page number, copy, product, softmax,
 // product and store, 10.0 us for one sequence of 500 keys of width 64.
 //
