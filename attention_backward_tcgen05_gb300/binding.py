@@ -769,11 +769,14 @@ def fab_paged_reserve(table, refs, source, kept, lens, k_cache, v_cache, workspa
                   stream)
 
 
+_CURRENT = contextlib.nullcontext()
+
+
 def _on(stream):
     """A context whose allocations belong to `stream` (None: the current one),
     so that torch does not hand their memory to other work too early."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _CURRENT
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
