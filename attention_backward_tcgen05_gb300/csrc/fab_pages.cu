@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) paged_accept_kernel(c
 // that each need all of the one before, with the cluster's barrier between them.
 // Each CTA has a share of the rows and a share of the pages.  `copy` copies what has
 // to be copied.  Planning is bound by the five steps, each two or three accesses long, and
-// the barriers: 256 rows over a pool of 131,072 pages 18 us with the copy's empty
+// the barriers: 256 rows over a pool of 131,072 pages 18.6 us with the copy's empty
 // launch, 16 rows of a small pool 11 (as three kernels, the plan's a single CTA, 87 and more).
 
 struct ReserveCopy {
@@ -409,7 +409,10 @@ constexpr int kPlanCtas = 8;  // the largest cluster that every GPU runs
 constexpr int kPlanThreads = 1024;
 // What the shares of a CTA come to.
 struct PlanTotals {
-  int64_t need, copies, free;  // fresh pages and copies of its rows, free ones of its pages
+  int64_t need;     // fresh pages of its rows
+  int copies;       // and copies (written in one with the next)
+  uint32_t misfit;  // references without entries or the reverse, weighted
+  int64_t free;     // free ones of its pages
 };
 struct ReserveSpace {
   int32_t* carried;     // [B][max_pages], of rows that continue another one
@@ -458,6 +461,14 @@ FAB_DEV RowPlan row_plan(const CacheProblem& p, int64_t b, bool* bad) {
 }
 FAB_DEV bool page_ok(const CacheProblem& p, int32_t page) { return page >= 0 && page < p.pages; }
 
+// A page's weight in the sums that show whether references fit the table: odd, so that one
+// page's misfit always shows, and otherwise spread over 32 bits, so that those of several cancel
+// by chance alone, once in 2^32.  (The bits of the golden ratio and of the root of 2.)
+FAB_DEV uint32_t weight(uint32_t page) {
+  const uint32_t x = page * 0x9E3779B9u;
+  return ((x ^ x >> 15) * 0x6A09E667u) | 1u;
+}
+
 // Sum over the block of one value a thread, and what the threads before this one
 // add up to.
 FAB_DEV int block_scan(int v, int* before, int* sums) {
@@ -491,6 +502,16 @@ FAB_DEV int block_sum(int v, int* sums) {
   return __reduce_add_sync(0xffffffffu, sums[threadIdx.x & 31]);
 }
 
+// The sums of two.
+FAB_DEV int2 block_sums(int v, int w, int2* sums) {
+  const int2 of_warp = make_int2(__reduce_add_sync(0xffffffffu, v), __reduce_add_sync(0xffffffffu, w));
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = of_warp;
+  __syncthreads();
+  const int2 x = sums[threadIdx.x & 31];
+  return make_int2(__reduce_add_sync(0xffffffffu, x.x), __reduce_add_sync(0xffffffffu, x.y));
+}
+
 constexpr int kPlanRows = 1024;        // rows of a CTA's share held in shared memory at once
 constexpr int kPlanSlots = 128;        // entries that a warp looks at
 constexpr int kPlanPages = 16 * kPlanThreads;  // pages that a CTA looks at at once
@@ -501,6 +522,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   __shared__ RowPlan rows_s[kPlanRows];
   __shared__ PlanTotals totals_s[kPlanCtas];
   __shared__ int sums[32];
+  __shared__ int2 sums2[32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = (int)blockIdx.x;
@@ -533,6 +555,9 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   };
   auto keeps = [&](int32_t x, int64_t b) { return x >= 0 && __ldcg(p.refs + x) == INT_MIN + (int)b; };
   const bool parts = b1 - b0 > kPlanRows;
+  // The references that step 1 leaves, less the entries that hold on to their page, both
+  // weighted by page: 0 where they fit.
+  uint32_t misfit = 0;
   // 1. Entries that go and come.  (A page that a row goes on writing is dropped.)
   each_part([&](int n, int64_t r0) {
     if ((int)threadIdx.x < n) page = wanted(rows_s[threadIdx.x]);
@@ -557,6 +582,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         if (had[u] >= p.pages) bad = true;
         if (r.source == b) {
           if (!stays && page_ok(p, had[u])) atomicSub(p.refs + had[u], 1);
+          if (stays && page_ok(p, had[u])) misfit -= weight((uint32_t)had[u]);
           if (carried && had[u] < 0) bad = true;
         } else {
           if (page_ok(p, had[u])) atomicSub(p.refs + had[u], 1);
@@ -566,7 +592,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
             if (!ok)
               bad = true;
             else if (stays)
-              atomicAdd(p.refs + get[u], 1);
+              atomicAdd(p.refs + get[u], 1), misfit -= weight((uint32_t)get[u]);
           }
         }
       }
@@ -575,10 +601,15 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   cluster_sync();
   // 2. Of the rows that would go on writing a page which no other row holds (its
   // references have all been dropped) the first keeps it: the lowest mark stays.
+  // (a count below zero that is no mark: more entries named the page than its references say)
+  auto odd = [](int32_t c) { return c < 0 && c > INT_MIN / 2; };
   each_part([&](int n, int64_t r0) {
-    if ((int)threadIdx.x >= n) return;
-    if (parts) page = wanted(rows_s[threadIdx.x]);
-    if (page >= 0 && __ldcg(p.refs + page) <= 0) atomicMin(p.refs + page, INT_MIN + (int)(r0 + threadIdx.x));
+    if ((int)threadIdx.x < n) {
+      if (parts) page = wanted(rows_s[threadIdx.x]);
+      const int32_t count = page >= 0 ? __ldcg(p.refs + page) : 1;
+      if (count <= 0) atomicMin(p.refs + page, INT_MIN + (int)(r0 + threadIdx.x));
+      bad |= odd(count);  // (the first to leave its mark sees what was there before)
+    }
   });
   cluster_sync();
   // 3. How many pages of the CTA's share are free, the fresh pages and copies of its rows.
@@ -591,7 +622,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int64_t at = x + k * 128 + lane * 4;
-      v[k] = make_int4(1, 1, 1, 1);
+      v[k] = make_int4(INT_MIN, INT_MIN, INT_MIN, INT_MIN);  // (as if kept: no page there)
       if (at + 4 <= g1) {
         v[k] = __ldcg(reinterpret_cast<const int4*>(p.refs + at));
       } else {
@@ -600,11 +631,15 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         if (at + 2 < g1) v[k].z = __ldcg(p.refs + at + 2);
       }
     }
-    auto odd = [](int32_t c) { return c < 0 && c > INT_MIN / 2; };  // (more entries named it than its references say)
     uint32_t bits = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (odd(v[k].x) || odd(v[k].y) || odd(v[k].z) || odd(v[k].w)) bad = true;
+      const int32_t c[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (odd(c[u])) bad = true;
+        misfit += (uint32_t)max(c[u], 0) * weight((uint32_t)x + k * 128 + lane * 4 + u);
+      }
       bits |= ((v[k].x == 0 ? 1u : 0u) | (v[k].y == 0 ? 2u : 0u) | (v[k].z == 0 ? 4u : 0u) | (v[k].w == 0 ? 8u : 0u))
               << (4 * k);
     }
@@ -612,7 +647,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   };
   // a row's fresh entries; a row whose page is not there gets a fresh one, and nothing is copied
   auto fresh_of = [&](const RowPlan& r) { return r.end - r.first + (r.part > 0 && !own ? 1 : 0); };
-  int64_t need = 0, copies = 0, free = 0;
+  int64_t need = 0, copies = 0;
   uint32_t mine = look(g0 + warp * 512);  // the last part's bits of this thread
   each_part([&](int n, int64_t r0) {
     int fresh = 0;
@@ -624,26 +659,47 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     need += block_sum(fresh, sums);
     copies += __syncthreads_count((int)threadIdx.x < n && page >= 0 && !own);  // (of this part's rows alone)
   });
-  free = block_sum(__popc(mine), sums);
+  int unused = __popc(mine);  // pages (of a thread, below 2^31 / 1024)
   for (int64_t x0 = g0 + kPlanPages; x0 < g1; x0 += kPlanPages) {
     mine = look(x0 + warp * 512);
-    free += block_sum(__popc(mine), sums);
+    unused += __popc(mine);
   }
+  const int2 of_pages = block_sums(unused, (int)misfit, sums2);
   if (threadIdx.x < kPlanCtas) {  // to every CTA of the cluster
     const uint32_t to = cluster_addr(smem_u32(totals_s + cta), threadIdx.x);
     st_cluster(to + offsetof(PlanTotals, need), need);
-    st_cluster(to + offsetof(PlanTotals, copies), copies);
-    st_cluster(to + offsetof(PlanTotals, free), free);
+    st_cluster(to + offsetof(PlanTotals, copies), (int64_t)(uint32_t)of_pages.y << 32 | copies);
+    st_cluster(to + offsetof(PlanTotals, free), of_pages.x);
   }
   cluster_sync();
   // 4. Ranks of the rows, the list of the free pages.
   int64_t need0 = 0, copies0 = 0, free0 = 0, all_need = 0, all_copies = 0, all_free = 0;
+  uint32_t unfit = 0;
 #pragma unroll
   for (int c = 0; c < kPlanCtas; ++c) {
     const PlanTotals t = totals_s[c];
     if (c < cta) need0 += t.need, copies0 += t.copies, free0 += t.free;
     all_need += t.need, all_copies += t.copies, all_free += t.free;
+    unfit += t.misfit;
   }
+  // What a row holds on to has a reference left, or the counts were too low: the page
+  // would be handed out, or another row would write it.  Looked for only where the sums say
+  // that something does not fit (256 rows: the look at each entry's count 4.2 us, the sums 0.9).
+  if (unfit != 0u)
+    each_part([&](int n, int64_t r0) {
+      for (int x = warp; x < n * segs; x += kPlanThreads / 32) {
+        const int i = x / segs;
+        const RowPlan r = rows_s[i];
+        const int stay = r.first - (r.part > 0 ? 1 : 0);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int s = (x - i * segs) * kPlanSlots + u * 32 + lane;
+          if (s >= stay) break;
+          const int32_t held = p.table[(int64_t)r.source * p.max_pages + s];  // (a row of no source holds nothing)
+          if (page_ok(p, held) && __ldcg(p.refs + held) <= 0) bad = true;
+        }
+      }
+    });
   each_part([&](int n, int64_t r0) {
     int fresh = 0;
     RowPlan r{-1, 0, 0, 0};

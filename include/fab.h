@@ -422,11 +422,14 @@ FAB_EXPORT size_t fab_paged_reserve_workspace_bytes(const fab_cache_dims* dims);
  * free, below zero the number that were missing: the last entries in that order
  * are then -1, and what a copy among them should have held is lost.
  * source, kept, lens: device int32 [B].  kept[b] past what the row source[b] holds,
- * or any of them out of range, and references that do not fit the table, are reported
- * as FAB_ERR_INVALID (the rows concerned are meaningless; nothing outside the
- * arguments is touched).  fab_cache_dims' T and words are not read.  workspace: device,
- * fab_paged_reserve_workspace_bytes() bytes, contents overwritten; calls that may
- * overlap on the GPU need one each. */
+ * or any of them out of range, are reported as FAB_ERR_INVALID (the rows concerned are
+ * meaningless; nothing outside the arguments is touched).  So are references too low
+ * for the table, by the call in which that matters: where a page that a row holds on to
+ * would be handed out or written by another, or a count falls below zero.  References
+ * above what the table says stand for holders besides it: for as long as they are there
+ * the page is not written, handed out or freed.  fab_cache_dims' T and words are not read.
+ * workspace: device, fab_paged_reserve_workspace_bytes() bytes, contents overwritten;
+ * calls that may overlap on the GPU need one each. */
 FAB_EXPORT int fab_paged_reserve(int32_t* table, int32_t* refs, const int32_t* source, const int32_t* kept,
                                  const int32_t* lens, int dtype, const fab_cache_dims* dims, void* k_cache,
                                  void* v_cache, void* workspace, size_t workspace_bytes, int32_t* spare,

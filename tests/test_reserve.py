@@ -220,6 +220,68 @@ def test_what_is_out_of_range_is_reported(gpu):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("W, page", [(4, 16), (300, 4)])
+def test_counts_too_low_are_reported(gpu, W, page):
+    # a page that a row holds would be handed out, or written by one row while another holds it
+    most = 5 * page // 2 if W == 4 else 250 * page - 2
+
+    def pool():
+        x = Pool(3, W, 3 * W + 2, page, 1, 16, 16, "f32", 1, 9)
+        x.step([0, 0, 0], [most, 20, 0])
+        return x, x.table[0].tolist()
+
+    end = (most - 1) // page  # the entry of the last, partly filled page
+    for entry in {0, 1, end - 1}:
+        x, row = pool()
+        x.refs[row[entry]] = 0
+        x.call([most, 20, 0], [most, 40, 20])
+        assert binding.fab_last_device_error() == binding.FAB_ERR_INVALID, entry
+        x, row = pool()  # handed on: row 2 goes on with what row 0 held
+        x.refs[row[entry]] = 0
+        x.call([0, 20, most], [0, 40, most], [-1, 1, 0])
+        assert binding.fab_last_device_error() == binding.FAB_ERR_INVALID, entry
+    x, row = pool()
+    x.step([most, 20, most], [most, 20, most], [0, 1, 0])
+    x.refs[row[end]] = 1  # of two
+    x.call([most, 20, most], [most + 1, 20, most])
+    assert binding.fab_last_device_error() == binding.FAB_ERR_INVALID
+    x, row = pool()
+    x.refs[row[end]] = 0
+    x.call([most, 20, 0], [most + 1, 20, 0])
+    assert binding.fab_last_device_error() == binding.FAB_ERR_INVALID
+
+
+@pytest.mark.gpu
+def test_a_count_too_low_among_many_rows(gpu):
+    B = 9000
+    x = Pool(B, 2, 3 * B, 2, 1, 8, 8, "bf16", 1, 9)
+    x.step([0] * B, [3] * B)
+    for b in (0, 1124, 1125, 5000, B - 1):
+        at = int(x.table[b, 0])
+        x.refs[at] = 0
+        x.call([3] * B, [3] * B)
+        assert binding.fab_last_device_error() == binding.FAB_ERR_INVALID, b
+        x.refs[at] = 1
+        x.call([3] * B, [3] * B)
+        assert binding.fab_last_device_error() == binding.FAB_OK, b
+
+
+@pytest.mark.gpu
+def test_counts_above_the_table_hold_pages(gpu):
+    # pages that something besides the table holds: never written, handed out or freed
+    x = Pool(2, 4, 9, 16, 2, 64, 64, "bf16", 2, 6)
+    x.step([0, 0], [40, 0])
+    x.refs[1:3] += 1
+    was = x.k.clone(), x.v.clone()
+    assert int(x.call([40, 0], [41, 17])) == 3
+    assert x.table.tolist() == [[0, 1, 3, -1], [4, 5, -1, -1]] and x.refs.tolist() == [1, 2, 1, 1, 1, 1, 0, 0, 0]
+    for c, old in zip((x.k, x.v), was):
+        assert torch.equal(c[:, :3], old[:, :3]) and torch.equal(c[:, 3, :, :8], old[:, 2, :, :8])
+    assert int(x.call([41, 17], [0, 0])) == 7
+    assert x.refs.tolist() == [0, 1, 1, 0, 0, 0, 0, 0, 0]
+
+
+@pytest.mark.gpu
 def test_operands_that_do_not_match_are_refused(gpu):
     x = Pool(3, 4, 20, 16, 1, 16, 16, "f32", 2, 9)
     n = torch.zeros(3, dtype=torch.int32, device="cuda")
