@@ -359,6 +359,13 @@ def _outputs(dev, *checks):
                 raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{dev}")
 
 
+def _apart(out, name, t, what):
+    """What a contiguous output holds is no part of the contiguous tensor t."""
+    a, b = out.data_ptr(), t.data_ptr()
+    if a < b + t.numel() * t.element_size() and b < a + out.numel() * out.element_size():
+        raise ValueError(f"{name} overlaps {what}, which is read until the call is over")
+
+
 def _ld(x, name, dtype, shape):
     """Elements between the rows of consecutive tokens of a layout of shape
     (..., tokens, heads, width): heads contiguous inside a row, rows evenly
@@ -731,8 +738,8 @@ def _accept_call(plan, starts, lens, table, seen, last, k_cache, v_cache, lens_o
 def fab_paged_accept(starts, lens, table, seen, last, k_cache, v_cache, lens_out, stream=None):
     plan = _accept_plan(_layouts(starts, lens, table, seen, last, k_cache, v_cache))
     _outputs(plan[3], (lens_out, "lens_out", torch.int32, (plan[0].B,)))
-    if abs(lens_out.data_ptr() - lens.data_ptr()) < 4 * plan[0].B:
-        raise ValueError("lens_out overlaps lens, which is read until the call is over")
+    for t, name in ((starts, "starts"), (lens, "lens"), (table, "table"), (seen, "seen"), (last, "last")):
+        _apart(lens_out, "lens_out", t, name)
     _accept_call(plan, starts, lens, table, seen, last, k_cache, v_cache, lens_out, stream)
 
 

@@ -21,6 +21,12 @@ int64_t elem_size(int dtype) { return dtype == FAB_F32 ? 4 : 2; }
 
 bool aligned(const void* p, int64_t a) { return p != nullptr && reinterpret_cast<uintptr_t>(p) % (uintptr_t)a == 0; }
 
+// n int32 at a and m at b have none in common
+bool apart(const void* a, int64_t n, const void* b, int64_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? (y - x) / 4 >= (uintptr_t)n : (x - y) / 4 >= (uintptr_t)m;
+}
+
 // a * b * c * d <= kMaxElems for positive factors
 bool fits(int64_t a, int64_t b, int64_t c, int64_t d) {
   return a <= kMaxElems / b && a * b <= kMaxElems / c && a * b * c <= kMaxElems / d;
@@ -406,6 +412,11 @@ FAB_API int fab_paged_accept(const int32_t* starts, const int32_t* lens, const i
   if (!aligned(starts, 4) || !aligned(lens, 4) || !aligned(table, 4) || !aligned(last, 4) || !aligned(lens_out, 4))
     return FAB_ERR_INVALID;
   if (!widths_ok(dims->DK, dims->DV)) return FAB_ERR_UNSUPPORTED;
+  // (what is read is read until the call is over)
+  if (!apart(lens_out, dims->B, starts, dims->B + 1) || !apart(lens_out, dims->B, lens, dims->B) ||
+      !apart(lens_out, dims->B, table, dims->B * dims->max_pages) ||
+      !apart(lens_out, dims->B, seen, dims->T * dims->words) || !apart(lens_out, dims->B, last, dims->B))
+    return FAB_ERR_INVALID;
   CacheProblem p = cache_problem(dims, dtype, k_cache, v_cache);
   p.starts = starts;
   p.lens = lens;

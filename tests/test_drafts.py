@@ -95,6 +95,18 @@ def test_accept_refuses_widths():
     assert call_accept(cache_dims(DK=264, layers=1)) == binding.FAB_ERR_UNSUPPORTED
 
 
+AT = dict(starts=A, lens=A + 4096, table=A + 8192, seen=A + 12288, last=A + 16384)
+LAST = dict(starts=8, lens=4, table=20, seen=12, last=4)  # bytes to the last element (cache_dims' sizes)
+
+
+@pytest.mark.parametrize("step", ["first", "last", "before"])
+@pytest.mark.parametrize("name", AT)
+def test_accept_refuses_lengths_over_what_it_reads(name, step):
+    # lens_out has two elements
+    out = AT[name] + {"first": 0, "last": LAST[name], "before": -4}[step]
+    assert call_accept(cache_dims(), out=out, **AT) == binding.FAB_ERR_INVALID
+
+
 def test_binding_refuses_what_does_not_fit():
     i32 = lambda *n: torch.zeros(*n, dtype=torch.int32)  # noqa: E731
     k = torch.zeros(5, 2, 16, 64)
@@ -663,3 +675,16 @@ def test_accept_refuses_what_does_not_match(gpu):
             binding.paged_accept(*bad)
     with pytest.raises(ValueError):
         binding.fab_paged_accept(starts, lens, table, seen, last, k, v, lens)
+
+
+@pytest.mark.gpu
+def test_lengths_over_what_accept_reads_are_refused(gpu):
+    x = Batch([8, 33], [40, 60], 2, 2, 64, 64, 16, "bf16", seed=7)
+    _, seen = drafted(x, 8)
+    last = torch.tensor([7, 32], dtype=torch.int32).cuda()
+    starts, lens, table = x.starts.cuda(), x.lens.cuda(), x.table.cuda()
+    k, v = layered(x, 2, 0)
+    for out in (starts[:2], starts[1:], lens, last, table.view(-1)[:2], table.view(-1)[-2:], seen.view(-1)[:2],
+                seen.view(-1)[-2:]):
+        with pytest.raises(ValueError):
+            binding.fab_paged_accept(starts, lens, table, seen, last, k, v, out)
