@@ -880,7 +880,10 @@ def draft_tree(starts, parents, most, stream=None):
     paged_attention and paged_accept, words enough for sequences of `most` new
     tokens.  parents (T,) int32: the number in its sequence of each token's
     predecessor, -1: what the cache held before the draft."""
-    plan = _tree_plan(_layouts(starts, parents), -(-int(most) // 32))
+    words = -(-int(most) // 32)
+    if most == 0 and parents.numel() == 0:  # (no sequence drafts anything)
+        words = 1
+    plan = _tree_plan(_layouts(starts, parents), words)
     with _on(stream):
         seen = torch.empty((plan[1], plan[2]), dtype=torch.int32, device=starts.device)
         _tree_call(plan, starts, parents, seen, stream)

@@ -688,3 +688,21 @@ def test_lengths_over_what_accept_reads_are_refused(gpu):
                 seen.view(-1)[-2:]):
         with pytest.raises(ValueError):
             binding.fab_paged_accept(starts, lens, table, seen, last, k, v, out)
+
+
+@pytest.mark.gpu
+def test_a_step_without_drafts(gpu):
+    x = Batch([0, 0], [20, 0], 2, 2, 64, 64, 16, "bf16", seed=7)
+    starts, lens, table = x.starts.cuda(), x.lens.cuda(), x.table.cuda()
+    parents = torch.empty(0, dtype=torch.int32, device="cuda")
+    seen = binding.draft_tree(starts, parents, 0)
+    assert seen.shape == (0, 1) and seen.dtype == torch.int32
+    k, v = layered(x, 2, 0)
+    none = torch.empty((0, 2, 64), dtype=x.dt, device="cuda")
+    q = binding.paged_append(none, none, none, None, None, None, None, starts, lens, table, k[0], v[0], seen=seen)
+    o, lse = binding.paged_attention(q, k[0], v[0], starts, lens, table, seen=seen)
+    assert q.shape == o.shape == (0, 2, 64) and lse.shape == (2, 0)
+    assert binding.paged_accept(starts, lens, table, seen, lens, k, v).tolist() == [20, 0]
+    for most in (-1, -32, -33):
+        with pytest.raises(ValueError):
+            binding.draft_tree(starts, parents, most)
