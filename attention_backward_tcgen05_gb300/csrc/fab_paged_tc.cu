@@ -83,7 +83,8 @@ struct UnitPart {
   int token0;     // first token of the unit
   int hk, g0;     // key/value head, first query head of it
   int slot;       // partial slot, or -1: the unit is whole
-  int pad[3];
+  int stays;      // 1: its keys and values keep their place in the L2
+  int pad[2];
 };
 static_assert(sizeof(UnitPart) == 64, "");
 
@@ -132,6 +133,17 @@ enum : int {
   B_DE = 45,  // + slot: every warp is done with it
   B_COUNT = 49
 };
+
+// Sequences of kForkLeast to kForkMost keys that begin with the same page as the one
+// kForkRows rows of the table before or behind them (forks and beams, which lie together) keep
+// their keys and values in the L2, others' give way.  Giving way and staying, width 128,
+// 32 heads on 8, one new token: 128 rows of 16 beams with 2,000 keys 134 and 130 us,
+// 3,000 205 and 187, 4,000 290 and 272, 5,000 367 and 366, 8,000 586 and 602; 256 rows of 32
+// beams with 4,000 560 and 500; 48 rows of 8 beams with 3,000 78 and 77, 5,000 123 and 131;
+// of fewer beams, 128 rows of 4 with 4,000 306 and 315, of 2 with 2,000 162 and 167; of
+// 1,000 keys as fast.  The look is the unit list's, where it delays no load: in the loading
+// warps it cost 256 rows of 300 keys 3%.
+constexpr int kForkRows = 4, kForkLeast = 1536, kForkMost = 4608;
 
 struct TcParams {
   PagedPlan plan;
@@ -229,6 +241,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 3) {
       // ------------------------------------------------------------ the units
       if (lane == 0) {
+        auto forked = [&](const PagedWalk& w) -> bool {
+          if (w.q.len < kForkLeast || w.q.len >= kForkMost) return false;
+          const int32_t* first = p.table + (int64_t)w.at.b * p.max_pages;
+          const int page = __ldg(first);
+          return (w.at.b >= kForkRows && __ldg(first - kForkRows * p.max_pages) == page) ||
+                 (w.at.b + kForkRows < plan.B && __ldg(first + kForkRows * p.max_pages) == page);
+        };
         PagedCut cut{0, 0, 0, 0, 0, 0, 0, 0};
         PagedWalk w;
         bool more = any;
@@ -254,6 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             u->hk = hk;
             u->g0 = (w.at.head - hk * plan.gblocks) * plan.gw;
             u->slot = w.whole() ? -1 : w.slot((int)blockIdx.x);
+            u->stays = w.q.n > 2 * plan.nt || forked(w);
           }
           mbar_arrive(bar(B_DF + slot));
           if (!more) break;
@@ -285,14 +305,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const UnitPart& u = units[us];
         if (!u.more) break;
         const int j0 = u.j0, j1 = u.j1, len = u.len, hk = u.hk;
-        // Keys and values that no other unit reads give way in the L2 to what is read
-        // again, the parts of cut units above all (32 drafts of 8 to 64 tokens 62.8 us like
-        // any other, 56.3 this way; 64 decoding sequences 98.7 and 95.6, one of 131,000
-        // keys 89.1 and 86.7); those of a sequence of several units stay.  (Pages that forks
-        // share are read more often and lose a little: 16 prompts of 4,000 tokens in 8 beams 291
-        // and 298 us, of 1,000 81 and 80.)
-        const uint64_t policy = u.n <= 2 * plan.nt ? first : normal;
+        // Keys and values that are read once, or by units far apart, give way in the L2 to
+        // what is read again soon, the parts of cut units above all (32 drafts of 8 to 64 tokens
+        // 63.2 us like any other, 56.6 this way; 64 decoding sequences 98.5 and 95.9, one of
+        // 131,000 keys 88.8 and 87.3); those of a sequence of several units of tokens stay.
+        // (A group of more than 128 heads is cut into units too, not far apart: 64 sequences of
+        // 2,000 keys and 160 heads on one 32.6 and 31.6 us, 8 of 8,000 and 512 on two 32.4 and
+        // 30.7, 16 of 4,000 and 256 on one 24.0 and 24.5.)
         const int32_t* table = p.table + (int64_t)u.b * p.max_pages;
+        const uint64_t policy = u.stays ? normal : first;
         // page of box `lane` of key tile j, and its first row there
         auto lookup = [&](int j, int& row) {
           const uint32_t m = (uint32_t)j * 128u + (uint32_t)(lane * p.box);

@@ -740,3 +740,34 @@ def test_workspaces_with_gaps_are_refused(gpu):
                                               None, w, w)
     binding.fab_paged_attention(*d, True, 0.125, ws, o, lse)
     x.check(o, lse, True, 0.125)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_rows_that_share_pages(gpu, dtype):
+    # forks: the same bits as for rows with pages of their own
+    D, page, H, Hkv = 64, 16, 4, 2
+    groups, held = [6, 1, 5, 2, 9, 3], [1600, 2000, 4607, 1535, 1700, 30]  # rows of each, tokens that they share
+    new = [1 + i % 3 for i in range(sum(groups))]
+    g = torch.Generator().manual_seed(3)
+    most = max(held) // page + 2
+    pages = sum(h // page + 2 * n for n, h in zip(groups, held))
+    k, v = (torch.randn((pages, Hkv, page, D), generator=g).to(DT[dtype]).cuda() for _ in range(2))
+    table, lens, used = torch.full((len(new), most), -1, dtype=torch.int32), [], 0
+    for n, h in zip(groups, held):
+        own = used + h // page
+        for _ in range(n):
+            b = len(lens)
+            lens.append(h + new[b])
+            table[b, : h // page] = torch.arange(used, used + h // page)
+            table[b, h // page: h // page + 2] = torch.arange(own, own + 2)
+            own += 2
+        used = own
+    flat = torch.arange(table.numel(), dtype=torch.int32).view_as(table)
+    at = table.clamp(min=0).flatten().long().cuda()
+    starts, lens = torch.tensor([0] + new).cumsum(0).int().cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    q = torch.randn((sum(new), H, D), generator=g).to(DT[dtype]).cuda()
+    for causal in (True, False):
+        got = binding.paged_attention(q, k, v, starts, lens, table.cuda(), causal)
+        want = binding.paged_attention(q, k[at], v[at], starts, lens, flat.cuda(), causal)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and got[0].isfinite().all()
