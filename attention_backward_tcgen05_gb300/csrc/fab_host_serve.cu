@@ -397,6 +397,9 @@ FAB_API int fab_draft_tree(const int32_t* starts, const int32_t* parents, int64_
   if (T > 0 && !aligned(parents, 4)) return FAB_ERR_INVALID;
   if (words > FAB_DRAFT_MAX_WORDS) return FAB_ERR_UNSUPPORTED;
   if (T == 0) return FAB_OK;
+  // (a sequence's rows of one word take the place of its parents once they have all been read)
+  if (!apart(seen, T * words, starts, B + 1) || (!apart(seen, T * words, parents, T) && (words > 1 || seen != parents)))
+    return FAB_ERR_INVALID;
   return from_cuda(launch_draft_tree(starts, parents, B, T, words, reinterpret_cast<uint32_t*>(seen),
                                      static_cast<cudaStream_t>(stream)));
 }

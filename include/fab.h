@@ -344,7 +344,8 @@ FAB_EXPORT int fab_paged_attention(const void* q, const void* k_cache, const voi
  * ancestors'.  parents [T] (device int32): token i of a sequence follows its token
  * parents[i] < i, or, -1, what the cache held before; anything else is reported
  * as FAB_ERR_INVALID and taken as -1.  starts as above; rows of tokens from
- * starts[B] on are left as they were.  Words past FAB_DRAFT_MAX_WORDS are
+ * starts[B] on are left as they were.  seen may be parents itself where words is 1, and
+ * overlaps neither otherwise.  Words past FAB_DRAFT_MAX_WORDS are
  * FAB_ERR_UNSUPPORTED. */
 FAB_EXPORT int fab_draft_tree(const int32_t* starts, const int32_t* parents, int64_t B, int64_t T, int64_t words,
                               int32_t* seen, fab_stream stream);

@@ -54,6 +54,13 @@ def test_tree_width_and_nothing_to_do():
     assert call_tree(T=0, parents=None, seen=None) == binding.FAB_OK
 
 
+@pytest.mark.parametrize("seen, words", [(A, 1), (A - 48, 1), (A + 8192 - 16, 1), (A + 8192 + 16, 1), (A + 8192 + 64, 1),
+                                         (A + 8192, 2), (A + 8192 - 144, 2), (A + 8192 + 64, 2)])
+def test_tree_refuses_rows_over_what_it_reads(seen, words):
+    # 20 tokens of two sequences; rows of one word may take the place of the parents
+    assert call_tree(starts=A, parents=A + 8192, B=2, T=20, words=words, seen=seen) == binding.FAB_ERR_INVALID
+
+
 @pytest.mark.parametrize("bad", [dict(seen=None), dict(seen=A + 8), dict(words=0), dict(words=-1),
                                  dict(words=1 << 40), dict(q=None)], ids=str)
 def test_append_and_attention_refuse(bad):
@@ -181,6 +188,15 @@ def test_tree_leaves_padding_and_takes_wider_rows(gpu):
     assert (seen[45:] == 99).all() and torch.equal(seen[:45].cpu(), packed(sight(new, parents), 7))
     none = binding.draft_tree(torch.zeros(4, dtype=torch.int32).cuda(), pad[:0], 5)
     assert none.shape == (0, 1)
+
+
+@pytest.mark.gpu
+def test_rows_of_one_word_take_the_parents_place(gpu):
+    new = [i % 33 for i in range(500)]
+    parents = [p for n in new for p in draw_parents(n, random.Random(n), "mixed")]
+    both = torch.tensor(parents, dtype=torch.int32).cuda()
+    binding.fab_draft_tree(starts_of(new).cuda(), both, both.view(-1, 1))
+    assert torch.equal(both.cpu().view(-1, 1), packed(sight(new, parents), 1))
 
 
 @pytest.mark.gpu
