@@ -445,7 +445,13 @@ FAB_API int fab_paged_reserve(int32_t* table, int32_t* refs, const int32_t* sour
       !aligned(lens, 4) || !aligned(spare, 4))
     return FAB_ERR_INVALID;
   if (!widths_ok(dims->DK, dims->DV)) return FAB_ERR_UNSUPPORTED;
-  if (!aligned(workspace, 16) || workspace_bytes < fab_paged_reserve_workspace_bytes(dims)) return FAB_ERR_WORKSPACE;
+  const size_t need = fab_paged_reserve_workspace_bytes(dims);
+  if (!aligned(workspace, 16) || workspace_bytes < need) return FAB_ERR_WORKSPACE;
+  // (written before the last of them is read)
+  if (!apart(spare, 1, table, dims->B * dims->max_pages) || !apart(spare, 1, refs, dims->pages) ||
+      (source && !apart(spare, 1, source, dims->B)) || !apart(spare, 1, kept, dims->B) ||
+      !apart(spare, 1, lens, dims->B) || !apart(spare, 1, workspace, (int64_t)(need / 4)))
+    return FAB_ERR_INVALID;
   CacheProblem p = cache_problem(dims, dtype, k_cache, v_cache);
   p.table = table;
   p.refs = refs;

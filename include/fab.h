@@ -419,9 +419,10 @@ FAB_EXPORT size_t fab_paged_reserve_workspace_bytes(const fab_cache_dims* dims);
  *   - further entries up to lens[b] are fresh pages, those behind are -1, and pages
  *     that no entry names any more are free (lens[b] = 0 frees a row).
  * Fresh pages are the free ones, lowest first, in order of row and entry, those
- * that this call frees among them.  spare [1] gets the number of pages left
- * free, below zero the number that were missing: the last entries in that order
- * are then -1, and what a copy among them should have held is lost.
+ * that this call frees among them.  spare [1], no part of the other arrays, gets the
+ * number of pages left free, below zero the number that were missing: the last
+ * entries in that order are then -1, and what a copy among them should have held is
+ * lost.
  * source, kept, lens: device int32 [B].  kept[b] past what the row source[b] holds,
  * or any of them out of range, are reported as FAB_ERR_INVALID (the rows concerned are
  * meaningless; nothing outside the arguments is touched).  So are references too low

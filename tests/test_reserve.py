@@ -41,6 +41,16 @@ def test_workspace_and_width_refusals():
     assert call_reserve(cache_dims(DK=264, layers=1)) == binding.FAB_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("name", ["table", "refs", "source", "kept", "lens", "ws"])
+def test_spare_over_what_the_call_uses_is_refused(name):
+    at = {n: A + 4096 * i for i, n in enumerate(("table", "refs", "source", "kept", "lens", "ws"))}
+    need = binding.fab_paged_reserve_workspace_bytes(cache_dims())
+    assert need <= 4096
+    last = dict(table=20, refs=28, source=4, kept=4, lens=4, ws=need - 4)[name]  # bytes to the last element
+    for spare in (at[name], at[name] + last):
+        assert call_reserve(cache_dims(), wsb=need, spare=spare, **at) == binding.FAB_ERR_INVALID
+
+
 def test_binding_refuses_what_does_not_fit():
     i32 = lambda *n: torch.zeros(*n, dtype=torch.int32)  # noqa: E731
     k = torch.zeros(5, 2, 16, 64)
