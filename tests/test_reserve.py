@@ -194,6 +194,44 @@ def test_too_few_pages(gpu):
 
 
 @pytest.mark.gpu
+def test_copies_that_get_no_page(gpu):
+    x = Pool(6, 4, 5, 16, 2, 64, 64, "bf16", 2, 7)
+    x.step([0] * 6, [20, 0, 0, 0, 0, 0])
+    assert x.step([20] * 6, [21] * 6, [0] * 6) == -2  # the first row keeps the page, three get copies, two nothing
+    assert x.table[:, 1].tolist() == [1, 2, 3, 4, -1, -1] and x.refs.tolist() == [6, 1, 1, 1, 1]
+    assert x.step([21, 21, 0, 16, 16, 16], [33, 21, 0, 16, 16, 40]) == -1
+
+
+# B, entries of a row, pages, page, Hkv, DK, DV, dtype, layers, gap; steps.  Fewer pages than the rows ask for:
+# in each, several steps run short, and copies of a page get none
+SHORT = {
+    "bf16": ((6, 9, 7, 16, 2, 64, 64, "bf16", 3, 0), 14),
+    "f32_odd": ((7, 9, 7, 5, 1, 7, 3, "f32", 2, 1), 14),
+    "bf16_many_rows": ((1500, 3, 1700, 16, 1, 8, 8, "bf16", 1, 0), 6),
+    "bf16_rows_of_several_shares": ((9000, 2, 9200, 2, 1, 8, 8, "bf16", 1, 0), 5),
+    "bf16_one_page": ((4, 2, 1, 16, 1, 8, 8, "bf16", 2, 0), 14),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", SHORT)
+def test_drawn_steps_with_too_few_pages(gpu, name):
+    (B, W, pages, page, *rest), steps = SHORT[name]
+    x = Pool(B, W, pages, page, *rest[:5], 5, rest[5])
+    r = random.Random(sum(map(ord, name)))
+    held, short = [0] * B, 0  # tokens that each row has pages for
+    for i in range(steps):
+        source = None if i % 3 == 0 else [r.choice([b, r.randrange(B), r.randrange(min(B, 9))]) for b in range(B)]
+        kept = [r.choice([held[s], held[s], r.randint(0, held[s])]) for s in (source or range(B))]
+        lens = [min(W * page, k + r.choice([0, 1, 1, r.randint(0, 2 * page)])) for k in kept]
+        short += x.step(kept, lens, source) < 0
+        held = [min((row + [-1]).index(-1) * page, n) for row, n in zip(x.table.tolist(), lens)]
+    assert short >= 2
+    x.step(held, [0] * B)
+    assert (x.refs == 0).all() and (x.table == -1).all()
+
+
+@pytest.mark.gpu
 def test_a_row_swapped_for_another(gpu):
     x = Pool(4, 5, 40, 8, 1, 16, 16, "f32", 1, 8)
     x.step([0] * 4, [5, 13, 29, 33])
