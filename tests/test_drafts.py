@@ -722,3 +722,103 @@ def test_a_step_without_drafts(gpu):
     for most in (-1, -32, -33):
         with pytest.raises(ValueError):
             binding.draft_tree(starts, parents, most)
+
+
+# ------------------------------------------------------------------ streams, graphs, repeats
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("handle", [False, True], ids=["stream", "handle"])
+def test_a_step_on_another_stream(gpu, dtype, handle):
+    # every call is told the stream, on which what it reads is written milliseconds later
+    x = Batch([30, 45, 3], [130, 300, 3], 4, 2, 64, 64, 16, dtype, seed=5)
+    parents = [p for n in x.new for p in draw_parents(n, random.Random(4), "recent")]
+    last = torch.tensor([29, 44, -1], dtype=torch.int32).cuda()
+    q, k, v = torch.randn(x.T, 8, 64, generator=x.g).to(x.dt).cuda().split([4, 2, 2], 1)
+    cos, sin = (t.cuda() for t in tables(310, 64))
+    given = torch.tensor(parents, dtype=torch.int32).cuda(), x.starts.cuda(), x.lens.cuda(), x.table.cuda()
+    kept = torch.tensor([100, 255, 0], dtype=torch.int32).cuda()
+
+    def step(stream, kc, vc, refs, parents, starts, lens, table):
+        spare = binding.paged_reserve(table, refs, kept, lens, kc, vc, stream=stream)
+        seen = binding.draft_tree(starts, parents, 45, stream=stream)
+        qo = binding.paged_append(q, k, v, None, None, cos, sin, starts, lens, table, kc, vc, stream=stream, seen=seen)
+        o, lse = binding.paged_attention(qo, kc, vc, starts, lens, table, stream=stream, seen=seen)
+        now = binding.paged_accept(starts, lens, table, seen, last, kc, vc, stream=stream)
+        return spare, seen, qo, o, lse, now, kc, vc, table, refs
+
+    def state():
+        refs = torch.bincount(x.table[x.table >= 0].long(), minlength=x.pages).int().cuda()
+        return x.k.nan_to_num(1).cuda(), x.v.nan_to_num(1).cuda(), refs
+
+    want = step(None, *state(), *(t.clone() for t in given))
+    side, late, own = torch.cuda.Stream(), [torch.zeros_like(t) for t in given], state()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        a = torch.randn(6000, 6000, device="cuda")
+        for _ in range(20):
+            a = a @ a * 1e-3
+        for t, g in zip(late, given):
+            t.copy_(g)
+    got = step(side.cuda_stream if handle else side, *own, *late)
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_calls_captured_behind_forks_joins_and_copies(gpu):
+    # each call behind something that is no kernel of the library: a copy, another stream's work, a join
+    x = Batch([30, 45, 3], [130, 300, 3], 4, 2, 64, 64, 16, "bf16", seed=5)
+    parents = [p for n in x.new for p in draw_parents(n, random.Random(4), "recent")]
+    given = (torch.tensor(parents, dtype=torch.int32).cuda(), x.starts.cuda(), x.k.nan_to_num(1).cuda(),
+             x.v.nan_to_num(1).cuda(), torch.randn(1, 300, 8, 64, generator=x.g).to(x.dt).cuda(), x.table.cuda(),
+             torch.bincount(x.table[x.table >= 0].long(), minlength=x.pages).int().cuda())
+    lens, last, kept = x.lens.cuda(), torch.tensor([29, 44, -1]).int().cuda(), torch.tensor([100, 250, 0]).int().cuda()
+    cos, sin = (t.cuda() for t in tables(310, 64))
+    used = [torch.zeros_like(t) for t in given]
+    side = torch.cuda.Stream()
+
+    def step():
+        main, (par, starts, k, v, rows, table, refs) = torch.cuda.current_stream(), used
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            par.copy_(given[0])
+            starts.copy_(given[1])
+            seen = binding.draft_tree(starts, par, 45)
+        for t, g in zip(used[2:], given[2:]):
+            t.copy_(g)
+        outs = binding.qk_norm_rope(rows[:, :, :4], rows[:, :, 4:6], rows[:, :, 6:], None, None, cos, sin)
+        main.wait_stream(side)
+        now = binding.paged_accept(starts, lens, table, seen, last, k, v)
+        moved = k.clone(), v.clone()
+        spare = binding.paged_reserve(table, refs, kept, lens, k, v)
+        return [seen, now, spare, table.clone(), refs.clone(), *moved, *outs]
+
+    want = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(5):
+        for t in (*got, *used):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_the_same_call_gives_the_same_bits(gpu, dtype):
+    x = Batch([64, 8, 33, 1, 200], [4000, 900, 33, 700, 1500], 8, 2, 128, 128, 16, dtype, seed=5)
+    _, seen = drafted(x, 6)
+    q, k, v, starts, lens, table = x.cuda()
+    ws = binding.alloc_paged(q, k, v, table)
+    want = binding.paged_attention(q, k, v, starts, lens, table, seen=seen)
+    for i in range(25):
+        ws.fill_(i * 10 + 1)  # (what it holds before does not matter)
+        o, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+        binding.fab_paged_attention_tree(q, k, v, starts, lens, table, seen, 128 ** -0.5, ws, o, lse)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
