@@ -564,16 +564,16 @@ cudaError_t launch_combine(const PagedPlan& plan, const PagedParts& parts, int g
   const int rows = plan.nt * plan.gw;
   const int per = kCombineThreads / (parts.dp <= 64 ? 16 : 32);  // rows of a block at once
   const int64_t units = paged_most_units(plan);
-  const bool few = units > grid;  // (units of more parts than two are few)
+  const bool pairs = units > grid;  // (most cut units then have two parts)
   // A block costs a place on an SM for 2 us even where its CTA holds no unit's first part.
   // Where units are far fewer than CTAs, blocks are launched for as many as there can be, and look
   // for theirs: one sequence of 131,000 keys and 64 new tokens 104.2 -> 102.2 us, of 500
   // keys and 7 new ones in f32 20.1 -> 18.4; not worth its look for one new token (86.9 ->
   // 87.8), nor for half as many units as CTAs (f32 chunks 21.3 -> 21.9).
-  const int listed = !few && units * 4 <= grid && plan.T > plan.B ? 1 : 0;
+  const int listed = !pairs && units * 4 <= grid && plan.T > plan.B ? 1 : 0;
   const dim3 g((unsigned)(listed ? units : grid - 1), (unsigned)((rows + per - 1) / per));
-  const auto kernel = parts.dp <= 64 ? (few ? paged_combine_kernel<T, 16, 2> : paged_combine_kernel<T, 16, 8>)
-                                     : (few ? paged_combine_kernel<T, 32, 2> : paged_combine_kernel<T, 32, 8>);
+  const auto kernel = parts.dp <= 64 ? (pairs ? paged_combine_kernel<T, 16, 2> : paged_combine_kernel<T, 16, 8>)
+                                     : (pairs ? paged_combine_kernel<T, 32, 2> : paged_combine_kernel<T, 32, 8>);
   return launch_early(kernel, g, kCombineThreads, 0, s, plan, parts, grid - 1, listed, DV, H, o, lse);
 }
 

@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) paged_accept_kernel(c
 // that each need all of the one before, with the cluster's barrier between them.
 // Each CTA has a share of the rows and a share of the pages.  `copy` copies what has
 // to be copied.  Planning is bound by the five steps, each two or three accesses long, and
-// the barriers: 256 rows over a pool of 131,072 pages 18.6 us with the copy's empty
+// the barriers: 256 rows over a pool of 131,072 pages 18.9 us with the copy's empty
 // launch, 16 rows of a small pool 11 (as three kernels, the plan's a single CTA, 87 and more).
 
 struct ReserveCopy {
@@ -788,7 +788,7 @@ constexpr int kCopyThreads = 256;
 
 // Units: (copy, layer, keys or values, head), a warp each.  Bound by HBM: 16 prompts
 // forked into 8 beams, 32 layers of 8 heads of width 128 (411 MB written, 59 MB read
-// once and then from the L2, for which the copies give way: 100 -> 96 us): 89 us, 75
+// once and then from the L2, for which the copies give way: 100 -> 96 us): 90 us, 75
 // of them the copy's, 6.3 TB/s.  Rings of bulk copies in place of the registers took 100 to 109.
 template <typename V>
 __global__ void __launch_bounds__(kCopyThreads) reserve_copy_kernel(const CacheProblem p, const ReserveSpace ws,
